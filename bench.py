@@ -80,9 +80,9 @@ KERNEL_SOURCES = {
     "gemm_sk_kernel": ["bs_gemm.hip", "bs_kernels.h"],
     "sk_reduce_kernel": ["bs_gemm.hip", "bs_kernels.h"],
     "mx_gemm_kernel": ["bs_gemm.hip", "bs_kernels.h"],
-    "quant_": ["bs_quant.hip", "bs_device.h", "bs_kernels.h", "bs_mx.h"],
-    "swiglu_bwd_quant_kernel": ["bs_quant.hip", "bs_device.h", "bs_kernels.h", "bs_mx.h"],
-    "mx_quant_kernel": ["bs_quant.hip", "bs_device.h", "bs_kernels.h", "bs_mx.h"],
+    "quant_": ["bs_quant.hip", "bs_device.h", "bs_kernels.h", "bs_mx.h", "bs_tile.h"],
+    "swiglu_bwd_quant_kernel": ["bs_quant.hip", "bs_device.h", "bs_kernels.h", "bs_mx.h", "bs_tile.h"],
+    "mx_quant_kernel": ["bs_quant.hip", "bs_device.h", "bs_kernels.h", "bs_mx.h", "bs_tile.h"],
     "stream_kernel": ["bs_diag.hip", "bs_kernels.h"],
 }
 
