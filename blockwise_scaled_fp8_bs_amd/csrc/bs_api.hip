@@ -7,16 +7,17 @@
 #include <vector>
 
 #include "../../include/bs.h"
+#include "bs_check.h"
 #include "bs_kernels.h"
 #include "bs_mx.h"
 
 namespace {
 
-// Leading dimensions (elements) stay below 2^22 so that the kernels' lane
-// and in-tile offsets (up to 256 rows of a tile) fit in 32 bits.
-constexpr int64_t kMaxLd = (int64_t)1 << 22;
-
 thread_local std::string g_last_error;
+
+}  // namespace
+
+namespace bs {
 
 bs_status fail(bs_status st, const char* fn, const char* fmt, ...) {
     char buf[512];
@@ -24,7 +25,11 @@ bs_status fail(bs_status st, const char* fn, const char* fmt, ...) {
     va_start(ap, fmt);
     vsnprintf(buf, sizeof buf, fmt, ap);
     va_end(ap);
-    g_last_error = std::string(fn) + ": " + buf;
+    try {  // no exception leaves a C entry point: the status stands without its message
+        g_last_error = std::string(fn) + ": " + buf;
+    } catch (...) {
+        g_last_error.clear();
+    }
     return st;
 }
 
@@ -33,20 +38,7 @@ bs_status ok() {
     return BS_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bs_status hip_status(hipError_t e, const char* fn) {
-    if (e == hipSuccess) return ok();
-    return fail(BS_ERR_HIP, fn, "kernel launch failed: %s", hipGetErrorString(e));
-}
-
-// Leading dimension checks, in elements.
-#define REQUIRE(cond, code, ...)                           \
-    do {                                                   \
-        if (!(cond)) return fail(code, fn, __VA_ARGS__);   \
-    } while (0)
-
-}  // namespace
+}  // namespace bs
 
 namespace bs {
 
@@ -86,6 +78,12 @@ DeviceFit device_fit(const void* kernel, int threads, int default_per_cu) {
 }
 
 }  // namespace bs
+
+using bs::aligned16;
+using bs::fail;
+using bs::hip_status;
+using bs::kMaxLd;
+using bs::ok;
 
 extern "C" {
 
