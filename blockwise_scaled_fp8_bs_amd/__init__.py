@@ -35,6 +35,23 @@ from .binding import (  # noqa: F401
     empty_scales,
     streamk_workspace,
 )
+from .binding_block import (  # noqa: F401,E402
+    BS_SCORE_SIGMOID,
+    BS_SCORE_SOFTMAX,
+    MoEPlan,
+    ResidNormGrads,
+    bs_moe_combine,
+    bs_moe_combine_dw,
+    bs_moe_gather_quant_1x128,
+    bs_moe_plan,
+    bs_moe_plan_rows,
+    bs_moe_route,
+    bs_moe_route_bwd,
+    bs_resid_norm,
+    bs_resid_norm_bwd,
+    bs_swiglu_bwd_quant_1x128_ckpt,
+    bs_swiglu_quant_1x128_ckpt,
+)
 from .linear import Float8BlockwiseLinear, float8_blockwise_linear, swap_linear_layers  # noqa: F401,E402
 from .ffn import Float8BlockwiseGatedFFN, float8_blockwise_gated_ffn  # noqa: F401,E402
 from .mx import Float8MXLinear, float8_mx_linear, mx_grouped_mm  # noqa: F401,E402

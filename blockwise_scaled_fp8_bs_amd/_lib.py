@@ -9,6 +9,7 @@ LIB_PATH = os.path.join(_HERE, "libbs.so")
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _E = ctypes.c_int  # C enums
+_F = ctypes.c_float
 
 # name -> (restype, argtypes); mirrors include/bs.h
 SIGNATURES = {
@@ -38,6 +39,24 @@ SIGNATURES = {
                                   _P]),
     "bs_grouped_scaled_mm": (_E, [_E, _I64, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _I64, _P, _I64,
                                   _I64, _E, _P, _I64, _I64, _E, _P]),
+    "bs_moe_route": (_E, [_P, _E, _I64, _I64, _I64, _P, _E, _I64, _I64, _I64, _I64, _E, _F, _P, _P, _P]),
+    "bs_moe_route_bwd": (_E, [_P, _E, _I64, _I64, _I64, _E, _I64, _E, _F, _P, _P, _P, _P, _I64, _P]),
+    "bs_moe_plan": (_E, [_P, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _I64, _P]),
+    "bs_moe_plan_rows": (_I64, [_I64, _I64, _I64, _I64]),
+    "bs_moe_plan_workspace_bytes": (_I64, [_I64, _I64, _I64]),
+    "bs_moe_gather_quant_1x128": (_E, [_P, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P,
+                                       _I64, _P, _I64, _P]),
+    "bs_moe_combine": (_E, [_P, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _P]),
+    "bs_moe_combine_dw": (_E, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _P]),
+    "bs_resid_norm": (_E, [_P, _P, _I64, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _E, _F, _F, _P, _I64, _P, _P, _P,
+                           _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
+    "bs_resid_norm_bwd": (_E, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _E, _F, _P,
+                               _P, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P]),
+    "bs_resid_norm_bwd_workspace_bytes": (_I64, [_I64, _I64, _I64]),
+    "bs_swiglu_quant_1x128_ckpt": (_E, [_P, _P, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P,
+                                        _I64, _P, _I64, _P]),
+    "bs_swiglu_bwd_quant_1x128_ckpt": (_E, [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P,
+                                            _I64, _P]),
     "bs_status_string": (ctypes.c_char_p, [_E]),
     "bs_last_error": (ctypes.c_char_p, []),
     "bs_diag_e4m3_census": (_E, [_P, _P, _P, _P]),

@@ -32,7 +32,8 @@ CFLAGS = [
     "-I", INCLUDE,
 ]
 
-SOURCES = ["bs_api.hip", "bs_quant.hip", "bs_gemm.hip", "bs_diag.hip"]
+SOURCES = ["bs_api.hip", "bs_quant.hip", "bs_gemm.hip", "bs_diag.hip", "bs_block_api.hip", "bs_route.hip", "bs_moe.hip",
+           "bs_norm.hip", "bs_ckpt.hip"]
 
 
 def _run(cmd):

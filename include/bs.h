@@ -481,6 +481,213 @@ bs_status bs_grouped_scaled_mm(bs_group_mode mode, int64_t G, int64_t M, int64_t
                                void* d, int64_t stride_dg, int64_t ldd, bs_dtype d_dtype,
                                hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Around the experts' products of an MoE block: router, dispatch, combine,
+ * residual norms, and the gated activation with an 8-bit checkpoint.
+ * ------------------------------------------------------------------------ */
+
+/* Scores of a router. */
+typedef enum bs_score_kind {
+    BS_SCORE_SOFTMAX = 0,  /* exp(l_e) / sum over all experts                 */
+    BS_SCORE_SIGMOID = 1   /* 1 / (1 + exp(-l_e))                             */
+} bs_score_kind;
+
+/*
+ * bs_moe_route -- chooses k of E experts for each of T tokens.
+ *   logits  [T, E], dtype BS_OUT_F32 or BS_OUT_BF16, ld_l >= E; any alignment
+ *           of its type (rows that are 16-byte aligned load faster)
+ *   bias    [E] float or NULL: added to the scores for the choice only
+ *   score   s_e of every expert as above
+ *   The choice value of an expert is s_e + bias_e with a bias, and its logit
+ *   without one (scores rise with their logits).  An expert whose logit is
+ *   -inf is masked: it is never chosen.  With n_group > 1 the experts form
+ *   n_group groups of E / n_group consecutive ones; a group's score is the
+ *   sum of the (up to) group_best (1 or 2) largest s_e + bias_e (s_e) of its
+ *   unmasked experts, and only the topk_group best groups stay.  The k
+ *   experts of largest choice value are taken in descending order; ties, of
+ *   groups and of experts, go to the lowest index.
+ *   idx     [T, k] int32, contiguous: the chosen experts, -1 where none is left
+ *   w       [T, k] float, contiguous: scale * s_e; with renormalize
+ *           scale * s_e / sum of the chosen (for the sigmoid / (sum + 1e-20));
+ *           0 where idx is -1.  A token with every logit -inf gets none.
+ * Choices between values that differ are exact: they are made on the logits,
+ * or on float64 scores.  A NaN logit ranks above every number and its weights
+ * (with softmax or renormalize: the token's) are NaN; +inf ranks first too,
+ * and its softmax is NaN as the formula gives.
+ *   1 <= E <= 1024, 1 <= k <= min(E, 32), E % n_group == 0,
+ *   1 <= topk_group <= n_group, scale finite and not 0.
+ */
+bs_status bs_moe_route(const void* logits, bs_dtype dtype, int64_t T, int64_t E, int64_t ld_l, const float* bias,
+                       bs_score_kind score, int64_t k, int64_t n_group, int64_t topk_group, int64_t group_best,
+                       int renormalize, float scale, int32_t* idx, float* w, hipStream_t stream);
+
+/*
+ * bs_moe_route_bwd -- gradient of the logits from the gradient dw [T, k] of
+ * the weights (the choice has none, nor has the bias):
+ *   softmax, renormalized   dl_j = w_j (dw_j - sum_i w_i dw_i / scale)
+ *   softmax                 dl_e = scale p_e (dw_e [e chosen] - sum_i p_i dw_i)
+ *   sigmoid, renormalized   dl_j = scale / (S + 1e-20) (dw_j - sum_i w_i dw_i / scale) s_j (1 - s_j)
+ *   sigmoid                 dl_j = scale dw_j s_j (1 - s_j)
+ * and 0 for all others.  idx and w as bs_moe_route wrote them; dlogits
+ * [T, E] in the type of the logits, ld_d >= E, every entry written.
+ * Entries of idx outside [0, E) are skipped, as are their dw.
+ */
+bs_status bs_moe_route_bwd(const void* logits, bs_dtype dtype, int64_t T, int64_t E, int64_t ld_l,
+                           bs_score_kind score, int64_t k, int renormalize, float scale, const int32_t* idx,
+                           const float* w, const float* dw, void* dlogits, int64_t ld_d, hipStream_t stream);
+
+/*
+ * bs_moe_plan -- sorts the T * k slots (token t, choice j: slot t * k + j) by
+ * expert, in slot order within an expert, into rows of the expert-ordered
+ * matrices that the grouped GEMMs read:
+ *   idx        [T, k] int32, contiguous; values outside [0, E) are not routed
+ *   align      every group's rows are padded to a multiple of align (128 for
+ *              BS_GROUP_K and the quantizers' column output, 1 for none)
+ *   M          rows of the matrices, at least bs_moe_plan_rows(T, k, E, align)
+ *   group_end  [E] int32: cumulative ends of the padded groups, as
+ *              bs_grouped_scaled_mm takes them (the last is <= M: rows past
+ *              it belong to no group)
+ *   counts     [E] int32: slots of each expert, unpadded
+ *   slot_row   [T, k] int32: row of each slot, -1 where not routed
+ *   row_slot   [M] int32: slot of each row, -1 for padding
+ *   workspace  bs_moe_plan_workspace_bytes(T, k, E) bytes of DEVICE memory,
+ *              16-byte aligned (NULL when that is 0)
+ * Everything stays on the device; the result does not depend on any order of
+ * execution.  T * k and M < 2^31, 1 <= E <= 1024, 1 <= k <= 32, align >= 1.
+ */
+bs_status bs_moe_plan(const int32_t* idx, int64_t T, int64_t k, int64_t E, int64_t align, int64_t M,
+                      int32_t* group_end, int32_t* counts, int32_t* slot_row, int32_t* row_slot, void* workspace,
+                      int64_t workspace_bytes, hipStream_t stream);
+
+/* Rows that hold every padded group whatever the routing: T*k slots and the
+ * padding of at most min(E, T*k) groups.  Invalid arguments give 0. */
+int64_t bs_moe_plan_rows(int64_t T, int64_t k, int64_t E, int64_t align);
+
+/* Workspace bytes of bs_moe_plan (0 up to 8192 slots). */
+int64_t bs_moe_plan_workspace_bytes(int64_t T, int64_t k, int64_t E);
+
+/*
+ * bs_moe_gather_quant_1x128 -- the rows of x in expert order, quantized from
+ * the read that gathers them: row r of the [M, D] result v is
+ *   v[r] = x[row_slot[r] / k] (times w[row_slot[r]] when w is set), or zeros
+ * where row_slot[r] is outside [0, T * k) (padding: the codes and scales of
+ * zero blocks).  The product is kept in fp32: it is quantized as it is, and
+ * rounded once to bf16 only for y.  Without w the codes and scales are those
+ * of bs_quant_1x128 on the gathered bf16 rows, bit for bit.
+ *   x         [T, D] bf16, ld_x >= D; row_slot [M] int32; w [T, k] float,
+ *             contiguous, or NULL (forward of the dispatch; with w and the
+ *             gradient of the combine's output as x: its backward)
+ *   y         optional [M, D] bf16 output, ld_y >= D
+ *   q_row/s_row, q_col/s_col   as bs_quant_1x128 writes them for v; at least
+ *             one of y and the two pairs must be set
+ *   D % 128 == 0; M % 128 == 0 when the col output is requested.
+ */
+bs_status bs_moe_gather_quant_1x128(const uint16_t* x, int64_t T, int64_t D, int64_t ld_x, int64_t k,
+                                    const int32_t* row_slot, int64_t M, const float* w, uint16_t* y, int64_t ld_y,
+                                    uint8_t* q_row, int64_t ld_qr, float* s_row, int64_t ld_sr, uint8_t* q_col,
+                                    int64_t ld_qc, float* s_col, int64_t ld_sc, hipStream_t stream);
+
+/*
+ * bs_moe_combine -- the experts' outputs back in token order:
+ *   out[t] = residual[t] + sum_j w[t, j] y[slot_row[t, j]]
+ * in fp32, in the order of the slots, rounded once.  Slots whose row is
+ * outside [0, M) add nothing, whatever their weight.
+ *   y [M, D] bf16, slot_row [T, k] int32, w [T, k] float or NULL (ones: the
+ *   backward of the dispatch), residual [T, D] bf16 or NULL (zeros),
+ *   out [T, D] bf16 (may be the residual itself); D % 8 == 0.
+ */
+bs_status bs_moe_combine(const uint16_t* y, int64_t M, int64_t D, int64_t ld_y, const int32_t* slot_row,
+                         const float* w, int64_t T, int64_t k, const uint16_t* residual, int64_t ld_res,
+                         uint16_t* out, int64_t ld_out, hipStream_t stream);
+
+/*
+ * bs_moe_combine_dw -- dw[t, j] = <dout[t], y[slot_row[t, j]]> in fp32, 0 for
+ * slots whose row is outside [0, M): the gradient of bs_moe_combine's
+ * weights.  (The gradient of y is bs_moe_gather_quant_1x128 of dout with w,
+ * that of the residual is dout.)  dw [T, k] float, contiguous; D % 8 == 0.
+ */
+bs_status bs_moe_combine_dw(const uint16_t* dout, int64_t T, int64_t D, int64_t ld_dout, const uint16_t* y,
+                            int64_t M, int64_t ld_y, const int32_t* slot_row, int64_t k, float* dw,
+                            hipStream_t stream);
+
+/*
+ * bs_resid_norm -- the norm after a block with its gate and scaled residual,
+ * and the norm before the next block:
+ *   r = x + alpha * gate * N(u) * w_post       (u set; N(u) = u / sqrt(mean(u^2) + eps))
+ *   h = N(r) * w_pre                           (w_pre set; r = x without u)
+ * r is the float64 value of its formula rounded once to bf16; h is computed
+ * from that bf16 r in fp32 and is what is quantized, unrounded.
+ *   x, u    [R, D] bf16 (the residual stream, the block's output or NULL)
+ *   w_post  [D] or NULL (u is added without a norm: N(u) w_post becomes u)
+ *   gate    [R / rows_per_gate, D] or NULL (ones), ld_gate >= D: rows
+ *           [i * rows_per_gate, (i + 1) * rows_per_gate) use gate row i;
+ *           R % rows_per_gate == 0
+ *   w_pre   [D] or NULL (no norm of r: no h, codes or rstd_r)
+ *   w_dtype type of w_post, gate and w_pre: BS_OUT_F32 or BS_OUT_BF16
+ *   r       [R, D] bf16, required with u (may be x itself), NULL without
+ *   rstd_u, rstd_r  [R] float, 1 / sqrt(mean + eps) of u and r, for the
+ *           backward; each may be NULL, but the col output needs rstd_r
+ *   h       optional [R, D] bf16
+ *   q_row/s_row, q_col/s_col   codes of h as bs_quant_1x128 lays them out
+ *   At least one of r, h, rstd_r and the pairs must be set.  D % 8 == 0,
+ *   D <= 16384; D % 128 == 0 with codes, R % 128 == 0 with the col output.
+ */
+bs_status bs_resid_norm(const uint16_t* x, const uint16_t* u, int64_t R, int64_t D, int64_t ld_x, int64_t ld_u,
+                        const void* w_post, const void* gate, int64_t ld_gate, int64_t rows_per_gate,
+                        const void* w_pre, bs_dtype w_dtype, float alpha, float eps, uint16_t* r, int64_t ld_r,
+                        float* rstd_u, float* rstd_r, uint16_t* h, int64_t ld_h, uint8_t* q_row, int64_t ld_qr,
+                        float* s_row, int64_t ld_sr, uint8_t* q_col, int64_t ld_qc, float* s_col, int64_t ld_sc,
+                        hipStream_t stream);
+
+/*
+ * bs_resid_norm_bwd -- its backward: from dh (gradient of h) and dr (of r,
+ * from the residual stream; NULL: none) to
+ *   dx      [R, D] bf16   the whole gradient of r, and so of x
+ *   du      [R, D] bf16   (with u)
+ *   dw_pre, dw_post  [D] float, dgate [R / rows_per_gate, D] float,
+ *           contiguous (each with its parameter; NULL: not computed)
+ * Sums over a row and over rows are taken in fp32 or wider, in an order that
+ * depends on the sizes alone.  r is the saved r (x without u); without w_pre
+ * dh must be NULL and dr set.  workspace: bs_resid_norm_bwd_workspace_bytes
+ * (R, D, rows_per_gate) bytes of DEVICE memory, 16-byte aligned.
+ * rows_per_gate = R without a gate.
+ */
+bs_status bs_resid_norm_bwd(const uint16_t* r, const uint16_t* u, const uint16_t* dh, const uint16_t* dr, int64_t R,
+                            int64_t D, int64_t ld_r, int64_t ld_u, int64_t ld_dh, int64_t ld_dr, const void* w_post,
+                            const void* gate, int64_t ld_gate, int64_t rows_per_gate, const void* w_pre,
+                            bs_dtype w_dtype, float alpha, const float* rstd_u, const float* rstd_r, uint16_t* dx,
+                            int64_t ld_dx, uint16_t* du, int64_t ld_du, float* dw_pre, float* dw_post, float* dgate,
+                            void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of bs_resid_norm_bwd (its partial column sums). */
+int64_t bs_resid_norm_bwd_workspace_bytes(int64_t R, int64_t D, int64_t rows_per_gate);
+
+/*
+ * bs_swiglu_quant_1x128_ckpt -- bs_swiglu_quant_1x128 that also keeps its
+ * inputs for the backward pass in 8 bits: the 1x128 row codes and scales of
+ * a and b, exactly as bs_quant_1x128 would write them, from the same read.
+ *   ck      [R, 2C] e4m3: a's codes in columns [0, C), b's in [C, 2C),
+ *           ld_ck >= 2C, a multiple of 16
+ *   s_ck    [2C/128][ld_sck >= R] float, K-major
+ *   a, b, q_row/s_row, q_col/s_col   as bs_swiglu_quant_1x128 (h is made from
+ *           the bf16 a and b, not from their codes); at least one pair set
+ */
+bs_status bs_swiglu_quant_1x128_ckpt(const uint16_t* a, const uint16_t* b, int64_t R, int64_t C, int64_t ld_a,
+                                     int64_t ld_b, uint8_t* ck, int64_t ld_ck, float* s_ck, int64_t ld_sck,
+                                     uint8_t* q_row, int64_t ld_qr, float* s_row, int64_t ld_sr, uint8_t* q_col,
+                                     int64_t ld_qc, float* s_col, int64_t ld_sc, hipStream_t stream);
+
+/*
+ * bs_swiglu_bwd_quant_1x128_ckpt -- bs_swiglu_bwd_quant_1x128 from that
+ * checkpoint: a and b are fl32(code * scale), da and db the float64 values of
+ * their formulas at those, rounded once to bf16 and quantized.
+ *   ck, s_ck as above; dh [R, C] bf16; outputs as bs_swiglu_bwd_quant_1x128.
+ */
+bs_status bs_swiglu_bwd_quant_1x128_ckpt(const uint8_t* ck, int64_t R, int64_t C, int64_t ld_ck, const float* s_ck,
+                                         int64_t ld_sck, const uint16_t* dh, int64_t ld_dh, uint8_t* q_row,
+                                         int64_t ld_qr, float* s_row, int64_t ld_sr, uint8_t* q_col, int64_t ld_qc,
+                                         float* s_col, int64_t ld_sc, hipStream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* bs_status_string(bs_status status);
 

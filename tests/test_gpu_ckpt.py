@@ -1,0 +1,84 @@
+"""GPU gated activation with an 8-bit checkpoint: codes of h and of [a | b]
+bit for bit, and the backward from them bit for bit against the float64
+formula at the kept values."""
+
+import numpy as np
+import pytest
+import torch
+
+import blockwise_scaled_fp8_bs_amd as bs
+from gpu_support import (bits16, check_canaries, check_scale_canaries, f32bits, guarded, need_gpu, scale_buffer, u8)
+from oracle import block, quant, swiglu
+from test_gpu_swiglu import _inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("R,C,cols", [(256, 512, True), (128, 128, True), (384, 640, True), (1, 128, False),
+                                      (200, 256, False)])
+def test_forward_and_backward(R, C, cols):
+    need_gpu()
+    a, b = _inputs(R, C, seed=R + C)
+    dh = torch.randn((R, C), generator=torch.Generator().manual_seed(3)).mul_(0.01).to(torch.bfloat16)
+    ab = torch.cat([a, b], 1).cuda()
+    kf, ck = guarded(R, 2 * C, torch.uint8, pad_cols=32)
+    pf, s_ck = scale_buffer(2 * C // 128, R)
+    qf, q = guarded(R, C, torch.uint8)
+    sf, s = scale_buffer(C // 128, R)
+    out = dict(q_row=q, s_row=s)
+    if cols:
+        cf, c = guarded(C, R, torch.uint8)
+        tf, t = scale_buffer(R // 128, C)
+        out.update(q_col=c, s_col=t)
+    print(f"ckpt forward R={R} C={C}", flush=True)
+    bs.bs_swiglu_quant_1x128_ckpt(ab[:, :C], ab[:, C:], ck, s_ck, **out)
+    torch.cuda.synchronize()
+    hb = swiglu.swiglu(bits16(a), bits16(b))
+    qr, sr = quant.quant_1x128_rowwise(hb)
+    assert np.array_equal(u8(q), qr) and np.array_equal(f32bits(s)[:, :R], sr.T.copy().view(np.uint32))
+    kr, ks = quant.quant_1x128_rowwise(np.concatenate([bits16(a), bits16(b)], 1))
+    assert np.array_equal(u8(ck), kr) and np.array_equal(f32bits(s_ck)[:, :R], ks.T.copy().view(np.uint32))
+    check_canaries(kf, R, 2 * C), check_canaries(qf, R, C)
+    check_scale_canaries(pf, 2 * C // 128, R), check_scale_canaries(sf, C // 128, R)
+    if cols:
+        qc, sc = quant.quant_1x128_colwise(hb)
+        assert np.array_equal(u8(c), qc) and np.array_equal(f32bits(t)[:, :C], sc.T.copy().view(np.uint32))
+        check_canaries(cf, C, R), check_scale_canaries(tf, R // 128, C)
+
+    kept = block.dequant_rows(kr, ks)
+    da = swiglu.round_to_bf16(np.concatenate(block.swiglu_grad(kept[:, :C], kept[:, C:], block.f64(bits16(dh))), 1))
+    qf, q = guarded(R, 2 * C, torch.uint8)
+    sf, s = scale_buffer(2 * C // 128, R)
+    out = dict(q_row=q, s_row=s)
+    if cols:
+        cf, c = guarded(2 * C, R, torch.uint8)
+        tf, t = scale_buffer(R // 128, 2 * C)
+        out.update(q_col=c, s_col=t)
+    print(f"ckpt backward R={R} C={C}", flush=True)
+    bs.bs_swiglu_bwd_quant_1x128_ckpt(ck, s_ck, dh.cuda(), **out)
+    torch.cuda.synchronize()
+    qr, sr = quant.quant_1x128_rowwise(da)
+    assert np.array_equal(f32bits(s)[:, :R], sr.T.copy().view(np.uint32)) and np.array_equal(u8(q), qr)
+    check_canaries(qf, R, 2 * C), check_scale_canaries(sf, 2 * C // 128, R)
+    if cols:
+        qc, sc = quant.quant_1x128_colwise(da)
+        assert np.array_equal(u8(c), qc) and np.array_equal(f32bits(t)[:, :2 * C], sc.T.copy().view(np.uint32))
+        check_canaries(cf, 2 * C, R), check_scale_canaries(tf, R // 128, 2 * C)
+        for only in (("q_row", "s_row"), ("q_col", "s_col")):
+            for n in only:
+                out[n].fill_(0)
+            bs.bs_swiglu_bwd_quant_1x128_ckpt(ck, s_ck, dh.cuda(), **{n: out[n] for n in only})
+            assert np.array_equal(u8(out[only[0]]), qr if only[0] == "q_row" else qc)
+
+
+def test_forward_equals_the_form_without_a_checkpoint():
+    need_gpu()
+    R, C = 512, 384
+    a, b = (t.cuda() for t in _inputs(R, C, seed=11))
+    mk = lambda: dict(q_row=torch.empty((R, C), dtype=torch.uint8, device="cuda"), s_row=bs.empty_scales(C // 128, R, "cuda"),  # noqa: E731
+                      q_col=torch.empty((C, R), dtype=torch.uint8, device="cuda"), s_col=bs.empty_scales(R // 128, C, "cuda"))
+    x, y = mk(), mk()
+    ck, s_ck = torch.empty((R, 2 * C), dtype=torch.uint8, device="cuda"), bs.empty_scales(2 * C // 128, R, "cuda")
+    bs.bs_swiglu_quant_1x128_ckpt(a, b, ck, s_ck, **x)
+    bs.bs_swiglu_quant_1x128(a, b, None, **y)
+    assert all(torch.equal(x[n], y[n]) for n in x)
