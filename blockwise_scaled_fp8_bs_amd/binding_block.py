@@ -13,7 +13,7 @@ from collections import namedtuple
 import torch
 
 from . import _lib
-from .binding import BS_OUT_BF16, BS_OUT_F32, _check, _ld, _mat, _ptr, _require, _scale, _stream
+from .binding import BS_OUT_BF16, BS_OUT_F32, _check, _mat, _require, _scale
 
 BS_SCORE_SOFTMAX = 0
 BS_SCORE_SIGMOID = 1
@@ -27,36 +27,83 @@ MoEPlan = namedtuple("MoEPlan", ["group_end", "counts", "slot_row", "row_slot"])
 ResidNormGrads = namedtuple("ResidNormGrads", ["dx", "du", "dw_pre", "dw_post", "dgate"])
 
 
-def _flat(t, name, dtype, shape):
-    """A contiguous GPU tensor of the given type and shape (None in the shape: any)."""
+# The helpers below return what the C call takes (addresses as integers, row
+# strides) and keep the common case to one comparison of the tensor's type,
+# device, shape and strides: a single token's call costs as much on the host
+# as on the GPU, so a message is only put together once a check has failed.
+
+def _stream_of(t, stream):
+    """Raw stream: the given one, or the current one of t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+def _fail_matrix(t, name, dtype, R, C):
+    _mat(t, name, dtype)
+    raise ValueError(f"{name} must be [{R}, {C}], got {list(t.shape)}")
+
+
+def _matrix(t, name, dtype, R, C):
+    """(address, row stride) of a row-major [R, C] GPU matrix."""
+    if t is None or t.dtype is not dtype or not t.is_cuda or t.shape != (R, C):
+        _fail_matrix(t, name, dtype, R, C)
+    ld, unit = t.stride()
+    if unit != 1 and C > 1:
+        _mat(t, name, dtype)
+    # the stride of an only row says nothing: its length stands for it
+    return t.data_ptr() or None, ld if R > 1 else (C + 15) // 16 * 16
+
+
+def _optional(t, name, dtype, R, C):
+    return (None, 0) if t is None else _matrix(t, name, dtype, R, C)
+
+
+def _first(t, name, dtype):
+    """Shape of the matrix that gives a call its sizes."""
+    if t is None or t.dtype is not dtype or not t.is_cuda or t.dim() != 2:
+        _mat(t, name, dtype)
+    return t.shape
+
+
+def _fail_flat(t, name, dtype, shape):
     _require(t is not None, f"{name} is required")
     _require(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
     _require(t.is_cuda, f"{name} must be a GPU tensor")
-    _require(t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)),
-             f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    _require(t.is_contiguous(), f"{name} must be contiguous; got strides {t.stride()}")
-    return t
+    _require(t.shape == shape, f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous; got strides {t.stride()}")
 
 
-def _bf16(t, name, R, D):
-    _mat(t, name, torch.bfloat16)
-    _require(tuple(t.shape) == (R, D), f"{name} must be [{R}, {D}], got {list(t.shape)}")
-    # the stride of an only row says nothing: its length stands for it
-    return _ld(t) if R > 1 else (D + 7) // 8 * 8
+def _flat(t, name, dtype, shape):
+    """Address of a contiguous GPU tensor of the given shape."""
+    if t is None or t.dtype is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        _fail_flat(t, name, dtype, shape)
+    return t.data_ptr() or None
+
+
+def _index(t, name, dims):
+    """Shape and address of a contiguous int32 GPU tensor."""
+    _require(t is not None, f"{name} is required")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must be {'[T, k]' if dims == 2 else '1-D'}, got {list(t.shape)}")
+    return t.shape, _flat(t, name, torch.int32, t.shape)
+
+
+def _scales(t, name, nkb, count):
+    """(address, row stride) of a K-major scale tensor [nkb, >= count]."""
+    if t is None or t.dtype is not torch.float32 or not t.is_cuda or t.dim() != 2 or t.shape[0] != nkb \
+            or t.shape[1] < count or t.stride(1) != 1:
+        _scale(t, name, nkb, count)
+    return t.data_ptr() or None, t.stride(0)
 
 
 def _codes(R, C, q_row, s_row, q_col, s_col):
     """C arguments of the row and column outputs of an [R, C] matrix."""
-    args = [None, 0, None, 0, None, 0, None, 0]
+    u8 = torch.uint8
+    row = col = (None, 0, None, 0)
     if q_row is not None or s_row is not None:
-        _mat(q_row, "q_row", torch.uint8)
-        _require(tuple(q_row.shape) == (R, C), f"q_row must be [{R}, {C}]")
-        args[0:4] = [_ptr(q_row), _ld(q_row), _ptr(s_row), _scale(s_row, "s_row", C // 128, R)]
+        row = _matrix(q_row, "q_row", u8, R, C) + _scales(s_row, "s_row", C // 128, R)
     if q_col is not None or s_col is not None:
-        _mat(q_col, "q_col", torch.uint8)
-        _require(tuple(q_col.shape) == (C, R), f"q_col must be the transpose [{C}, {R}]")
-        args[4:8] = [_ptr(q_col), _ld(q_col), _ptr(s_col), _scale(s_col, "s_col", R // 128, C)]
-    return args
+        col = _matrix(q_col, "q_col", u8, C, R) + _scales(s_col, "s_col", R // 128, C)
+    return row + col
 
 
 # ----------------------------------------------------------------------------
@@ -64,10 +111,10 @@ def _codes(R, C, q_row, s_row, q_col, s_col):
 # ----------------------------------------------------------------------------
 
 def _logits(t, name):
-    _require(t is not None and t.dtype in _DT, f"{name} must be bfloat16 or float32")
-    _mat(t, name, t.dtype)
-    T, E = t.shape
-    return T, E, _ld(t) if T > 1 else E
+    if t is None or t.dtype not in _DT:
+        raise ValueError(f"{name} must be bfloat16 or float32")
+    T, E = _first(t, name, t.dtype)
+    return (T, E) + _matrix(t, name, t.dtype, T, E)
 
 
 def bs_moe_route(logits, k, bias=None, score=BS_SCORE_SOFTMAX, n_group=1, topk_group=1, group_best=1,
@@ -79,34 +126,33 @@ def bs_moe_route(logits, k, bias=None, score=BS_SCORE_SOFTMAX, n_group=1, topk_g
     with the largest sum of their group_best best scores stay.  idx is -1 and w
     0 where no expert is left to choose.
     """
-    T, E, ld = _logits(logits, "logits")
-    if bias is not None:
-        _flat(bias, "bias", torch.float32, (E,))
-    idx = torch.empty((T, k), dtype=torch.int32, device=logits.device) if idx is None else \
-        _flat(idx, "idx", torch.int32, (T, k))
-    w = torch.empty((T, k), dtype=torch.float32, device=logits.device) if w is None else \
-        _flat(w, "w", torch.float32, (T, k))
-    _check(_lib.load().bs_moe_route(_ptr(logits), _DT[logits.dtype], T, E, ld, _ptr(bias), score, k, n_group,
-                                    topk_group, group_best, int(renormalize), scale, _ptr(idx), _ptr(w),
-                                    _stream(stream)), "bs_moe_route")
+    T, E, p, ld = _logits(logits, "logits")
+    if k < 1:
+        raise ValueError(f"k={k} must be >= 1")
+    if idx is None:
+        idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    if w is None:
+        w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    _check(_lib.load().bs_moe_route(
+        p, _DT[logits.dtype], T, E, ld, None if bias is None else _flat(bias, "bias", torch.float32, (E,)), score, k,
+        n_group, topk_group, group_best, int(renormalize), scale, _flat(idx, "idx", torch.int32, (T, k)),
+        _flat(w, "w", torch.float32, (T, k)), _stream_of(logits, stream)), "bs_moe_route")
     return idx, w
 
 
 def bs_moe_route_bwd(logits, idx, w, dw, score=BS_SCORE_SOFTMAX, renormalize=True, scale=1.0, out=None, stream=None):
     """dlogits [T, E] (the type of logits) from the gradient dw [T, k] of the weights."""
-    T, E, ld = _logits(logits, "logits")
-    _require(idx is not None and idx.dim() == 2, "idx must be [T, k]")
-    k = idx.shape[1]
-    _flat(idx, "idx", torch.int32, (T, k))
-    _flat(w, "w", torch.float32, (T, k))
-    _flat(dw, "dw", torch.float32, (T, k))
+    T, E, p, ld = _logits(logits, "logits")
+    (_, k), p_idx = _index(idx, "idx", 2)
+    shape = (T, k)
     if out is None:
         out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    _mat(out, "out", logits.dtype)
-    _require(tuple(out.shape) == (T, E), f"out must be [{T}, {E}]")
-    _check(_lib.load().bs_moe_route_bwd(_ptr(logits), _DT[logits.dtype], T, E, ld, score, k, int(renormalize), scale,
-                                        _ptr(idx), _ptr(w), _ptr(dw), _ptr(out),
-                                        _ld(out) if T > 1 else E, _stream(stream)), "bs_moe_route_bwd")
+    if idx.shape[0] != T:
+        _fail_flat(idx, "idx", torch.int32, shape)
+    _check(_lib.load().bs_moe_route_bwd(
+        p, _DT[logits.dtype], T, E, ld, score, k, int(renormalize), scale, p_idx,
+        _flat(w, "w", torch.float32, shape), _flat(dw, "dw", torch.float32, shape),
+        *_matrix(out, "out", logits.dtype, T, E), _stream_of(logits, stream)), "bs_moe_route_bwd")
     return out
 
 
@@ -116,7 +162,7 @@ def bs_moe_route_bwd(logits, idx, w, dw, score=BS_SCORE_SOFTMAX, renormalize=Tru
 
 def bs_moe_plan_rows(T, k, E, align=128):
     """Rows that hold every group padded to ``align``, whatever the routing."""
-    return int(_lib.load().bs_moe_plan_rows(T, k, E, align))
+    return _lib.load().bs_moe_plan_rows(T, k, E, align)
 
 
 def bs_moe_plan(idx, E, align=128, M=None, stream=None):
@@ -125,25 +171,22 @@ def bs_moe_plan(idx, E, align=128, M=None, stream=None):
     idx [T, k] int32, values outside [0, E) are not routed.  M: rows of the
     expert-ordered matrices, bs_moe_plan_rows by default.
     """
-    _require(idx is not None and idx.dim() == 2, "idx must be [T, k]")
-    _flat(idx, "idx", torch.int32, (None, None))
-    T, k = idx.shape
+    (T, k), p_idx = _index(idx, "idx", 2)
     lib = _lib.load()
     if M is None:
-        M = int(lib.bs_moe_plan_rows(T, k, E, align))
-    _require(E >= 1 and M >= 0, f"E={E} must be >= 1 and M={M} >= 0")
-    dev, i32 = idx.device, torch.int32
-    # one allocation for the four arrays; each starts 16-byte aligned
-    sizes = [(E + 3) // 4 * 4, (E + 3) // 4 * 4, (T * k + 3) // 4 * 4, M]
-    buf = torch.empty(sum(sizes), dtype=i32, device=dev)
-    ends, counts, slots, rows = torch.split(buf, sizes)
-    plan = MoEPlan(ends[:E], counts[:E], slots[:T * k].view(T, k), rows)
-    nbytes = int(lib.bs_moe_plan_workspace_bytes(T, k, E))
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    _check(lib.bs_moe_plan(_ptr(idx), T, k, E, align, M, _ptr(plan.group_end), _ptr(plan.counts),
-                           _ptr(plan.slot_row), _ptr(plan.row_slot), _ptr(ws), nbytes, _stream(stream)),
+        M = lib.bs_moe_plan_rows(T, k, E, align)
+    if E < 1 or M < 0:
+        raise ValueError(f"E={E} must be >= 1 and M={M} >= 0")
+    # one allocation: the four arrays, each 16-byte aligned, then the workspace
+    e4, n4, m4 = (E + 3) // 4 * 4, (T * k + 3) // 4 * 4, (M + 3) // 4 * 4
+    nbytes = lib.bs_moe_plan_workspace_bytes(T, k, E)
+    buf = torch.empty(2 * e4 + n4 + m4 + nbytes // 4, dtype=torch.int32, device=idx.device)
+    at = buf.data_ptr()
+    _check(lib.bs_moe_plan(p_idx, T, k, E, align, M, at, at + 4 * e4, at + 8 * e4, at + 8 * e4 + 4 * n4,
+                           at + 8 * e4 + 4 * (n4 + m4) if nbytes else None, nbytes, _stream_of(idx, stream)),
            "bs_moe_plan")
-    return plan
+    return MoEPlan(buf[:E], buf[e4:e4 + E], buf.as_strided((T, k), (k, 1), 2 * e4),
+                   buf[2 * e4 + n4:2 * e4 + n4 + M])
 
 
 def bs_moe_gather_quant_1x128(x, row_slot, k, w=None, y=None, q_row=None, s_row=None, q_col=None, s_col=None,
@@ -151,48 +194,43 @@ def bs_moe_gather_quant_1x128(x, row_slot, k, w=None, y=None, q_row=None, s_row=
     """Rows of x [T, D] in expert order, times w [T, k] if given: bf16 rows y
     [M, D] and/or their 1x128 codes along rows and transposed columns, outputs
     as in bs_quant_1x128."""
-    _mat(x, "x", torch.bfloat16)
-    T, D = x.shape
-    ld_x = _bf16(x, "x", T, D)
-    _flat(row_slot, "row_slot", torch.int32, (None,))
-    M = row_slot.shape[0]
-    if w is not None:
-        _flat(w, "w", torch.float32, (T, k))
-    _check(_lib.load().bs_moe_gather_quant_1x128(_ptr(x), T, D, ld_x, k, _ptr(row_slot), M, _ptr(w), _ptr(y),
-                                                 0 if y is None else _bf16(y, "y", M, D),
-                                                 *_codes(M, D, q_row, s_row, q_col, s_col), _stream(stream)),
-           "bs_moe_gather_quant_1x128")
+    bf16 = torch.bfloat16
+    T, D = _first(x, "x", bf16)
+    (M,), p_slot = _index(row_slot, "row_slot", 1)
+    p, ld = _matrix(x, "x", bf16, T, D)
+    _check(_lib.load().bs_moe_gather_quant_1x128(
+        p, T, D, ld, k, p_slot, M, None if w is None else _flat(w, "w", torch.float32, (T, k)),
+        *_optional(y, "y", bf16, M, D), *_codes(M, D, q_row, s_row, q_col, s_col), _stream_of(x, stream)),
+        "bs_moe_gather_quant_1x128")
 
 
 def bs_moe_combine(y, slot_row, w=None, residual=None, out=None, stream=None):
     """out [T, D] = residual + sum over the slots of w [T, k] (ones if None)
     times the rows slot_row [T, k] of y [M, D]; fp32 sum, bf16 out."""
-    _mat(y, "y", torch.bfloat16)
-    M, D = y.shape
-    _flat(slot_row, "slot_row", torch.int32, (None, None))
-    T, k = slot_row.shape
-    if w is not None:
-        _flat(w, "w", torch.float32, (T, k))
+    bf16 = torch.bfloat16
+    M, D = _first(y, "y", bf16)
+    (T, k), p_row = _index(slot_row, "slot_row", 2)
     if out is None:
-        out = torch.empty((T, D), dtype=torch.bfloat16, device=y.device)
-    _check(_lib.load().bs_moe_combine(_ptr(y), M, D, _bf16(y, "y", M, D), _ptr(slot_row), _ptr(w), T, k,
-                                      _ptr(residual), 0 if residual is None else _bf16(residual, "residual", T, D),
-                                      _ptr(out), _bf16(out, "out", T, D), _stream(stream)), "bs_moe_combine")
+        out = torch.empty((T, D), dtype=bf16, device=y.device)
+    p, ld = _matrix(y, "y", bf16, M, D)
+    _check(_lib.load().bs_moe_combine(
+        p, M, D, ld, p_row, None if w is None else _flat(w, "w", torch.float32, (T, k)), T, k,
+        *_optional(residual, "residual", bf16, T, D), *_matrix(out, "out", bf16, T, D), _stream_of(y, stream)),
+        "bs_moe_combine")
     return out
 
 
 def bs_moe_combine_dw(dout, y, slot_row, dw=None, stream=None):
     """dw [T, k] = <dout [T, D] of the token, row slot_row of y [M, D]>, fp32."""
-    _mat(dout, "dout", torch.bfloat16)
-    _mat(y, "y", torch.bfloat16)
-    M, D = y.shape
-    _flat(slot_row, "slot_row", torch.int32, (None, None))
-    T, k = slot_row.shape
+    bf16 = torch.bfloat16
+    M, D = _first(y, "y", bf16)
+    (T, k), p_row = _index(slot_row, "slot_row", 2)
     if dw is None:
         dw = torch.empty((T, k), dtype=torch.float32, device=y.device)
-    _flat(dw, "dw", torch.float32, (T, k))
-    _check(_lib.load().bs_moe_combine_dw(_ptr(dout), T, D, _bf16(dout, "dout", T, D), _ptr(y), M,
-                                         _bf16(y, "y", M, D), _ptr(slot_row), k, _ptr(dw), _stream(stream)),
+    p_dout, ld_dout = _matrix(dout, "dout", bf16, T, D)
+    p, ld = _matrix(y, "y", bf16, M, D)
+    _check(_lib.load().bs_moe_combine_dw(p_dout, T, D, ld_dout, p, M, ld, p_row, k,
+                                         _flat(dw, "dw", torch.float32, (T, k)), _stream_of(y, stream)),
            "bs_moe_combine_dw")
     return dw
 
@@ -202,24 +240,22 @@ def bs_moe_combine_dw(dout, y, slot_row, dw=None, stream=None):
 # ----------------------------------------------------------------------------
 
 def _norm_params(R, D, w_pre, w_post, gate):
-    """Checked (dtype, ld_gate, rows_per_gate) of the parameters."""
-    dt = None
-    for t, name in ((w_pre, "w_pre"), (w_post, "w_post"), (gate, "gate")):
-        if t is None:
-            continue
-        _require(t.dtype in _DT, f"{name} must be bfloat16 or float32, got {t.dtype}")
-        _require(dt is None or dt == t.dtype, "w_pre, w_post and gate must have one type")
-        dt = t.dtype
-        if t is gate:
-            _mat(t, name, dt)
-            _require(t.shape[1] == D, f"gate must be [B, {D}], got {list(t.shape)}")
-        else:
-            _flat(t, name, dt, (D,))
-    if gate is None:
-        return dt, 0, R
-    B = gate.shape[0]
-    _require(B >= 1 and R % B == 0, f"the {R} rows must be a multiple of the gate's {B}")
-    return dt, _ld(gate) if B > 1 else (D + 7) // 8 * 8, R // B
+    """(address of w_pre, of w_post, of gate, ld_gate, rows_per_gate, type)."""
+    some = w_pre if w_pre is not None else w_post if w_post is not None else gate
+    if some is None:
+        return None, None, None, 0, R, BS_OUT_F32
+    dt = some.dtype
+    if dt not in _DT:
+        raise ValueError(f"w_pre, w_post and gate must be bfloat16 or float32, got {dt}")
+    p_gate, ld_gate, per = None, 0, R
+    if gate is not None:
+        B = _first(gate, "gate", dt)[0]
+        p_gate, ld_gate = _matrix(gate, "gate", dt, B, D)
+        if B < 1 or R % B != 0:
+            raise ValueError(f"the {R} rows must be a multiple of the gate's {B}")
+        per = R // B
+    return (None if w_pre is None else _flat(w_pre, "w_pre", dt, (D,)),
+            None if w_post is None else _flat(w_post, "w_post", dt, (D,)), p_gate, ld_gate, per, _DT[dt])
 
 
 def bs_resid_norm(x, w_pre=None, u=None, w_post=None, gate=None, alpha=1.0, eps=1e-6, r=None, h=None, rstd_u=None,
@@ -231,17 +267,16 @@ def bs_resid_norm(x, w_pre=None, u=None, w_post=None, gate=None, alpha=1.0, eps=
     x, u [R, D] bf16; w_pre, w_post [D] and gate [B, D] of one type, bf16 or
     fp32; consecutive R / B rows share a row of the gate.
     """
-    _mat(x, "x", torch.bfloat16)
-    R, D = x.shape
-    dt, ld_gate, per = _norm_params(R, D, w_pre, w_post, gate)
-    for t, name in ((rstd_u, "rstd_u"), (rstd_r, "rstd_r")):
-        if t is not None:
-            _flat(t, name, torch.float32, (R,))
-    ld = lambda t, name: 0 if t is None else _bf16(t, name, R, D)  # noqa: E731
-    _check(_lib.load().bs_resid_norm(_ptr(x), _ptr(u), R, D, ld(x, "x"), ld(u, "u"), _ptr(w_post), _ptr(gate),
-                                     ld_gate, per, _ptr(w_pre), _DT.get(dt, BS_OUT_F32), alpha, eps, _ptr(r),
-                                     ld(r, "r"), _ptr(rstd_u), _ptr(rstd_r), _ptr(h), ld(h, "h"),
-                                     *_codes(R, D, q_row, s_row, q_col, s_col), _stream(stream)), "bs_resid_norm")
+    bf16, f32 = torch.bfloat16, torch.float32
+    R, D = _first(x, "x", bf16)
+    p_pre, p_post, p_gate, ld_gate, per, dt = _norm_params(R, D, w_pre, w_post, gate)
+    p_x, ld_x = _matrix(x, "x", bf16, R, D)
+    p_u, ld_u = _optional(u, "u", bf16, R, D)
+    _check(_lib.load().bs_resid_norm(
+        p_x, p_u, R, D, ld_x, ld_u, p_post, p_gate, ld_gate, per, p_pre, dt, alpha, eps,
+        *_optional(r, "r", bf16, R, D), None if rstd_u is None else _flat(rstd_u, "rstd_u", f32, (R,)),
+        None if rstd_r is None else _flat(rstd_r, "rstd_r", f32, (R,)), *_optional(h, "h", bf16, R, D),
+        *_codes(R, D, q_row, s_row, q_col, s_col), _stream_of(x, stream)), "bs_resid_norm")
 
 
 def bs_resid_norm_bwd(r, rstd_r, w_pre, dh, dr=None, u=None, rstd_u=None, w_post=None, gate=None, alpha=1.0,
@@ -249,63 +284,58 @@ def bs_resid_norm_bwd(r, rstd_r, w_pre, dh, dr=None, u=None, rstd_u=None, w_post
     """ResidNormGrads from dh [R, D] and dr [R, D] (None: zeros): dx, du [R, D]
     bf16, dw_pre, dw_post [D] and dgate [B, D] fp32.  r: the saved r (x without
     u).  Without w_pre (no norm of r) r, rstd_r and dh are None."""
+    bf16, f32 = torch.bfloat16, torch.float32
     some = dr if r is None else r
-    _mat(some, "dr" if r is None else "r", torch.bfloat16)
-    R, D = some.shape
-    dt, ld_gate, per = _norm_params(R, D, w_pre, w_post, gate)
-    dev, f32 = some.device, torch.float32
-    for t, name, need in ((rstd_r, "rstd_r", w_pre), (rstd_u, "rstd_u", w_post)):
-        if need is not None:
-            _flat(t, name, f32, (R,))
-    ld = lambda t, name: 0 if t is None else _bf16(t, name, R, D)  # noqa: E731
-    dx = torch.empty((R, D), dtype=torch.bfloat16, device=dev)
-    du = torch.empty((R, D), dtype=torch.bfloat16, device=dev) if u is not None else None
+    R, D = _first(some, "dr" if r is None else "r", bf16)
+    p_pre, p_post, p_gate, ld_gate, per, dt = _norm_params(R, D, w_pre, w_post, gate)
+    dev = some.device
+    dx = torch.empty((R, D), dtype=bf16, device=dev)
+    du = torch.empty((R, D), dtype=bf16, device=dev) if u is not None else None
     make = torch.empty if R > 0 else torch.zeros     # no rows: the sums are zero
     dw_pre = make(D, dtype=f32, device=dev) if w_pre is not None else None
     dw_post = make(D, dtype=f32, device=dev) if w_post is not None else None
-    dgate = make((R // per if R else gate.shape[0], D), dtype=f32, device=dev) if gate is not None else None
+    dgate = make((gate.shape[0], D), dtype=f32, device=dev) if gate is not None else None
+    grads = ResidNormGrads(dx, du, dw_pre, dw_post, dgate)
     if R == 0:
-        return ResidNormGrads(dx, du, dw_pre, dw_post, dgate)
+        return grads
     lib = _lib.load()
-    nbytes = int(lib.bs_resid_norm_bwd_workspace_bytes(R, D, per))
+    nbytes = lib.bs_resid_norm_bwd_workspace_bytes(R, D, per)
     ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-    _check(lib.bs_resid_norm_bwd(_ptr(r), _ptr(u), _ptr(dh), _ptr(dr), R, D, ld(r, "r"), ld(u, "u"), ld(dh, "dh"),
-                                 ld(dr, "dr"), _ptr(w_post), _ptr(gate), ld_gate, per, _ptr(w_pre),
-                                 _DT.get(dt, BS_OUT_F32), alpha, _ptr(rstd_u), _ptr(rstd_r), _ptr(dx), ld(dx, "dx"),
-                                 _ptr(du), ld(du, "du"), _ptr(dw_pre), _ptr(dw_post), _ptr(dgate), _ptr(ws),
-                                 ws.numel(), _stream(stream)), "bs_resid_norm_bwd")
-    return ResidNormGrads(dx, du, dw_pre, dw_post, dgate)
+    p_r, ld_r = _optional(r, "r", bf16, R, D)
+    p_u, ld_u = _optional(u, "u", bf16, R, D)
+    p_dh, ld_dh = _optional(dh, "dh", bf16, R, D)
+    p_dr, ld_dr = _optional(dr, "dr", bf16, R, D)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _check(lib.bs_resid_norm_bwd(
+        p_r, p_u, p_dh, p_dr, R, D, ld_r, ld_u, ld_dh, ld_dr, p_post, p_gate, ld_gate, per, p_pre, dt, alpha,
+        None if w_post is None else _flat(rstd_u, "rstd_u", f32, (R,)),
+        None if w_pre is None else _flat(rstd_r, "rstd_r", f32, (R,)), dx.data_ptr(), D, ptr(du), D if u is not None else 0,
+        ptr(dw_pre), ptr(dw_post), ptr(dgate), ws.data_ptr(), nbytes, _stream_of(some, stream)), "bs_resid_norm_bwd")
+    return grads
 
 
 # ----------------------------------------------------------------------------
 # gated activation with an 8-bit checkpoint
 # ----------------------------------------------------------------------------
 
-def _ckpt(ck, s_ck, R, C):
-    _mat(ck, "ck", torch.uint8)
-    _require(tuple(ck.shape) == (R, 2 * C), f"ck must be [{R}, {2 * C}]")
-    return _ld(ck) if R > 1 else max(_ld(ck), 2 * C), _scale(s_ck, "s_ck", 2 * C // 128, R)
-
-
 def bs_swiglu_quant_1x128_ckpt(a, b, ck, s_ck, q_row=None, s_row=None, q_col=None, s_col=None, stream=None):
     """bs_swiglu_quant_1x128 that also writes the 1x128 row codes of a and b
     for the backward: ck [R, 2C] uint8 (a then b), s_ck [2C/128, >= R]."""
-    _mat(a, "a", torch.bfloat16)
-    R, C = a.shape
-    ld_ck, ld_sck = _ckpt(ck, s_ck, R, C)
-    _check(_lib.load().bs_swiglu_quant_1x128_ckpt(_ptr(a), _ptr(b), R, C, _bf16(a, "a", R, C), _bf16(b, "b", R, C),
-                                                  _ptr(ck), ld_ck, _ptr(s_ck), ld_sck,
-                                                  *_codes(R, C, q_row, s_row, q_col, s_col), _stream(stream)),
-           "bs_swiglu_quant_1x128_ckpt")
+    bf16 = torch.bfloat16
+    R, C = _first(a, "a", bf16)
+    p_a, ld_a = _matrix(a, "a", bf16, R, C)
+    p_b, ld_b = _matrix(b, "b", bf16, R, C)
+    _check(_lib.load().bs_swiglu_quant_1x128_ckpt(
+        p_a, p_b, R, C, ld_a, ld_b, *_matrix(ck, "ck", torch.uint8, R, 2 * C), *_scales(s_ck, "s_ck", 2 * C // 128, R),
+        *_codes(R, C, q_row, s_row, q_col, s_col), _stream_of(a, stream)), "bs_swiglu_quant_1x128_ckpt")
 
 
 def bs_swiglu_bwd_quant_1x128_ckpt(ck, s_ck, dh, q_row=None, s_row=None, q_col=None, s_col=None, stream=None):
     """bs_swiglu_bwd_quant_1x128 from the checkpoint (ck, s_ck): the codes of
     [da | db] [R, 2C], rows and/or transposed columns."""
-    _mat(dh, "dh", torch.bfloat16)
-    R, C = dh.shape
-    ld_ck, ld_sck = _ckpt(ck, s_ck, R, C)
-    _check(_lib.load().bs_swiglu_bwd_quant_1x128_ckpt(_ptr(ck), R, C, ld_ck, _ptr(s_ck), ld_sck, _ptr(dh),
-                                                      _bf16(dh, "dh", R, C),
-                                                      *_codes(R, 2 * C, q_row, s_row, q_col, s_col), _stream(stream)),
-           "bs_swiglu_bwd_quant_1x128_ckpt")
+    bf16 = torch.bfloat16
+    R, C = _first(dh, "dh", bf16)
+    p_ck, ld_ck = _matrix(ck, "ck", torch.uint8, R, 2 * C)
+    _check(_lib.load().bs_swiglu_bwd_quant_1x128_ckpt(
+        p_ck, R, C, ld_ck, *_scales(s_ck, "s_ck", 2 * C // 128, R), *_matrix(dh, "dh", bf16, R, C),
+        *_codes(R, 2 * C, q_row, s_row, q_col, s_col), _stream_of(dh, stream)), "bs_swiglu_bwd_quant_1x128_ckpt")
