@@ -308,7 +308,7 @@ bs_status bs_resid_norm(const uint16_t* x, const uint16_t* u, int64_t R, int64_t
 
 int64_t bs_resid_norm_bwd_workspace_bytes(int64_t R, int64_t D, int64_t rows_per_gate) {
     if (R < 1 || R > kMaxI32 || D < 1 || D > bs::kMaxNormDim || rows_per_gate < 1 || R % rows_per_gate != 0) return 0;
-    const bs::NormBwdSplit sp = bs::norm_bwd_split(R, rows_per_gate);
+    const bs::NormBwdSplit sp = bs::norm_bwd_split(R, D, rows_per_gate);
     return (2 * sp.blocks + (sp.chunks > 1 ? sp.segs * sp.chunks : 0)) * D * 4;
 }
 

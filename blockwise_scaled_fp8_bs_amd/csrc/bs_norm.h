@@ -55,7 +55,7 @@ struct NormBwdSplit {
     int64_t chunks;          // workgroups per segment
     int64_t rows;            // rows of a chunk
 };
-NormBwdSplit norm_bwd_split(int64_t R, int64_t rows_per_gate);
+NormBwdSplit norm_bwd_split(int64_t R, int64_t D, int64_t rows_per_gate);
 
 struct SwigluCkptArgs {
     const uint16_t *a, *b;

@@ -3,12 +3,18 @@
 // h = r rstd_r w_pre, the norm that the next block reads, quantized 1x128
 // where its products want codes; and their backward pass.
 //
-// A row is held in registers by TP threads (64 or 256), NC chunks of 8 bf16
-// each, between its load and its last use: x, u, dh and dr are read once.
+// Bound by HBM: each tensor of a row is read once and held in registers, in
+// chunks of 8 bf16 a thread, between its load and its last use; a workgroup
+// walks down consecutive rows with the parameters in registers and the next
+// row's loads under way.  At 16384 rows of 5120, fp32 parameters: r and
+// rstd_r from x and u 109 us (503 MB, 4.6 TB/s), h's codes along rows and
+// columns from r 61 us, the backward pass 210 us (1.01 GB, 4.8 TB/s); with
+// the parameters read again for every row it took 430 us.
+//
 // r is the float64 value of its formula rounded once to bf16, so that what
-// the later passes and the oracle compute from r starts from the same bits;
-// squares are summed in float64, which the largest finite bf16 row does not
-// overflow.
+// the later passes and the oracle compute from r starts from the same bits.
+// Sums of squares are exact enough for that in float64 (u) or redone in it
+// where fp32 overflows or vanishes (r): no finite bf16 row does.
 #include "bs_norm.h"
 #include "bs_tile.h"
 
@@ -33,6 +39,14 @@ __device__ __forceinline__ void fill8(float* f, float v) {
     for (int j = 0; j < 8; ++j) f[j] = v;
 }
 
+// f times 8 parameters from column c on.
+__device__ __forceinline__ void mul_w(const void* p, bool bf16, int64_t c, float* f) {
+    float w[8];
+    load_w(p, bf16, c, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= w[j];
+}
+
 __device__ __forceinline__ uint4 pack8(const float* f) {
     return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
 }
@@ -41,112 +55,224 @@ __device__ __forceinline__ const void* gate_row(const void* gate, bool bf16, int
     return reinterpret_cast<const uint8_t*>(gate) + row * (bf16 ? 2 : 4);
 }
 
-// Sum over the TP threads of a row, in a fixed order; all of them get it.
-// lds: 4 doubles per call in flight (TP = 256).
-template <int TP>
-__device__ __forceinline__ double row_sum(double v, double* lds) {
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) v += __shfl_xor(v, s);
-    if constexpr (TP > 64) {
-        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = (lds[0] + lds[1]) + (lds[2] + lds[3]);
-    }
+// 16 bytes of row `row` from column c on; columns past n bytes read 0 (the
+// descriptor ends with the row; that of an absent tensor is empty).
+__device__ __forceinline__ u32x4 load_row(const uint16_t* base, int64_t row, int64_t ld, int64_t n, int c) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc(base + row * ld, n), 2 * c, 0, 0));
+}
+__device__ __forceinline__ void store_row(uint16_t* base, int64_t row, int64_t ld, int64_t n, int c, uint4 v) {
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{v.x, v.y, v.z, v.w}, rsrc(base + row * ld, n), 2 * c, 0, 0);
+}
+__device__ __forceinline__ void unpack8(u32x4 v, float* f) { bs::unpack8(make_uint4(v[0], v[1], v[2], v[3]), f); }
+
+// One DPP step of a sum over a wave.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, ROWS, 0xF, false));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+    return v + __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+
+// Sum over the wave, in its last lane: quads, halves of rows, rows, then row
+// 0 into 1 and 2 into 3, then both into the last.
+template <typename T>
+__device__ __forceinline__ T wave_sum_last(T v) {
+    v = dpp_add<0xB1, 0xF>(v);   // quad_perm 1,0,3,2
+    v = dpp_add<0x4E, 0xF>(v);   // quad_perm 2,3,0,1
+    v = dpp_add<0x141, 0xF>(v);  // row_half_mirror
+    v = dpp_add<0x140, 0xF>(v);  // row_mirror
+    v = dpp_add<0x142, 0xA>(v);  // row_bcast 15
+    v = dpp_add<0x143, 0xC>(v);  // row_bcast 31
     return v;
 }
 
-template <int TP, int NC>
-__global__ __launch_bounds__(256) void resid_norm_kernel(ResidNormArgs a) {
-    __shared__ double s_sum[2][4];
-    const int p = threadIdx.x % TP;
-    const int64_t at = (int64_t)blockIdx.x * (256 / TP) + threadIdx.x / TP;
-    const bool real = at < a.R;
-    const int64_t row = real ? at : a.R - 1;
+// Sum over the workgroup in a fixed order, in every thread.  lds: 16 values,
+// zeroed before the first use (waves that are not there add 0), two of them
+// in turn for sums that follow one another.
+template <int MAXT, typename T>
+__device__ __forceinline__ T block_sum(T v, T* lds) {
+    v = wave_sum_last(v);
+    if ((threadIdx.x & 63) == 63) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    T s = 0;
+#pragma unroll
+    for (int w = 0; w < (MAXT + 192) / 256 * 4; w += 4) s += (lds[w] + lds[w + 1]) + (lds[w + 2] + lds[w + 3]);
+    return s;
+}
 
-    uint4 raw[NC];
+// 1 / sqrt(v) in float64: the hardware's estimate and two Newton steps.
+__device__ __forceinline__ double rsqrt64(double v) {
+    double y = __builtin_amdgcn_rsq(v);
+    const double h = 0.5 * v;
+    y = y * __builtin_fma(-h * y, y, 1.5);
+    return y * __builtin_fma(-h * y, y, 1.5);
+}
+
+// A workgroup has a thread for each NC chunks of 8 columns and walks down
+// `per` rows: the parameters stay in registers, and a row's loads are under
+// way while the one before it is worked on.
+// HOLD: without it (rows of more than 8192 columns, whose chunks would not
+// fit beside them) the parameters and the row are read where they are used.
+template <int NC, int MAXT, bool HOLD>
+__global__ __launch_bounds__(MAXT) void resid_norm_kernel(ResidNormArgs a, int64_t per) {
+    __shared__ double s_sum[2][16];
+    __shared__ float s_sumf[2][16];
+    const int p = threadIdx.x, TP = blockDim.x;
+    const int64_t lo = (int64_t)blockIdx.x * per, hi = lo + per < a.R ? lo + per : a.R;
+    const int64_t bytes = a.D * 2, b_u = a.u != nullptr ? bytes : 0;
+    const bool pre = a.w_pre != nullptr, post = a.w_post != nullptr, has_u = a.u != nullptr;
+    const double inv_d = 1.0 / (double)a.D, eps = (double)a.eps;
+    // with columns to quantize, the tile kernel below makes all codes from r and rstd_r
+    const bool rows = a.q_row != nullptr && a.q_col == nullptr;
+
+    int col[NC];
+    bool in[NC];
+    float wp_held[NC][8];
+    double wg_held[NC][8];  // alpha gate w_post
+    auto load_wp = [&](int i, float* f) {
+        fill8(f, 0.f);
+        if (pre && in[i]) load_w(a.w_pre, a.w_bf16, col[i], f);
+    };
+    auto load_wg = [&](const void* gate, int i, double* f) {
+        float w[8], g[8];
+        fill8(w, 1.f);
+        fill8(g, 1.f);
+        if (in[i] && post) load_w(a.w_post, a.w_bf16, col[i], w);
+        if (in[i] && gate != nullptr) load_w(gate, a.w_bf16, col[i], g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = (double)w[j] * (double)g[j] * (double)a.alpha;
+    };
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        const int64_t c = (int64_t)(p + i * TP) * 8;
-        raw[i] = c < a.D ? *reinterpret_cast<const uint4*>(a.x + row * a.ld_x + c) : make_uint4(0, 0, 0, 0);
+        col[i] = (p + i * TP) * 8;
+        in[i] = col[i] < a.D;
+        if (HOLD) load_wp(i, wp_held[i]);
     }
-    if (a.u != nullptr) {
-        uint4 ru[NC];
-        double ss = 0.0;
+    if (p < 32) (&s_sum[0][0])[p] = 0.0;
+    if (p < 32) (&s_sumf[0][0])[p] = 0.f;
+    __syncthreads();
+
+    u32x4 cur_x[NC], cur_u[NC], next_x[NC], next_u[NC];
+    auto load = [&](int64_t row, u32x4* ox, u32x4* ou) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int64_t c = (int64_t)(p + i * TP) * 8;
-            ru[i] = c < a.D ? *reinterpret_cast<const uint4*>(a.u + row * a.ld_u + c) : make_uint4(0, 0, 0, 0);
+            ox[i] = load_row(a.x, row, a.ld_x, bytes, col[i]);
+            ou[i] = load_row(a.u, row, a.ld_u, b_u, col[i]);
         }
-        double scale = a.alpha;
-        if (a.w_post != nullptr) {
+    };
+    if (HOLD) load(lo, next_x, next_u);
+    int64_t seg_end = lo;  // first row of the next gate segment
+    const void* gate = nullptr;
+    for (int64_t row = lo; row < hi; ++row) {
+        if (HOLD) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                cur_x[i] = next_x[i];
+                cur_u[i] = next_u[i];
+            }
+            if (row + 1 < hi) load(row + 1, next_x, next_u);
+        } else {
+            load(row, cur_x, cur_u);
+        }
+        if (has_u) {
+            if (row == seg_end) {
+                const int64_t seg = row / a.rows_per_gate;
+                seg_end = (seg + 1) * a.rows_per_gate;
+                if (a.gate != nullptr) gate = gate_row(a.gate, a.w_bf16, seg * a.ld_gate);
+                if (HOLD && (row == lo || gate != nullptr)) {
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) load_wg(gate, i, wg_held[i]);
+                }
+            }
+            double rstd = 1.0;
+            if (post) {
+                double ss = 0.0;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    float f[8];
+                    unpack8(cur_u[i], f);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)f[j], (double)f[j], ss);
+                }
+                ss = block_sum<MAXT>(ss, s_sum[0]);
+                rstd = rsqrt64(__builtin_fma(ss, inv_d, eps));
+                if (a.rstd_u != nullptr && p == 0) a.rstd_u[row] = (float)rstd;
+            }
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                float f[8], fu[8];
+                double wg[8], d[8];
+                unpack8(cur_x[i], f);
+                unpack8(cur_u[i], fu);
+                if (!HOLD) load_wg(gate, i, wg);
+                // float64 to fp32 to bf16 is one rounding unless the fp32 value
+                // is a tie between two bf16 ones (one in 2^16): those are redone
+                uint32_t tie = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    d[j] = __builtin_fma(rstd * (HOLD ? wg_held[i][j] : wg[j]), (double)fu[j], (double)f[j]);
+                    f[j] = (float)d[j];
+                    tie |= (__float_as_uint(f[j]) & 0xFFFFu) == 0x8000u ? 1u : 0u;
+                }
+                if (tie) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] = bf16_from_double(d[j]);
+                }
+                const uint4 v = pack8(f);
+                cur_x[i] = u32x4{v.x, v.y, v.z, v.w};
+                store_row(a.r, row, a.ld_r, bytes, col[i], v);
+            }
+        }
+        if (!pre) {
+            if (post) __syncthreads();  // s_sum[0] is written again in the next row
+            continue;
+        }
+        // fp32 squares, in float64 where their sum leaves fp32's range
+        float fs = 0.f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            float f[8];
+            unpack8(cur_x[i], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) fs = __builtin_fmaf(f[j], f[j], fs);
+        }
+        fs = block_sum<MAXT>(fs, s_sumf[post ? 0 : (int)(row & 1)]);
+        double ss = fs;
+        if (!(fs > 1e-25f && fs < 1e38f)) {
+            ss = 0.0;
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 float f[8];
-                unpack8(ru[i], f);
+                unpack8(cur_x[i], f);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)f[j], (double)f[j], ss);
             }
-            ss = row_sum<TP>(ss, s_sum[0]);
-            const double rstd = 1.0 / sqrt(ss / (double)a.D + (double)a.eps);
-            scale *= rstd;
-            if (a.rstd_u != nullptr && p == 0 && real) a.rstd_u[row] = (float)rstd;
+            ss = block_sum<MAXT>(ss, s_sum[1]);
         }
-        const void* const gate =
-            a.gate != nullptr ? gate_row(a.gate, a.w_bf16, row / a.rows_per_gate * a.ld_gate) : nullptr;
+        const float rstd = (float)rsqrt64(__builtin_fma(ss, inv_d, eps));
+        if (a.rstd_r != nullptr && p == 0) a.rstd_r[row] = rstd;
+        if (a.h == nullptr && !rows) continue;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int64_t c = (int64_t)(p + i * TP) * 8;
-            if (c < a.D) {
-                float fx[8], fu[8], w[8], g[8];
-                unpack8(raw[i], fx);
-                unpack8(ru[i], fu);
-                fill8(w, 1.f);
-                fill8(g, 1.f);
-                if (a.w_post != nullptr) load_w(a.w_post, a.w_bf16, c, w);
-                if (gate != nullptr) load_w(gate, a.w_bf16, c, g);
+            float f[8];
+            unpack8(cur_x[i], f);
+            float wp[8];
+            if (!HOLD) load_wp(i, wp);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const double wg = (double)w[j] * (double)g[j];
-                    fx[j] = bf16_from_double(__builtin_fma(scale * wg, (double)fu[j], (double)fx[j]));
-                }
-                raw[i] = pack8(fx);
-                if (real) *reinterpret_cast<uint4*>(a.r + row * a.ld_r + c) = raw[i];
-            }
-        }
-    }
-    if (a.w_pre == nullptr) return;
-    double ss = 0.0;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        float f[8];
-        unpack8(raw[i], f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)f[j], (double)f[j], ss);
-    }
-    ss = row_sum<TP>(ss, s_sum[1]);
-    const float rstd = (float)(1.0 / sqrt(ss / (double)a.D + (double)a.eps));
-    if (!real) return;
-    if (a.rstd_r != nullptr && p == 0) a.rstd_r[row] = rstd;
-    // with columns to quantize, the tile kernel below makes all codes from r and rstd_r
-    const bool rows = a.q_row != nullptr && a.q_col == nullptr;
-    if (a.h == nullptr && !rows) return;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int64_t c = (int64_t)(p + i * TP) * 8;
-        if (c < a.D) {
-            float f[8], w[8];
-            unpack8(raw[i], f);
-            load_w(a.w_pre, a.w_bf16, c, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * w[j];
-            if (a.h != nullptr) *reinterpret_cast<uint4*>(a.h + row * a.ld_h + c) = pack8(f);
-            if (rows) {  // 16 lanes hold a block of 128 columns
+            for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * (HOLD ? wp_held[i][j] : wp[j]);
+            if (a.h != nullptr) store_row(a.h, row, a.ld_h, bytes, col[i], pack8(f));
+            if (rows && in[i]) {  // 16 lanes hold a block of 128 columns
                 float m = 0.f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
                 const Scale sc = block_scale(__uint_as_float(row16_max(__float_as_uint(m))));
-                *reinterpret_cast<uint2*>(a.q_row + row * a.ld_qr + c) = quant8(f, sc);
-                if ((p & 15) == 0) a.s_row[(c / kTile) * a.ld_sr + row] = sc.s;
+                *reinterpret_cast<uint2*>(a.q_row + row * a.ld_qr + col[i]) = quant8(f, sc);
+                if ((p & 15) == 0) a.s_row[(col[i] / kTile) * a.ld_sr + row] = sc.s;
             }
         }
     }
@@ -187,14 +313,24 @@ __global__ __launch_bounds__(kThreads) void norm_quant_kernel(ResidNormArgs a) {
 //   dr' = dr + rstd_r (q - n mean(q n))            (dx; what flows into u's side)
 //   du  = rstd_u (G dr' - m mean(G dr' m))
 // mean(G dr' m) = (sum G m (dr + rstd_r q) - rstd_r mean(q n) sum G m n) / D, so
-// the three sums of a row are taken in one exchange.  Each workgroup keeps the
-// column sums of its rows (dh n, alpha gate dr' m, alpha dr' m w_post) in
-// registers; norm_sum_kernel adds the workgroups' in a fixed order.
-template <int TP, int NC>
-__global__ __launch_bounds__(TP) void resid_norm_bwd_kernel(ResidNormBwdArgs a, NormBwdSplit sp, float* p_pre,
-                                                            float* p_post, float* p_gate) {
-    __shared__ float s_sum[2][3][4];
-    const int p = threadIdx.x;
+// the three sums of a row are taken in one exchange.  A workgroup has a
+// thread for each NC chunks of 8 columns and walks down its rows: the
+// parameters and the column sums (dh n and dr' m, of which the gradients of
+// w_post and of the gate are multiples within a gate's segment) stay in
+// registers, and a row's loads are under way while the one before it is
+// worked on.  norm_sum_kernel adds the workgroups' sums in a fixed order.
+struct NormRow {
+    u32x4 r, u, h, d;
+};
+
+// HOLD: the parameters and the next row stay in registers.  Without it (rows
+// of more than 8192 columns, whose two chunks a thread would not fit beside
+// them) both are read where they are used, and a workgroup has one segment.
+template <int NC, int MAXT, bool HOLD>
+__global__ __launch_bounds__(MAXT) void resid_norm_bwd_kernel(ResidNormBwdArgs a, NormBwdSplit sp, float* p_pre,
+                                                              float* p_post, float* p_gate) {
+    __shared__ __attribute__((aligned(16))) float s_sum[2][3][16];
+    const int p = threadIdx.x, TP = blockDim.x;
     const int64_t b = blockIdx.x;
     const int64_t S = a.rows_per_gate;
     int64_t seg = sp.chunks > 1 ? b / sp.chunks : b * sp.segs_per_block;
@@ -202,138 +338,165 @@ __global__ __launch_bounds__(TP) void resid_norm_bwd_kernel(ResidNormBwdArgs a, 
     int64_t seg_end = sp.chunks > 1 ? seg + 1 : seg + sp.segs_per_block;
     if (seg_end > sp.segs) seg_end = sp.segs;
     const float inv_d = 1.f / (float)a.D;
+    const bool pre = a.w_pre != nullptr, post = a.w_post != nullptr;
 
-    float acc_pre[NC][8], acc_post[NC][8], acc_gate[NC][8];
+    const int64_t bytes = a.D * 2, b_pre = pre ? bytes : 0, b_u = a.u != nullptr ? bytes : 0;
+    const int64_t b_d = a.dr != nullptr ? bytes : 0;
+    bool in[NC];
+    int col[NC];
+    float wp_held[NC][8], acc_pre[NC][8], acc_post[NC][8];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
+        col[i] = (p + i * TP) * 8;
+        in[i] = col[i] < a.D;
         fill8(acc_pre[i], 0.f);
         fill8(acc_post[i], 0.f);
-        fill8(acc_gate[i], 0.f);
+        if (HOLD) {
+            fill8(wp_held[i], 0.f);
+            if (pre && in[i]) load_w(a.w_pre, a.w_bf16, col[i], wp_held[i]);
+        }
     }
+    // w_pre, and alpha gate w_post, of chunk i
+    auto load_wp = [&](int i, float* f) {
+        fill8(f, 0.f);
+        if (pre && in[i]) load_w(a.w_pre, a.w_bf16, col[i], f);
+    };
+    auto load_g = [&](const void* gate, int i, float* f) {
+        fill8(f, a.alpha);
+        if (in[i] && gate != nullptr) mul_w(gate, a.w_bf16, col[i], f);
+        if (in[i] && post) mul_w(a.w_post, a.w_bf16, col[i], f);
+    };
+    for (int i = p; i < 96; i += TP) (&s_sum[0][0][0])[i] = 0.f;  // waves that are not there add 0
+    __syncthreads();
+    auto load = [&](int64_t row, NormRow* o) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            o[i].r = load_row(a.r, row, a.ld_r, b_pre, col[i]);
+            o[i].h = load_row(a.dh, row, a.ld_dh, b_pre, col[i]);
+            o[i].u = load_row(a.u, row, a.ld_u, b_u, col[i]);
+            o[i].d = load_row(a.dr, row, a.ld_dr, b_d, col[i]);
+        }
+    };
     int parity = 0;
     for (; seg < seg_end; ++seg) {
         const void* const gate = a.gate != nullptr ? gate_row(a.gate, a.w_bf16, seg * a.ld_gate) : nullptr;
         const int64_t lo = seg * S + chunk * sp.rows;
         const int64_t hi = sp.chunks > 1 ? (lo + sp.rows < (seg + 1) * S ? lo + sp.rows : (seg + 1) * S) : (seg + 1) * S;
-        for (int64_t row = lo; row < hi; ++row) {
-            uint4 rr[NC], ru[NC], rh[NC], rd[NC];
-            const uint4 zero = make_uint4(0, 0, 0, 0);
+        float g_held[NC][8], acc_m[NC][8];  // alpha gate w_post; sum of dr' m
 #pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                const int64_t c = (int64_t)(p + i * TP) * 8;
-                const bool in = c < a.D;
-                rr[i] = in && a.w_pre != nullptr ? *reinterpret_cast<const uint4*>(a.r + row * a.ld_r + c) : zero;
-                rh[i] = in && a.w_pre != nullptr ? *reinterpret_cast<const uint4*>(a.dh + row * a.ld_dh + c) : zero;
-                ru[i] = in && a.u != nullptr ? *reinterpret_cast<const uint4*>(a.u + row * a.ld_u + c) : zero;
-                rd[i] = in && a.dr != nullptr ? *reinterpret_cast<const uint4*>(a.dr + row * a.ld_dr + c) : zero;
+        for (int i = 0; i < NC; ++i) {
+            fill8(acc_m[i], 0.f);
+            if (HOLD) load_g(gate, i, g_held[i]);
+        }
+        NormRow cur[NC], next[NC];
+        if (HOLD) load(lo, next);
+        for (int64_t row = lo; row < hi; ++row) {
+            if (HOLD) {
+#pragma unroll
+                for (int i = 0; i < NC; ++i) cur[i] = next[i];
+            } else {
+                load(row, cur);
             }
-            const float rstd_r = a.w_pre != nullptr ? a.rstd_r[row] : 0.f;
-            const float rstd_u = a.w_post != nullptr ? a.rstd_u[row] : 1.f;
+            const float rstd_r = pre ? a.rstd_r[row] : 0.f;
+            const float rstd_u = post ? a.rstd_u[row] : 1.f;
+            if (HOLD && row + 1 < hi) load(row + 1, next);
             float s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                const int64_t c = (int64_t)(p + i * TP) * 8;
-                if (c < a.D) {
-                    float n[8], h[8], m[8], d[8], wp[8], wq[8], g[8];
-                    unpack8(rr[i], n);
-                    unpack8(rh[i], h);
-                    unpack8(ru[i], m);
-                    unpack8(rd[i], d);
-                    fill8(wp, 0.f);
-                    fill8(wq, 1.f);
-                    fill8(g, 1.f);
-                    if (a.w_pre != nullptr) load_w(a.w_pre, a.w_bf16, c, wp);
-                    if (a.w_post != nullptr) load_w(a.w_post, a.w_bf16, c, wq);
-                    if (gate != nullptr) load_w(gate, a.w_bf16, c, g);
+                float n[8], h[8], m[8], d[8];
+                unpack8(cur[i].r, n);
+                unpack8(cur[i].h, h);
+                unpack8(cur[i].u, m);
+                unpack8(cur[i].d, d);
+                float wp[8], G[8];
+                if (!HOLD) load_wp(i, wp);
+                if (!HOLD) load_g(gate, i, G);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float nn = n[j] * rstd_r, q = h[j] * wp[j];
-                        s1 = __builtin_fmaf(q, nn, s1);
-                        const float gm = g[j] * wq[j] * (m[j] * rstd_u);
-                        s2 = __builtin_fmaf(gm, __builtin_fmaf(rstd_r, q, d[j]), s2);
-                        s3 = __builtin_fmaf(gm, nn, s3);
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    const float nn = n[j] * rstd_r, q = h[j] * (HOLD ? wp_held[i][j] : wp[j]);
+                    s1 = __builtin_fmaf(q, nn, s1);
+                    const float gm = (HOLD ? g_held[i][j] : G[j]) * (m[j] * rstd_u);
+                    s2 = __builtin_fmaf(gm, __builtin_fmaf(rstd_r, q, d[j]), s2);
+                    s3 = __builtin_fmaf(gm, nn, s3);
                 }
             }
+            s1 = wave_sum_last(s1);
+            s2 = wave_sum_last(s2);
+            s3 = wave_sum_last(s3);
+            float(*const ls)[16] = s_sum[parity];
+            parity ^= 1;
+            if ((p & 63) == 63) {
+                ls[0][p >> 6] = s1;
+                ls[1][p >> 6] = s2;
+                ls[2][p >> 6] = s3;
+            }
+            __syncthreads();
+            float t3[3];
 #pragma unroll
-            for (int s = 1; s < 64; s <<= 1) {
-                s1 += __shfl_xor(s1, s);
-                s2 += __shfl_xor(s2, s);
-                s3 += __shfl_xor(s3, s);
-            }
-            if constexpr (TP > 64) {
-                float(*const ls)[4] = s_sum[parity];
-                parity ^= 1;
-                if ((p & 63) == 0) {
-                    ls[0][p >> 6] = s1;
-                    ls[1][p >> 6] = s2;
-                    ls[2][p >> 6] = s3;
+            for (int k = 0; k < 3; ++k) {
+                t3[k] = 0.f;
+#pragma unroll
+                for (int w = 0; w < (MAXT + 192) / 256 * 4; w += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(&ls[k][w]);
+                    t3[k] += (v.x + v.y) + (v.z + v.w);
                 }
-                __syncthreads();
-                s1 = (ls[0][0] + ls[0][1]) + (ls[0][2] + ls[0][3]);
-                s2 = (ls[1][0] + ls[1][1]) + (ls[1][2] + ls[1][3]);
-                s3 = (ls[2][0] + ls[2][1]) + (ls[2][2] + ls[2][3]);
             }
-            const float c1 = s1 * inv_d;
-            const float c2 = a.w_post != nullptr ? a.alpha * (s2 - rstd_r * c1 * s3) * inv_d : 0.f;
+            const float c1 = t3[0] * inv_d;
+            const float c2 = post ? (t3[1] - rstd_r * c1 * t3[2]) * inv_d : 0.f;
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                const int64_t c = (int64_t)(p + i * TP) * 8;
-                if (c < a.D) {
-                    float n[8], h[8], m[8], d[8], wp[8], wq[8], g[8];
-                    unpack8(rr[i], n);
-                    unpack8(rh[i], h);
-                    unpack8(ru[i], m);
-                    unpack8(rd[i], d);
-                    fill8(wp, 0.f);
-                    fill8(wq, 1.f);
-                    fill8(g, 1.f);
-                    if (a.w_pre != nullptr) load_w(a.w_pre, a.w_bf16, c, wp);
-                    if (a.w_post != nullptr) load_w(a.w_post, a.w_bf16, c, wq);
-                    if (gate != nullptr) load_w(gate, a.w_bf16, c, g);
-                    float du[8];
+                float n[8], h[8], m[8], d[8], du[8];
+                unpack8(cur[i].r, n);
+                unpack8(cur[i].h, h);
+                unpack8(cur[i].u, m);
+                unpack8(cur[i].d, d);
+                float wp[8], G[8];
+                if (!HOLD) load_wp(i, wp);
+                if (!HOLD) load_g(gate, i, G);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float nn = n[j] * rstd_r;
-                        acc_pre[i][j] = __builtin_fmaf(h[j], nn, acc_pre[i][j]);
-                        d[j] += rstd_r * __builtin_fmaf(-nn, c1, h[j] * wp[j]);
-                        const float mm = m[j] * rstd_u, ad = a.alpha * d[j];
-                        acc_post[i][j] = __builtin_fmaf(ad * g[j], mm, acc_post[i][j]);
-                        acc_gate[i][j] = __builtin_fmaf(ad * wq[j], mm, acc_gate[i][j]);
-                        du[j] = rstd_u * __builtin_fmaf(-mm, c2, ad * g[j] * wq[j]);
-                    }
-                    *reinterpret_cast<uint4*>(a.dx + row * a.ld_dx + c) = pack8(d);
-                    if (a.du != nullptr) *reinterpret_cast<uint4*>(a.du + row * a.ld_du + c) = pack8(du);
+                for (int j = 0; j < 8; ++j) {
+                    const float nn = n[j] * rstd_r;
+                    acc_pre[i][j] = __builtin_fmaf(h[j], nn, acc_pre[i][j]);
+                    d[j] += rstd_r * __builtin_fmaf(-nn, c1, h[j] * (HOLD ? wp_held[i][j] : wp[j]));
+                    const float mm = m[j] * rstd_u;
+                    acc_m[i][j] = __builtin_fmaf(d[j], mm, acc_m[i][j]);
+                    du[j] = rstd_u * __builtin_fmaf(-mm, c2, (HOLD ? g_held[i][j] : G[j]) * d[j]);
                 }
+                store_row(a.dx, row, a.ld_dx, bytes, col[i], pack8(d));
+                store_row(a.du, row, a.ld_du, b_u, col[i], pack8(du));
             }
         }
-        if (a.gate != nullptr) {
 #pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                const int64_t c = (int64_t)(p + i * TP) * 8;
-                if (c < a.D) {
-                    float4* o = reinterpret_cast<float4*>(p_gate + (seg * sp.chunks + chunk) * a.D + c);
-                    o[0] = make_float4(acc_gate[i][0], acc_gate[i][1], acc_gate[i][2], acc_gate[i][3]);
-                    o[1] = make_float4(acc_gate[i][4], acc_gate[i][5], acc_gate[i][6], acc_gate[i][7]);
-                }
-                fill8(acc_gate[i], 0.f);
+        for (int i = 0; i < NC; ++i) {
+            if (!in[i]) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc_m[i][j] *= a.alpha;
+            if (p_gate != nullptr) {
+                float g[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[j] = acc_m[i][j];
+                if (post) mul_w(a.w_post, a.w_bf16, col[i], g);
+                float4* o = reinterpret_cast<float4*>(p_gate + (seg * sp.chunks + chunk) * a.D + col[i]);
+                o[0] = make_float4(g[0], g[1], g[2], g[3]);
+                o[1] = make_float4(g[4], g[5], g[6], g[7]);
             }
+            if (gate != nullptr) mul_w(gate, a.w_bf16, col[i], acc_m[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc_post[i][j] = HOLD ? acc_post[i][j] + acc_m[i][j] : acc_m[i][j];
         }
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        const int64_t c = (int64_t)(p + i * TP) * 8;
-        if (c < a.D) {
-            if (p_pre != nullptr) {
-                float4* o = reinterpret_cast<float4*>(p_pre + b * a.D + c);
-                o[0] = make_float4(acc_pre[i][0], acc_pre[i][1], acc_pre[i][2], acc_pre[i][3]);
-                o[1] = make_float4(acc_pre[i][4], acc_pre[i][5], acc_pre[i][6], acc_pre[i][7]);
-            }
-            if (p_post != nullptr) {
-                float4* o = reinterpret_cast<float4*>(p_post + b * a.D + c);
-                o[0] = make_float4(acc_post[i][0], acc_post[i][1], acc_post[i][2], acc_post[i][3]);
-                o[1] = make_float4(acc_post[i][4], acc_post[i][5], acc_post[i][6], acc_post[i][7]);
-            }
+        if (!in[i]) continue;
+        if (p_pre != nullptr) {
+            float4* o = reinterpret_cast<float4*>(p_pre + b * a.D + col[i]);
+            o[0] = make_float4(acc_pre[i][0], acc_pre[i][1], acc_pre[i][2], acc_pre[i][3]);
+            o[1] = make_float4(acc_pre[i][4], acc_pre[i][5], acc_pre[i][6], acc_pre[i][7]);
+        }
+        if (p_post != nullptr) {
+            float4* o = reinterpret_cast<float4*>(p_post + b * a.D + col[i]);
+            o[0] = make_float4(acc_post[i][0], acc_post[i][1], acc_post[i][2], acc_post[i][3]);
+            o[1] = make_float4(acc_post[i][4], acc_post[i][5], acc_post[i][6], acc_post[i][7]);
         }
     }
 }
@@ -370,35 +533,40 @@ __global__ __launch_bounds__(256) void norm_sum_kernel(const float* p_pre, float
     }
 }
 
-template <int TP, int NC>
-void norm_fwd(const ResidNormArgs& a, hipStream_t stream) {
-    constexpr int RPB = 256 / TP;
-    hipLaunchKernelGGL((resid_norm_kernel<TP, NC>), dim3((unsigned)((a.R + RPB - 1) / RPB)), dim3(256), 0, stream, a);
+// Threads of a workgroup: the chunks of a row over NC, in whole waves.
+template <int NC>
+unsigned norm_threads(int64_t D) {
+    return (unsigned)((D / 8 + 64 * NC - 1) / (64 * NC) * 64);
 }
 
-template <int TP, int NC>
+template <int NC, int MAXT>
+void norm_fwd(const ResidNormArgs& a, hipStream_t stream) {
+    const unsigned threads = norm_threads<NC>(a.D);
+    // enough workgroups for 32 waves of one chunk on each of 256 CUs, so that a
+    // CU has several to change between and each still walks down many rows
+    const int64_t waves = NC * threads / 64, blocks = 256 * (waves < 32 ? 32 / waves : 1);
+    constexpr bool kHold = NC * MAXT <= 1024;
+    const int64_t per = kHold ? (a.R + blocks - 1) / blocks : 1;
+    hipLaunchKernelGGL((resid_norm_kernel<NC, MAXT, kHold>), dim3((unsigned)((a.R + per - 1) / per)),
+                       dim3(threads), 0, stream, a, per);
+}
+
+template <int NC, int MAXT>
 void norm_bwd(const ResidNormBwdArgs& a, const NormBwdSplit& sp, float* pp, float* pq, float* pg, hipStream_t stream) {
-    hipLaunchKernelGGL((resid_norm_bwd_kernel<TP, NC>), dim3((unsigned)sp.blocks), dim3(TP), 0, stream, a, sp, pp, pq,
-                       pg);
+    hipLaunchKernelGGL((resid_norm_bwd_kernel<NC, MAXT, NC == 1>), dim3((unsigned)sp.blocks),
+                       dim3(norm_threads<NC>(a.D)), 0, stream, a, sp, pp, pq, pg);
 }
 
 }  // namespace
 
-// Threads and chunks by the row's length: a wave alone (no barrier) up to
-// 1024 columns, 256 threads beyond, the fewest chunks that hold the row.
-#define BS_NORM_BY_D(CALL)                      \
-    if (a.D <= 512) { CALL(64, 1); }            \
-    else if (a.D <= 1024) { CALL(64, 2); }      \
-    else if (a.D <= 2048) { CALL(256, 1); }     \
-    else if (a.D <= 4096) { CALL(256, 2); }     \
-    else if (a.D <= 6144) { CALL(256, 3); }     \
-    else if (a.D <= 8192) { CALL(256, 4); }     \
-    else { CALL(256, 8); }
-
 hipError_t launch_resid_norm(const ResidNormArgs& a, hipStream_t stream) {
-#define BS_CALL(TP, NC) norm_fwd<TP, NC>(a, stream)
-    BS_NORM_BY_D(BS_CALL)
-#undef BS_CALL
+    // D = 5120 at 16384 rows, r alone: 109 us in three chunks, 118 in one, 129 in two (640 threads
+    // are ten waves on four SIMDs, and a second workgroup of them does not fit beside the first)
+    if (a.D <= 2048) norm_fwd<1, 256>(a, stream);
+    else if (a.D <= 4096) norm_fwd<1, 512>(a, stream);
+    else if (a.D <= 6144) norm_fwd<3, 256>(a, stream);
+    else if (a.D <= 8192) norm_fwd<1, 1024>(a, stream);
+    else norm_fwd<2, 1024>(a, stream);
     if (a.q_col != nullptr) {
         const dim3 grid((unsigned)((a.R / kTile) * (a.D / kTile))), block(kThreads);
         if (a.q_row != nullptr) hipLaunchKernelGGL(norm_quant_kernel<true>, grid, block, 0, stream, a);
@@ -407,10 +575,12 @@ hipError_t launch_resid_norm(const ResidNormArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-NormBwdSplit norm_bwd_split(int64_t R, int64_t rows_per_gate) {
-    // about 1024 workgroups, four for each CU, so that the rows of one hide
-    // another's loads; a chunk never crosses a gate's segment
-    const int64_t S = rows_per_gate, want = (R + 1023) / 1024;
+NormBwdSplit norm_bwd_split(int64_t R, int64_t D, int64_t rows_per_gate) {
+    // workgroups for 8 waves on each of 256 CUs (at 16384 rows of 1024 columns:
+    // 48 us, 62 with 2 waves; of 4096: 165 us, 175 with 16; more of them write
+    // more partial sums); a chunk never crosses a gate's segment
+    const int64_t waves = (D + 511) / 512, blocks = 256 * (waves < 8 ? 8 / waves : 1);
+    const int64_t S = rows_per_gate, want = (R + blocks - 1) / blocks;
     NormBwdSplit sp{};
     sp.segs = R / S;
     if (S > want) {
@@ -420,7 +590,7 @@ NormBwdSplit norm_bwd_split(int64_t R, int64_t rows_per_gate) {
         sp.chunks = (S + sp.rows - 1) / sp.rows;
         sp.blocks = sp.segs * sp.chunks;
     } else {
-        sp.segs_per_block = want / S > 0 ? want / S : 1;
+        sp.segs_per_block = want / S > 0 && D <= 8192 ? want / S : 1;
         sp.chunks = 1;
         sp.rows = S;
         sp.blocks = (sp.segs + sp.segs_per_block - 1) / sp.segs_per_block;
@@ -429,7 +599,7 @@ NormBwdSplit norm_bwd_split(int64_t R, int64_t rows_per_gate) {
 }
 
 hipError_t launch_resid_norm_bwd(const ResidNormBwdArgs& a, hipStream_t stream) {
-    const NormBwdSplit sp = norm_bwd_split(a.R, a.rows_per_gate);
+    const NormBwdSplit sp = norm_bwd_split(a.R, a.D, a.rows_per_gate);
     float* at = a.ws;
     float *pp = nullptr, *pq = nullptr, *pg = nullptr;
     if (a.dw_pre != nullptr) { pp = at; at += sp.blocks * a.D; }
@@ -437,9 +607,12 @@ hipError_t launch_resid_norm_bwd(const ResidNormBwdArgs& a, hipStream_t stream) 
     if (a.dgate != nullptr) {
         pg = sp.chunks > 1 ? at : a.dgate;  // whole segments need no second pass
     }
-#define BS_CALL(TP, NC) norm_bwd<TP, NC>(a, sp, pp, pq, pg, stream)
-    BS_NORM_BY_D(BS_CALL)
-#undef BS_CALL
+    // the bound on the threads sets how many registers one may take
+    if (a.D <= 2048) norm_bwd<1, 256>(a, sp, pp, pq, pg, stream);
+    else if (a.D <= 4096) norm_bwd<1, 512>(a, sp, pp, pq, pg, stream);
+    else if (a.D <= 6144) norm_bwd<1, 768>(a, sp, pp, pq, pg, stream);
+    else if (a.D <= 8192) norm_bwd<1, 1024>(a, sp, pp, pq, pg, stream);
+    else norm_bwd<2, 1024>(a, sp, pp, pq, pg, stream);
     const int64_t kinds = a.dgate != nullptr && sp.chunks > 1 ? 2 + sp.segs : 2;
     hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((a.D + 31) / 32), (unsigned)kinds), dim3(256), 0, stream, pp,
                        a.dw_pre, pq, a.dw_post, pg, a.dgate, a.D, sp.blocks, sp.chunks);
