@@ -8,12 +8,146 @@
 // and keep their arithmetic: fp32, with the float64 formula where the fp32
 // result lies near a bf16 rounding tie, so h, da and db are the float64
 // values of their formulas rounded once.
+//
+// At 16384 x 8192 the forward takes 225 us in a step (1.10 GB, 4.9 TB/s: HBM;
+// its vector instructions would take 183), the backward 295 (3.7 TB/s; 314
+// with a wave less on each SIMD): 72 vector instructions an element, 255 us
+// at 2.2 GHz, of them 26 the two quantizations of da and of db, about 20 the
+// gradient and 12 the proof that its rounding is certain.
 #include "bs_norm.h"
 #include "bs_tile.h"
 
 namespace bs {
 
 namespace {
+
+// ---- elements that the fp32 path leaves undecided ----
+// A thread notes them in a 64-bit mask over its 8x8 block.  Their float64
+// values are computed for one element of every lane at a time; putting them
+// in place is a lane after another, so that the word's index is uniform: the
+// block stays in registers, where a uniform index is an indexed move, and an
+// element costs a few instructions.  (A blend of all 32 words by a per-lane
+// index costs 128.)
+typedef uint32_t Packed __attribute__((ext_vector_type(32)));  // word 4 i + j / 2: row i, columns j, j + 1 (bf16)
+
+// Makes the mask a value at this point: left alone, the compiler keeps the 64
+// comparisons' lane masks until the end instead.
+__device__ __forceinline__ void pin(uint32_t& m) { asm volatile("" : "+v"(m)); }
+
+__device__ __forceinline__ void pack_row(Packed& p, int i, const float* f) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[4 * i + j] = pack_bf16(f[2 * j], f[2 * j + 1]);
+}
+__device__ __forceinline__ void unpack_packed(const Packed& p, TileRegs& t) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) unpack8(make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]), t.f[i]);
+}
+
+// Takes an element off a mask that is not empty.
+__device__ __forceinline__ int next_marked(uint32_t& m0, uint32_t& m1) {
+    const bool first = m0 != 0;
+    const int bit = __builtin_clz(first ? m0 : m1);
+    (first ? m0 : m1) &= ~(0x80000000u >> bit);
+    return (first ? 0 : 32) + bit;
+}
+
+// value(e) gives element e's bf16 value (as a float).
+template <typename F>
+__device__ __forceinline__ void redo_marked(uint32_t m0, uint32_t m1, Packed& block, F&& value) {
+    while (uint64_t lanes = __ballot((m0 | m1) != 0)) {
+        int e = 0;
+        float v = 0.f;
+        if ((m0 | m1) != 0) {
+            e = next_marked(m0, m1);
+            v = value(e);
+        }
+        const uint32_t h = __float_as_uint(v) >> 16, put = h | (h << 16);
+        const int lane = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+        while (lanes != 0) {
+            const int from = __builtin_ctzll(lanes);
+            lanes &= lanes - 1;
+            const int w = __builtin_amdgcn_readlane(e, from) >> 1;
+            const uint32_t mask32 = lane == from ? ((e & 1) ? 0xFFFF0000u : 0xFFFFu) : 0u;
+            block[w] = (put & mask32) | (block[w] & ~mask32);
+        }
+    }
+}
+
+// Two blocks at once (da and db, whose indexed forms would not fit beside one
+// another): element e of each by blends, the masks of a row's four words
+// shared by the rows and by both blocks.
+__device__ __forceinline__ uint32_t blend(uint32_t mask, uint32_t put, uint32_t word) {
+    return (put & mask) | (word & ~mask);
+}
+__device__ __forceinline__ void set_pair(Raw& x, Raw& y, int e, float vx, float vy) {
+    const uint32_t hx = __float_as_uint(vx) >> 16, hy = __float_as_uint(vy) >> 16;
+    const uint32_t px = hx | (hx << 16), py = hy | (hy << 16);
+    const uint32_t field = (e & 1) ? 0xFFFF0000u : 0xFFFFu, w = ((uint32_t)e >> 1) & 3u, row = (uint32_t)e >> 3;
+    const uint32_t k0 = w == 0 ? field : 0u, k1 = w == 1 ? field : 0u, k2 = w == 2 ? field : 0u, k3 = w == 3 ? field : 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const bool at = row == (uint32_t)i;
+        const uint32_t m0 = at ? k0 : 0u, m1 = at ? k1 : 0u, m2 = at ? k2 : 0u, m3 = at ? k3 : 0u;
+        x.v[i] = make_uint4(blend(m0, px, x.v[i].x), blend(m1, px, x.v[i].y), blend(m2, px, x.v[i].z), blend(m3, px, x.v[i].w));
+        y.v[i] = make_uint4(blend(m0, py, y.v[i].x), blend(m1, py, y.v[i].y), blend(m2, py, y.v[i].z), blend(m3, py, y.v[i].w));
+    }
+}
+
+// Windows, in fp32 ulps around a bf16 rounding tie, inside which a value is
+// redone.  With u = 2^-24: exp_neg errs by 3.2 u (the hardware exponential's
+// 2 u and an fma), s = rcp(1 + e) by 3.2 + 1 + 2 u, e s by 7.2 u, products by
+// 1 u more each, so da by 10.2 u + 7.2 u |a (1 - s)| / |t|, db and h by 8.2 u;
+// k u of a value is less than k of its ulps.
+constexpr float kWindowDa = 11.0f, kWindowDaT = 8.0f;
+constexpr uint32_t kWindow1 = 9;
+// An h or db that overflows fp32 is over bf16's largest value too, by more than
+// those errors, and is the infinity that the float64 value rounds to.
+constexpr float kSafe = 7.9e-31f;  // 2^-100
+
+// |low half-word of r - 0x8000| > kWindow1
+__device__ __forceinline__ bool off_tie1(float r) {
+    return (uint16_t)(__float_as_uint(r) - (0x8000u - kWindow1)) > 2 * kWindow1;
+}
+
+// h = silu(a) b in fp32 and whether its bf16 rounding is certain: as
+// swiglu_fast, with the window above.
+__device__ __forceinline__ float gate_h(float a, float b, bool& ok) {
+    const float silu = a * __builtin_amdgcn_rcpf(1.0f + exp_neg(a));
+    const float r = silu * b;
+    ok = (a > -69.0f) & ((silu == 0.0f) | (fabsf(silu) >= kMinNormal)) & off_tie1(r);
+    return r;
+}
+
+// da and db in fp32 and whether both roundings are certain.  |da| >= 2^-100
+// leaves no factor of it below the normal range (|t| < 1.1, s < 1), so one
+// comparison stands for theirs; a checkpointed a is 0 or over 2^-9 1e-12 / 448,
+// so silu(a) is 0 or normal.
+__device__ __forceinline__ void gate_grad(float a, float b, float dh, float& da, float& db, bool& ok) {
+    const float e = exp_neg(a);
+    const float s = __builtin_amdgcn_rcpf(1.0f + e);
+    const float an = a * (e * s);  // a (1 - s)
+    const float t = 1.0f + an;
+    const float p1 = dh * b;
+    da = p1 * s * t;
+    const float silu = a * s;
+    db = dh * silu;
+    const float mag = fabsf(da);
+    ok = (a > -69.0f) & ((p1 == 0.0f) | ((mag >= kSafe) & (mag < __builtin_inff()))) &
+         ((tie_distance(da) - kWindowDa) * fabsf(t) > kWindowDaT * fabsf(an)) & off_tie1(db);
+}
+
+// 1x128 codes of row i of a thread's block (columns 8 tc .. +7 of the tile)
+// to q, its scale where this lane is to store it (see quant_tile_rows).
+__device__ __forceinline__ void quant_row(const float* f, int i, __amdgpu_buffer_rsrc_t rq, int voff, int ld, int tc,
+                                          float& my_scale) {
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+    const Scale sc = block_scale(__uint_as_float(row16_max(__float_as_uint(m))));
+    const uint2 qv = quant8(f, sc);
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{qv.x, qv.y}, rq, voff, i * ld, 0);
+    if ((tc & 7) == i) my_scale = sc.s;
+}
 
 template <bool ROW, bool COL>
 __global__ __launch_bounds__(kThreads) void swiglu_ckpt_kernel(SwigluCkptArgs a) {
@@ -24,33 +158,47 @@ __global__ __launch_bounds__(kThreads) void swiglu_ckpt_kernel(SwigluCkptArgs a)
     const int64_t col_tiles = a.C / kTile;
     const int64_t r0 = (blockIdx.x / col_tiles) * kTile, c0 = (blockIdx.x % col_tiles) * kTile;
     const int64_t rows = (a.R - r0) < kTile ? (a.R - r0) : kTile;
-    Raw ra, rb, ph;
+    Raw ra, rb;
+    Packed ph;
     load_raw(a.a, a.ld_a, r0, c0, a.R, (8 * tr) * (int)(a.ld_a * 2) + 16 * tc, ra);
     load_raw(a.b, a.ld_b, r0, c0, a.R, (8 * tr) * (int)(a.ld_b * 2) + 16 * tc, rb);
+    const __amdgpu_buffer_rsrc_t ka = rsrc(a.ck + r0 * a.ld_ck + c0, rows * a.ld_ck);
+    const __amdgpu_buffer_rsrc_t kb = rsrc(a.ck + r0 * a.ld_ck + a.C + c0, rows * a.ld_ck);
+    const int voff_k = (8 * tr) * (int)a.ld_ck + 8 * tc;
+    float sa = 0.f, sb = 0.f;
+    uint32_t m[2] = {0u, 0u};
+    // row by row: the checkpoint's codes of a and b, and h
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float fa[8], fb[8], g[8];
         unpack8(ra.v[i], fa);
         unpack8(rb.v[i], fb);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = swiglu_fast(fa[j], fb[j]);
-        ph.v[i] = make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]),
-                             pack_bf16(g[6], g[7]));
+        for (int j = 0; j < 8; ++j) {
+            bool ok;
+            g[j] = gate_h(fa[j], fb[j], ok);
+            m[i >> 2] = m[i >> 2] + m[i >> 2] + (ok ? 0u : 1u);  // one add with carry; element 0 ends in bit 31
+        }
+        pin(m[i >> 2]);
+        quant_row(fa, i, ka, voff_k, (int)a.ld_ck, tc, sa);
+        quant_row(fb, i, kb, voff_k, (int)a.ld_ck, tc, sb);
+        pack_row(ph, i, g);
+        __builtin_amdgcn_sched_barrier(0);
     }
-    TileRegs tl;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int64_t co = (half ? a.C : 0) + c0;
-        unpack_tile(half ? rb : ra, tl);
-        quant_tile_rows(tl, rows, a.ck + r0 * a.ld_ck + co, a.ld_ck, a.s_ck + (co / kTile) * a.ld_sck + r0, tr, tc);
+    if (tc < 8) {  // lanes tc < 8 hold the scales of rows 8 tr + tc
+        const __amdgpu_buffer_rsrc_t za = rsrc(a.s_ck + (c0 / kTile) * a.ld_sck + r0, rows * 4);
+        const __amdgpu_buffer_rsrc_t zb = rsrc(a.s_ck + ((a.C + c0) / kTile) * a.ld_sck + r0, rows * 4);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sa), za, (8 * tr + tc) * 4, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sb), zb, (8 * tr + tc) * 4, 0, 0);
     }
-    fixup_block(ph, [&](int e) {
+    redo_marked(m[0], m[1], ph, [&](int e) {
         const int64_t r = r0 + 8 * tr + (e >> 3), c = c0 + 8 * tc + (e & 7);
-        if (r >= a.R) return;
-        raw_set(ph, e, swiglu_bf16_f64(__uint_as_float((uint32_t)a.a[r * a.ld_a + c] << 16),
-                                       __uint_as_float((uint32_t)a.b[r * a.ld_b + c] << 16)));
+        if (r >= a.R) return 0.f;  // rows past the end read as zeros, which are never marked
+        return swiglu_bf16_f64(__uint_as_float((uint32_t)a.a[r * a.ld_a + c] << 16),
+                               __uint_as_float((uint32_t)a.b[r * a.ld_b + c] << 16));
     });
-    unpack_tile(ph, tl);
+    TileRegs tl;
+    unpack_packed(ph, tl);
     if (ROW)
         quant_tile_rows(tl, rows, a.q_row + r0 * a.ld_qr + c0, a.ld_qr, a.s_row + (c0 / kTile) * a.ld_sr + r0, tr, tc);
     if (COL)
@@ -94,7 +242,7 @@ __device__ __forceinline__ void load_ck(const uint8_t* ck, int64_t ld, const flo
 }
 
 template <bool ROW, bool COL>
-__global__ __launch_bounds__(kThreads) void swiglu_bwd_ckpt_kernel(SwigluBwdCkptArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void swiglu_bwd_ckpt_kernel(SwigluBwdCkptArgs a) {
     __shared__ float s_colmax[2][4][kTile];
     __shared__ __attribute__((aligned(16))) uint8_t s_tr[COL ? 2 : 1][COL ? kTile * kTile : 16];
     const int t = threadIdx.x;
@@ -109,7 +257,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_bwd_ckpt_kernel(SwigluBwdCkpt
     load_ck(a.ck + r0 * a.ld_ck + c0, a.ld_ck, sa, rows, tr, tc, ka);
     load_ck(a.ck + r0 * a.ld_ck + a.C + c0, a.ld_ck, sb, rows, tr, tc, kb);
     load_raw(a.dh, a.ld_dh, r0, c0, a.R, (8 * tr) * (int)(a.ld_dh * 2) + 16 * tc, rd);
-    Raw pda, pdb;  // da and db packed as bf16 (da marked where undecided)
+    Raw pd[2];  // da and db packed as bf16
+    uint32_t m[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float fa[8], fb[8], fd[8], ga[8], gb[8];
@@ -117,27 +266,37 @@ __global__ __launch_bounds__(kThreads) void swiglu_bwd_ckpt_kernel(SwigluBwdCkpt
         decode8(kb.q[i], kb.s[i], fb);
         unpack8(rd.v[i], fd);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) swiglu_grad_fast(fa[j], fb[j], fd[j], ga[j], gb[j]);
-        pda.v[i] = make_uint4(pack_bf16(ga[0], ga[1]), pack_bf16(ga[2], ga[3]), pack_bf16(ga[4], ga[5]),
-                              pack_bf16(ga[6], ga[7]));
-        pdb.v[i] = make_uint4(pack_bf16(gb[0], gb[1]), pack_bf16(gb[2], gb[3]), pack_bf16(gb[4], gb[5]),
-                              pack_bf16(gb[6], gb[7]));
+        for (int j = 0; j < 8; ++j) {
+            bool ok;
+            gate_grad(fa[j], fb[j], fd[j], ga[j], gb[j], ok);
+            m[i >> 2] = m[i >> 2] + m[i >> 2] + (ok ? 0u : 1u);  // one add with carry; element 0 ends in bit 31
+            if (j == 3) {
+                pin(m[i >> 2]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        pin(m[i >> 2]);
+        pd[0].v[i] = make_uint4(pack_bf16(ga[0], ga[1]), pack_bf16(ga[2], ga[3]), pack_bf16(ga[4], ga[5]),
+                                pack_bf16(ga[6], ga[7]));
+        pd[1].v[i] = make_uint4(pack_bf16(gb[0], gb[1]), pack_bf16(gb[2], gb[3]), pack_bf16(gb[4], gb[5]),
+                                pack_bf16(gb[6], gb[7]));
+        __builtin_amdgcn_sched_barrier(0);
     }
-    fixup_block(pda, [&](int e) {
+    while ((m[0] | m[1]) != 0) {
+        const int e = next_marked(m[0], m[1]);
         const int rl = 8 * tr + (e >> 3);
         const int64_t r = r0 + rl, c = c0 + 8 * tc + (e & 7);
-        if (r >= a.R) return;
+        if (r >= a.R) continue;  // rows past the end read as zeros, which are never marked
         const float2 g = swiglu_grad_bf16_f64(decode1(a.ck[r * a.ld_ck + c], sa[rl]),
                                               decode1(a.ck[r * a.ld_ck + a.C + c], sb[rl]),
                                               __uint_as_float((uint32_t)a.dh[r * a.ld_dh + c] << 16));
-        raw_set(pda, e, g.x);
-        raw_set(pdb, e, g.y);
-    });
+        set_pair(pd[0], pd[1], e, g.x, g.y);
+    }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int64_t co = (half ? a.C : 0) + c0;
         TileRegs tl;
-        unpack_tile(half ? pdb : pda, tl);
+        unpack_tile(pd[half], tl);
         if (ROW)
             quant_tile_rows(tl, rows, a.q_row + r0 * a.ld_qr + co, a.ld_qr, a.s_row + (co / kTile) * a.ld_sr + r0, tr,
                             tc);
