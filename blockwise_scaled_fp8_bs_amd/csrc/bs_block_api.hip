@@ -105,6 +105,7 @@ bs_status bs_moe_route(const void* logits, bs_dtype dtype, int64_t T, int64_t E,
     a.group_best = (int32_t)group_best;
     a.renorm = renormalize != 0; a.scale = scale; a.idx = idx; a.w = w;
     a.vec = vec_rows(logits, ld_l, dtype);
+    a.vec_bias = aligned16(bias);
     // groups that are all kept decide nothing
     if (topk_group == n_group) a.n_group = a.topk_group = 1;
     return hip_status(bs::launch_route(a, stream), fn);

@@ -22,7 +22,8 @@ struct RouteArgs {
     float scale;
     int32_t* idx;  // [T, k]
     float* w;      // [T, k]
-    bool vec;      // rows of logits allow 16-byte loads
+    bool vec, vec_bias;  // 16-byte loads of the logits' rows, of the bias
+    int32_t lds_token;   // floats of LDS of a token (set by the launcher)
 };
 
 struct RouteBwdArgs {

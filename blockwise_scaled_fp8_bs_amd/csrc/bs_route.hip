@@ -5,11 +5,12 @@
 // count), each holding V consecutive experts in registers, so that a wave
 // routes 64 / L tokens at once and a reduction over a token's experts is
 // log2(L) lane exchanges.  The choice is between values that may lie next to
-// one another, so it is made on exact keys: the logits themselves where no
-// bias is added (scores rise with their logits), float64 scores otherwise
-// (gfx950 runs float64 vector arithmetic at the unpacked fp32 rate).  Equal
-// keys go to the lowest expert: a lane's experts are consecutive, so that is
-// the lowest lane of the ballot and its first maximum.
+// one another and has to be exact: by the logits themselves where neither bias
+// nor groups are in play (scores rise with their logits), else by scores in
+// fp32 with a bound on their error, and in float64 for the tokens (some in a
+// thousand) whose choice that leaves in doubt.  Equal keys go to the lowest
+// expert: a lane's experts are consecutive, so that is the lowest lane of the
+// ballot and its first maximum.
 #include "bs_moe.h"
 #include "bs_device.h"
 
@@ -18,7 +19,7 @@ namespace bs {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr double kTinySum = 1e-20;  // added to the sum of the chosen sigmoid scores
+constexpr float kTinySum = 1e-20f;  // added to the sum of the chosen sigmoid scores
 
 // ---- reductions over the L lanes of a token; every lane gets the result ----
 // Steps 1 and 2 are quad permutes; 4 and 8 mirror halves of a 16-lane row
@@ -77,7 +78,8 @@ constexpr float kNegInf = -__builtin_inff();
 // V logits from expert e0 on; experts past E read as -inf.
 template <bool BF16, int V>
 __device__ __forceinline__ void load_logits(const void* base, int64_t row, int e0, int E, bool vec, float* f) {
-    if (vec && e0 + V <= E) {
+    constexpr bool kWhole = V % (BF16 ? 8 : 4) == 0;  // whole 16-byte loads
+    if (kWhole && vec && e0 + V <= E) {
         if constexpr (BF16) {
             const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + row + e0);
 #pragma unroll
@@ -91,8 +93,12 @@ __device__ __forceinline__ void load_logits(const void* base, int64_t row, int e
             }
         }
     } else {
+        // the last expert stands in for those past it, so that no load is conditional
 #pragma unroll
-        for (int v = 0; v < V; ++v) f[v] = e0 + v < E ? load_logit(base, BF16, row + e0 + v) : kNegInf;
+        for (int v = 0; v < V; ++v) {
+            const float x = load_logit(base, BF16, row + (e0 + v < E ? e0 + v : E - 1));
+            f[v] = e0 + v < E ? x : kNegInf;
+        }
     }
 }
 
@@ -106,12 +112,310 @@ __device__ __forceinline__ void wave_sync() {
 
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
 
-// F64: the keys are float64 scores (a bias or groups are in play).
-template <bool BF16, int L, int V, bool F64>
-__global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
-    extern __shared__ double s_dyn[];
-    using Key = typename std::conditional<F64, double, float>::type;
+// exp(x) for the choice: the product's rounding makes it err by |x| units of
+// 2^-24 and the hardware exponential by 2 more, where what counts is the error
+// of a score, exp(x) of the largest: at most 3 units.  Infinities and NaN come
+// out as they should.
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896f); }
+
+// Largest of V values with its place, the first of equals: halves compared
+// pairwise, since a chain of V dependent steps would take V latencies.  (By
+// recursion on values: a loop over arrays is turned into indexing them by the
+// result of a comparison.)
+template <typename Key>
+struct Placed {
+    Key value;
+    int place;
+};
+template <int V, int FROM = 0, typename Key>
+__device__ __forceinline__ Placed<Key> first_max(const Key* key) {
+    if constexpr (V == 1) {
+        return {key[FROM], FROM};
+    } else {
+        const Placed<Key> x = first_max<V / 2, FROM>(key), y = first_max<V / 2, FROM + V / 2>(key);
+        const bool up = y.value > x.value;
+        return {up ? y.value : x.value, up ? y.place : x.place};
+    }
+}
+template <int V, int FROM = 0>
+__device__ __forceinline__ uint32_t tree_max(const uint32_t* key) {
+    if constexpr (V == 1) {
+        return key[FROM];
+    } else {
+        const uint32_t x = tree_max<V / 2, FROM>(key), y = tree_max<V / 2, FROM + V / 2>(key);
+        return x > y ? x : y;
+    }
+}
+
+// The lowest expert among the lanes of a token that offer one (kMaxExperts: none).
+template <int L>
+__device__ __forceinline__ int lowest(bool offer, int e) {
+    return seg_reduce<L>(offer ? e : (int)kMaxExperts, [](int x, int y) { return x < y ? x : y; });
+}
+
+// k rounds over a token's keys: the best one left, ties to the lowest expert;
+// slot j's expert goes to lane j % L.
+template <int L, int V, int KR, typename Key>
+__device__ __forceinline__ void select_k(Key* key, int k, int l, int32_t* mine_idx) {
     constexpr Key kNone = -(Key)__builtin_inff();
+#pragma unroll
+    for (int r = 0; r < KR; ++r) {
+        mine_idx[r] = -1;
+        for (int q = 0; q < L; ++q) {
+            if (r * L + q >= k) break;
+            const Placed<Key> best = first_max<V>(key);
+            const Key mx = seg_max<L>(best.value);
+            const int e = lowest<L>(best.value == mx, l * V + best.place);
+#pragma unroll
+            for (int v = 0; v < V; ++v) key[v] = l * V + v == e ? kNone : key[v];
+            if (q == l && mx > kNone) mine_idx[r] = e;
+        }
+    }
+}
+
+// The choice in float64, from the logits on: what the definition says.  By all
+// 64 lanes, slot j's expert to lane j.
+template <bool BF16, int L, int V, int KR>
+__device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t row, int l, double* mine, int32_t* mine_idx) {
+    constexpr double kNone = -__builtin_inf();
+    const int E = (int)a.E, e0 = l * V;
+    float lg[V];
+    load_logits<BF16, V>(a.logits, row, e0, E, a.vec, lg);
+    double key[V];
+    float m = kNegInf;
+    if (!a.sigmoid) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) m = fmaxf(m, lg[v]);
+        m = seg_max<L>(m);
+    }
+    double sum = 0.0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const double d = lg[v];
+        key[v] = a.sigmoid ? sigmoid64(d) : (lg[v] == kNegInf ? 0.0 : exp(d - (double)m));
+        sum += key[v];
+    }
+    if (!a.sigmoid) {
+        const double r = 1.0 / seg_sum<L>(sum);
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] *= r;
+    }
+    if (a.bias != nullptr) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] += e0 + v < E ? (double)a.bias[e0 + v] : 0.0;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (key[v] != key[v]) key[v] = __builtin_inf();  // NaN ranks first
+        if (lg[v] == kNegInf) key[v] = kNone;            // and a masked expert never
+    }
+    if (a.n_group > 1) {
+        // Group scores: the keys go to LDS, one element more than Eg per
+        // group (lanes that read different groups then use different
+        // banks, and that element takes the group's score, then whether it
+        // is kept); lane l takes the groups l, l + L, ... of its token.  A
+        // token's lanes are in one wave: its LDS operations run in order.
+        const int G = a.n_group, Eg = E / G;
+        const int g_first = e0 / Eg;
+        int at = e0 + g_first, left = Eg - (e0 - g_first * Eg);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (e0 + v < E) mine[at] = key[v];
+            left -= 1;
+            at += left == 0 ? 2 : 1;
+            left = left == 0 ? Eg : left;
+        }
+        wave_sync();
+        for (int g = l; g < G; g += L) {
+            double b1 = kNone, b2 = kNone;
+#pragma unroll 4
+            for (int i = 0; i < Eg; ++i) {
+                const double x = mine[g * (Eg + 1) + i];
+                b2 = fmax(b2, fmin(b1, x));
+                b1 = fmax(b1, x);
+            }
+            if (a.group_best > 1 && b2 > kNone) b1 += b2;
+            mine[g * (Eg + 1) + Eg] = b1;
+        }
+        wave_sync();
+        // a group is kept if fewer than topk_group are better
+        uint32_t kept = 0;  // bit i: group l + i L (at most V of them)
+        for (int g = l, i = 0; g < G; g += L, ++i) {
+            const double own = mine[g * (Eg + 1) + Eg];
+            int better = 0;
+#pragma unroll 4
+            for (int h = 0; h < G; ++h) {
+                const double o = mine[h * (Eg + 1) + Eg];
+                better += (o > own) | ((o == own) & (h < g));
+            }
+            kept |= (better < a.topk_group ? 1u : 0u) << i;
+        }
+        wave_sync();
+        for (int g = l, i = 0; g < G; g += L, ++i) mine[g * (Eg + 1) + Eg] = (double)((kept >> i) & 1u);
+        wave_sync();
+        at = g_first * (Eg + 1) + Eg;
+        left = Eg - (e0 - g_first * Eg);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (e0 + v < E && mine[at] == 0.0) key[v] = kNone;
+            left -= 1;
+            at += left == 0 ? Eg + 1 : 0;
+            left = left == 0 ? Eg : left;
+        }
+        if (a.bias == nullptr) {  // without a bias experts are ranked by their logits
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (key[v] != kNone) key[v] = lg[v] != lg[v] ? __builtin_inf() : (double)lg[v];
+        }
+    }
+    select_k<L, V, KR>(key, a.k, l, mine_idx);
+}
+
+// Order-preserving image of a float in unsigned integers, and back.
+__device__ __forceinline__ uint32_t to_ordered(float f) {
+    const uint32_t b = __float_as_uint(f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// The choice in fp32 where that is certain.  Scores err by at most 8 (sigmoid,
+// of values up to 1) or 32 (softmax, of the largest: exponent, sum and
+// quotient) units of 2^-24, a sum with the bias by one more of itself, and a
+// key gives up its lowest log2(V) bits to the expert's place in its lane, so
+// that a maximum finds both: two choices nearer than twice that are
+// uncertain, unless logit and bias are the same and so the tie is real.
+// Returns whether the token's choice is uncertain (then route_exact decides).
+template <int L, int V, int KR>
+__device__ __forceinline__ bool route_fast(const RouteArgs& a, const float* lg, const float* bias,
+                                           const float* row_lds, int l, float* group_lds, int32_t* mine_idx) {
+    const int E = (int)a.E, e0 = l * V;
+    constexpr float u = 5.9604645e-08f;  // 2^-24
+    float c[V];
+    float err = 16.f * u;
+    if (a.sigmoid) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) c[v] = __builtin_amdgcn_rcpf(1.0f + exp_fast(-lg[v]));
+    } else {
+        float m = kNegInf, sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) m = fmaxf(m, lg[v]);
+        m = seg_max<L>(m);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            c[v] = lg[v] == kNegInf ? 0.f : exp_fast(lg[v] - m);
+            sum += c[v];
+        }
+        const float r = 1.0f / seg_sum<L>(sum);
+#pragma unroll
+        for (int v = 0; v < V; ++v) c[v] *= r;
+        err = 64.f * u * r;  // r: the largest score
+    }
+    if (a.bias != nullptr) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) c[v] += bias[v];
+    }
+    bool unsure = false, keep = true;
+    if (a.n_group > 1) {
+        // whole lanes per group (the caller has seen to it): the two best of a
+        // lane, then of the group's lanes
+        const int G = a.n_group, lanes = E / G / V, g = l / lanes;
+        float b1 = kNegInf, b2 = kNegInf;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float x = lg[v] == kNegInf ? kNegInf : c[v];
+            unsure |= x != x;
+            b2 = __builtin_amdgcn_fmed3f(b1, b2, x);
+            b1 = fmaxf(b1, x);
+        }
+#define BS_MERGE(STEP)                                                            \
+        if constexpr (L > STEP) {                                                 \
+            if (lanes > STEP) {                                                   \
+                const float o1 = lane_swap<STEP>(b1), o2 = lane_swap<STEP>(b2);   \
+                b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));                         \
+                b1 = fmaxf(b1, o1);                                               \
+            }                                                                     \
+        }
+        BS_MERGE(1) BS_MERGE(2) BS_MERGE(4) BS_MERGE(8) BS_MERGE(16) BS_MERGE(32)
+#undef BS_MERGE
+        const float own = a.group_best > 1 && b2 > kNegInf ? b1 + b2 : b1;
+        if (g < G) group_lds[g] = own;
+        wave_sync();
+        int surely = 0, maybe = 0;  // groups that are, and may be, better
+        const float w0 = 2.f * err + 4.f * u * fabsf(own);
+#pragma unroll 4
+        for (int h = 0; h < G; ++h) {
+            const float o = group_lds[h], w = w0 + 4.f * u * fabsf(o);
+            surely += o - own > w;
+            maybe += (h != g) & !(own - o > w);
+        }
+        keep = surely < a.topk_group;
+        unsure |= b1 > kNegInf && keep != (maybe < a.topk_group);
+        wave_sync();  // the next use of group_lds
+    }
+    if (a.bias == nullptr) {  // ranked by their logits, exactly
+        float key[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            key[v] = !keep || lg[v] == kNegInf ? kNegInf : lg[v] != lg[v] ? __builtin_inff() : lg[v];
+        select_k<L, V, KR>(key, a.k, l, mine_idx);
+        return unsure;
+    }
+    constexpr uint32_t kPlace = V - 1;
+    uint32_t key[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const float x = c[v] != c[v] ? __builtin_inff() : c[v];
+        key[v] = !keep || lg[v] == kNegInf ? 0u : (to_ordered(x) & ~kPlace) | (uint32_t)(kPlace - v);
+    }
+    float prev = 0.f;
+    int prev_e = -1;
+#pragma unroll
+    for (int r = 0; r <= KR; ++r) {  // one round more than k: the first that is left out
+        if (r < KR) mine_idx[r] = -1;
+        for (int q = 0; q < (r < KR ? L : 1); ++q) {
+            const int j = r * L + q;
+            if (j > a.k) break;
+            const uint32_t best = tree_max<V>(key), top = best & ~kPlace;
+            const uint32_t mx = seg_reduce<L>(top, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+            const int own_e = e0 + (int)(kPlace - (best & kPlace));
+            const int e = lowest<L>(top == mx, own_e);
+            const uint32_t gone = e == own_e ? best : 0xFFFFFFFFu;
+#pragma unroll
+            for (int v = 0; v < V; ++v) key[v] = key[v] == gone ? 0u : key[v];
+            if (mx == 0u) break;
+            const float cur = from_ordered(mx);
+            if (prev_e >= 0) {
+                const float w = err + (float)(2 * V + 2) * 2.f * u * fmaxf(fabsf(prev), fabsf(cur));
+                if (!(prev - cur > w)) {
+                    const bool same = row_lds[prev_e] == row_lds[e] && a.bias[prev_e] == a.bias[e];
+                    unsure |= !same;
+                }
+            }
+            prev = cur;
+            prev_e = e;
+            if (r < KR && q == l && j < a.k) mine_idx[r] = e;
+        }
+    }
+    return unsure;
+}
+
+// A lane's logits to its token's row in LDS.
+template <int V>
+__device__ __forceinline__ void keep_row(float* lds, const float* lg) {
+    wave_sync();
+#pragma unroll
+    for (int v = 0; v < V; v += 4)
+        *reinterpret_cast<float4*>(lds + v) = make_float4(lg[v], lg[v + 1], lg[v + 2], lg[v + 3]);
+    wave_sync();
+}
+
+// SCORES: the choice goes by scores (a bias or groups are in play); without,
+// by the logits, and exactly so in fp32.
+template <bool BF16, int L, int V, bool SCORES>
+__global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, bool fast) {
+    extern __shared__ double s_dyn[];
     constexpr int TPB = kThreads / L;  // tokens of a block
     constexpr int KR = (int)kMaxTopK < V * L ? ((int)kMaxTopK + L - 1) / L : V;  // slots a lane may hold
 
@@ -122,168 +426,79 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
     const int64_t row = (real ? tok : a.T - 1) * a.ld;
     const int E = (int)a.E, e0 = l * V;
 
-    float lg[V];
+    // the one trip to memory: the logits (also to LDS, where the chosen ones
+    // are looked up at the end) and the bias
+    float* const row_lds = reinterpret_cast<float*>(s_dyn) + tb * a.lds_token;
+    float lg[V], bias[V];
     load_logits<BF16, V>(a.logits, row, e0, E, a.vec, lg);
-
-    float m = 0.f;
-    double z = 1.0;  // softmax: the largest logit and the sum of exp(l - m)
-    const bool need_z = !a.sigmoid && (F64 || !a.renorm);
-    if (need_z) {
-        m = kNegInf;
+    if (SCORES && a.bias != nullptr) load_logits<false, V>(a.bias, 0, e0, E, a.vec_bias, bias);
+    keep_row<V>(row_lds + e0, lg);
+    float m = kNegInf, z = 0.f;  // softmax over all experts: the largest logit, the sum of exp(l - m)
+    if (!a.sigmoid && !a.renorm) {
 #pragma unroll
         for (int v = 0; v < V; ++v) m = fmaxf(m, lg[v]);
         m = seg_max<L>(m);
+#pragma unroll
+        for (int v = 0; v < V; ++v) z += lg[v] == kNegInf ? 0.f : expf(lg[v] - m);
+        z = seg_sum<L>(z);
     }
-    Key key[V];
-    if constexpr (F64) {
-        double sum = 0.0;
+
+    int32_t mine_idx[KR];
+    if constexpr (SCORES) {
+        bool unsure = true;
+        if (fast) unsure = route_fast<L, V, KR>(a, lg, bias, row_lds, l, row_lds + L * V, mine_idx);
+        // rare: the tokens in doubt one after another, each by the whole wave
+        // (a wave that redid its tokens as they lie would take 12 us more at
+        // 256 experts, and some wave always has one)
+        uint64_t some = __ballot(unsure);
+        while (some != 0) {
+            const int lane = threadIdx.x & 63, at = __builtin_ctzll(some) / L * L;
+            constexpr uint64_t kToken = L < 64 ? (1ull << L) - 1 : ~0ull;
+            some &= ~(kToken << at);
+            const int tw = (threadIdx.x & ~63) / L + at / L;  // the token's place in the block
+            int64_t t = (int64_t)blockIdx.x * TPB + tw;
+            if (t >= a.T) t = a.T - 1;
+            float* const lds = reinterpret_cast<float*>(s_dyn) + tw * a.lds_token;
+            constexpr int VW = V * L > 64 ? V * L / 64 : 1;
+            int32_t exact[1];
+            route_exact<BF16, 64, VW, 1>(a, t * a.ld, lane, reinterpret_cast<double*>(lds), exact);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const double d = lg[v];
-            key[v] = a.sigmoid ? sigmoid64(d) : (lg[v] == kNegInf ? 0.0 : exp(d - (double)m));
-            sum += key[v];
-        }
-        if (!a.sigmoid) {
-            z = seg_sum<L>(sum);
-            const double r = 1.0 / z;
-#pragma unroll
-            for (int v = 0; v < V; ++v) key[v] *= r;
-        }
-        if (a.bias != nullptr) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) key[v] += e0 + v < E ? (double)a.bias[e0 + v] : 0.0;
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (key[v] != key[v]) key[v] = __builtin_inf();  // NaN ranks first
-            if (lg[v] == kNegInf) key[v] = kNone;            // and a masked expert never
-        }
-        if (a.n_group > 1) {
-            // Group scores: the keys go to LDS, one element more than Eg per
-            // group (lanes that read different groups then use different
-            // banks, and that element takes the group's score, then whether it
-            // is kept); lane l takes the groups l, l + L, ... of its token.  A
-            // token's lanes are in one wave: its LDS operations run in order.
-            const int G = a.n_group, Eg = E / G;
-            double* const mine = s_dyn + tb * (E + G);
-            const int g_first = e0 / Eg;
-            int at = e0 + g_first, left = Eg - (e0 - g_first * Eg);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (e0 + v < E) mine[at] = key[v];
-                left -= 1;
-                at += left == 0 ? 2 : 1;
-                left = left == 0 ? Eg : left;
+            for (int r = 0; r < KR; ++r) {
+                const int32_t e = __shfl(exact[0], (r * L + l) & 63);
+                if (seg == at) mine_idx[r] = r * L + l < a.k ? e : -1;
             }
-            wave_sync();
-            for (int g = l; g < G; g += L) {
-                double b1 = kNone, b2 = kNone;
-                for (int i = 0; i < Eg; ++i) {
-                    const double x = mine[g * (Eg + 1) + i];
-                    b2 = fmax(b2, fmin(b1, x));
-                    b1 = fmax(b1, x);
-                }
-                if (a.group_best > 1 && b2 > kNone) b1 += b2;
-                mine[g * (Eg + 1) + Eg] = b1;
-            }
-            wave_sync();
-            // a group is kept if fewer than topk_group are better
-            uint32_t kept = 0;  // bit i: group l + i L (at most V of them)
-            for (int g = l, i = 0; g < G; g += L, ++i) {
-                const double own = mine[g * (Eg + 1) + Eg];
-                int better = 0;
-                for (int h = 0; h < G; ++h) {
-                    const double o = mine[h * (Eg + 1) + Eg];
-                    better += (o > own) | ((o == own) & (h < g));
-                }
-                kept |= (better < a.topk_group ? 1u : 0u) << i;
-            }
-            wave_sync();
-            for (int g = l, i = 0; g < G; g += L, ++i) mine[g * (Eg + 1) + Eg] = (double)((kept >> i) & 1u);
-            wave_sync();
-            at = g_first * (Eg + 1) + Eg;
-            left = Eg - (e0 - g_first * Eg);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (e0 + v < E && mine[at] == 0.0) key[v] = kNone;
-                left -= 1;
-                at += left == 0 ? Eg + 1 : 0;
-                left = left == 0 ? Eg : left;
-            }
-            if (a.bias == nullptr) {  // without a bias experts are ranked by their logits
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (key[v] != kNone) key[v] = lg[v] != lg[v] ? __builtin_inf() : (double)lg[v];
-            }
+            if (seg == at) keep_row<V>(row_lds + e0, lg);  // (the exact keys took its place)
         }
     } else {
-        if (need_z) {
-            float sum = 0.f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) sum += lg[v] == kNegInf ? 0.f : expf(lg[v] - m);
-            z = (double)seg_sum<L>(sum);
-        }
+        float key[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) key[v] = lg[v] != lg[v] ? __builtin_inff() : lg[v];
+        select_k<L, V, KR>(key, a.k, l, mine_idx);
     }
 
-    // k rounds: the best key left, its expert to the lane that holds slot j
-    int32_t mine_idx[KR];
-#pragma unroll
-    for (int r = 0; r < KR; ++r) {
-        mine_idx[r] = -1;
-        for (int q = 0; q < L; ++q) {
-            if (r * L + q >= a.k) break;
-            Key bm = key[0];
-            int bi = 0;
-#pragma unroll
-            for (int v = 1; v < V; ++v) {
-                if (key[v] > bm) {
-                    bm = key[v];
-                    bi = v;
-                }
-            }
-            int e = e0 + bi;
-            Key mx = bm;
-            bool win = true;
-            if constexpr (L > 1) {
-                mx = seg_max<L>(bm);
-                uint64_t vote = __ballot(bm == mx) >> seg;
-                if constexpr (L < 64) vote &= (1ull << L) - 1;
-                const int first = __builtin_ctzll(vote);
-                win = first == l;
-                e = __shfl(e, seg + first);
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (win && v == bi) key[v] = kNone;
-            if (q == l && mx > kNone) mine_idx[r] = e;
-        }
-    }
-
-    // weights of the chosen experts, in float64 (a few values per token)
-    double s[KR];
+    // weights of the chosen experts, in fp32
+    float s[KR];
     float top = kNegInf;
     if (!a.sigmoid && a.renorm) {
 #pragma unroll
         for (int r = 0; r < KR; ++r) {
             if (r * L >= a.k) break;
-            if (mine_idx[r] >= 0) top = fmaxf(top, load_logit(a.logits, BF16, row + mine_idx[r]));
+            if (mine_idx[r] >= 0) top = fmaxf(top, row_lds[mine_idx[r]]);
         }
         top = seg_max<L>(top);
     }
-    double sum = 0.0;
+    float sum = 0.f;
 #pragma unroll
     for (int r = 0; r < KR; ++r) {
-        s[r] = 0.0;
+        s[r] = 0.f;
         if (r * L >= a.k) continue;
         if (mine_idx[r] >= 0) {
-            const double d = load_logit(a.logits, BF16, row + mine_idx[r]);
-            s[r] = a.sigmoid ? sigmoid64(d) : a.renorm ? exp(d - (double)top) : exp(d - (double)m) / z;
+            const float d = row_lds[mine_idx[r]];
+            s[r] = a.sigmoid ? 1.0f / (1.0f + expf(-d)) : a.renorm ? expf(d - top) : expf(d - m) / z;
         }
         sum += s[r];
     }
-    double f = a.scale;
+    float f = a.scale;
     if (a.renorm) {
         sum = seg_sum<L>(sum);
         if (a.sigmoid) sum += kTinySum;
@@ -295,7 +510,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
         const int j = r * L + l;
         if (j < a.k) {
             a.idx[tok * a.k + j] = mine_idx[r];
-            a.w[tok * a.k + j] = mine_idx[r] >= 0 ? (float)(s[r] * f) : 0.f;
+            a.w[tok * a.k + j] = mine_idx[r] >= 0 ? s[r] * f : 0.f;
         }
     }
 }
@@ -360,7 +575,7 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a) {
     }
     dot = seg_sum<L>(dot);
     float f = a.scale;
-    if (a.sigmoid && a.renorm) f = a.scale / (seg_sum<L>(ssum) + (float)kTinySum);
+    if (a.sigmoid && a.renorm) f = a.scale / (seg_sum<L>(ssum) + kTinySum);
 #pragma unroll
     for (int r = 0; r < KR; ++r) {
         if (e[r] >= 0) {
@@ -414,15 +629,23 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a) {
 }
 
 template <int L, int V>
-hipError_t route_lv(const RouteArgs& a, hipStream_t stream) {
+hipError_t route_lv(RouteArgs a, hipStream_t stream) {
     constexpr int TPB = kThreads / L;
     const dim3 grid((unsigned)((a.T + TPB - 1) / TPB)), block(kThreads);
-    const bool f64 = a.bias != nullptr || a.n_group > 1;
-    const size_t lds = a.n_group > 1 ? (size_t)TPB * (a.E + a.n_group) * sizeof(double) : 0;
-    if (a.bf16 && f64) hipLaunchKernelGGL((route_kernel<true, L, V, true>), grid, block, lds, stream, a);
-    else if (a.bf16) hipLaunchKernelGGL((route_kernel<true, L, V, false>), grid, block, 0, stream, a);
-    else if (f64) hipLaunchKernelGGL((route_kernel<false, L, V, true>), grid, block, lds, stream, a);
-    else hipLaunchKernelGGL((route_kernel<false, L, V, false>), grid, block, 0, stream, a);
+    const bool scores = a.bias != nullptr || a.n_group > 1;
+    // LDS of a token: its logits and the groups' scores; with groups the exact
+    // path puts E + n_group float64 keys in their place
+    int64_t words = L * V + (a.n_group > 1 ? a.n_group : 0);
+    if (a.n_group > 1 && 2 * (a.E + a.n_group) > words) words = 2 * (a.E + a.n_group);
+    a.lds_token = (int32_t)((words + 3) / 4 * 4);
+    const size_t lds = (size_t)TPB * a.lds_token * sizeof(float);
+    // fp32 first where every group is a power of two of whole lanes
+    const int64_t lanes = a.E / a.n_group / V;
+    const bool fast = a.n_group == 1 || (lanes * V * a.n_group == a.E && (lanes & (lanes - 1)) == 0);
+    if (a.bf16 && scores) hipLaunchKernelGGL((route_kernel<true, L, V, true>), grid, block, lds, stream, a, fast);
+    else if (a.bf16) hipLaunchKernelGGL((route_kernel<true, L, V, false>), grid, block, lds, stream, a, fast);
+    else if (scores) hipLaunchKernelGGL((route_kernel<false, L, V, true>), grid, block, lds, stream, a, fast);
+    else hipLaunchKernelGGL((route_kernel<false, L, V, false>), grid, block, lds, stream, a, fast);
     return hipGetLastError();
 }
 

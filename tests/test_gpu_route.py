@@ -138,3 +138,25 @@ def test_route_empty_batch_and_far_scores():
     l = torch.full((1, 8), -80.0, device="cuda")     # sum far below 1e-20: the weights vanish, nothing is NaN
     _, w = bs.bs_moe_route(l, 2, score=bs.BS_SCORE_SIGMOID)
     assert (w.cpu() < 1e-10).all() and not torch.isnan(w).any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("kind", [block.SOFTMAX, block.SIGMOID], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G", [(64, 1), (256, 8), (128, 1), (512, 4), (32, 4), (48, 3)])
+def test_route_choices_next_to_one_another(E, G, kind, dtype):
+    """A bias that brings the choice values within about an fp32 step of a few
+    levels: only float64 tells them apart."""
+    need_gpu()
+    T, k = 24, min(8, E // G)
+    l = _logits(T, E, dtype, seed=77)
+    l[3:5] = 0.25
+    s = block.scores(_f64(l), kind)
+    for row, level in ((0, 0.75), (7, 0.125), (11, -0.5)):
+        want = np.where(np.arange(E) % 3 == 0, level, level + 0.01)
+        bias = torch.from_numpy((want - s[row]).astype(np.float32))
+        kw = dict(n_group=G, topk_group=max(1, G // 2), group_best=2)
+        print(f"route near ties E={E} G={G} kind={kind} {dtype} row={row}", flush=True)
+        want_idx, want_w = block.route(_f64(l), k, bias=_f64(bias), kind=kind, **kw)
+        idx, w = bs.bs_moe_route(l.cuda(), k, bias=bias.cuda(), score=kind, **kw)
+        assert np.array_equal(idx.cpu().numpy(), want_idx)
+        _weights_close(w.cpu().double().numpy(), want_w)
