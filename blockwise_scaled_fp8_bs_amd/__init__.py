@@ -55,3 +55,11 @@ from .binding_block import (  # noqa: F401,E402
 from .linear import Float8BlockwiseLinear, float8_blockwise_linear, swap_linear_layers  # noqa: F401,E402
 from .ffn import Float8BlockwiseGatedFFN, float8_blockwise_gated_ffn  # noqa: F401,E402
 from .mx import Float8MXLinear, float8_mx_linear, mx_grouped_mm  # noqa: F401,E402
+from .moe import (  # noqa: F401,E402
+    Float8BlockwiseMoE,
+    float8_blockwise_moe_ffn,
+    moe_combine,
+    moe_dispatch,
+    moe_route,
+    resid_norm,
+)
