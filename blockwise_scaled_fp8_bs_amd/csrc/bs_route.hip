@@ -287,9 +287,11 @@ __device__ __forceinline__ float from_ordered(uint32_t k) {
 // that a maximum finds both: two choices nearer than twice that are
 // uncertain, unless logit and bias are the same and so the tie is real.
 // Returns whether the token's choice is uncertain (then route_exact decides).
+// whole: every group is a power of two of whole lanes (see route_lv).
 template <int L, int V, int KR>
 __device__ __forceinline__ bool route_fast(const RouteArgs& a, const float* lg, const float* bias,
-                                           const float* row_lds, int l, float* group_lds, int32_t* mine_idx) {
+                                           const float* row_lds, int l, float* group_lds, bool whole,
+                                           int32_t* mine_idx) {
     const int E = (int)a.E, e0 = l * V;
     constexpr float u = 5.9604645e-08f;  // 2^-24
     float c[V];
@@ -316,15 +318,32 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const float* lg, 
 #pragma unroll
         for (int v = 0; v < V; ++v) c[v] += bias[v];
     }
-    bool unsure = false, keep = true;
-    if (a.n_group > 1) {
-        // whole lanes per group (the caller has seen to it): the two best of a
-        // lane, then of the group's lanes
+    uint32_t dead = 0;  // bit v: masked
+#pragma unroll
+    for (int v = 0; v < V; ++v) dead |= (uint32_t)(lg[v] == kNegInf || c[v] == kNegInf) << v;
+    bool unsure = false;
+    // Groups better than g, surely and maybe, from their scores `stride` apart:
+    // true if g stays.
+    const auto stays = [&](const float* score, int stride, int g, float own) {
+        int surely = 0, maybe = 0;
+        const float w0 = 2.f * err + 4.f * u * fabsf(own);
+#pragma unroll 4
+        for (int h = 0; h < a.n_group; ++h) {
+            const float o = score[h * stride], w = w0 + 4.f * u * fabsf(o);
+            surely += o - own > w;
+            maybe += (h != g) & (o != kNegInf) & !(own - o > w);
+        }
+        const bool keep = surely < a.topk_group;
+        unsure |= own != kNegInf && keep != (maybe < a.topk_group);
+        return keep;
+    };
+    if (a.n_group > 1 && whole) {
+        // the two best of a lane, then of the group's lanes
         const int G = a.n_group, lanes = E / G / V, g = l / lanes;
         float b1 = kNegInf, b2 = kNegInf;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float x = lg[v] == kNegInf ? kNegInf : c[v];
+            const float x = (dead >> v) & 1u ? kNegInf : c[v];
             unsure |= x != x;
             b2 = __builtin_amdgcn_fmed3f(b1, b2, x);
             b1 = fmaxf(b1, x);
@@ -342,23 +361,56 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const float* lg, 
         const float own = a.group_best > 1 && b2 > kNegInf ? b1 + b2 : b1;
         if (g < G) group_lds[g] = own;
         wave_sync();
-        int surely = 0, maybe = 0;  // groups that are, and may be, better
-        const float w0 = 2.f * err + 4.f * u * fabsf(own);
-#pragma unroll 4
-        for (int h = 0; h < G; ++h) {
-            const float o = group_lds[h], w = w0 + 4.f * u * fabsf(o);
-            surely += o - own > w;
-            maybe += (h != g) & !(own - o > w);
+        if (!stays(group_lds, 1, g, own)) dead = ~0u;
+        wave_sync();  // the next use of group_lds
+    } else if (a.n_group > 1) {
+        // groups of any size: through LDS, laid out as in route_exact (16
+        // experts in 4 groups, 8192 tokens: 7 us; by route_exact alone 41)
+        const int G = a.n_group, Eg = E / G, g_first = e0 / Eg;
+        int at = e0 + g_first, left = Eg - (e0 - g_first * Eg);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float x = (dead >> v) & 1u ? kNegInf : c[v];
+            unsure |= x != x;
+            if (e0 + v < E) group_lds[at] = x;
+            left -= 1;
+            at += left == 0 ? 2 : 1;
+            left = left == 0 ? Eg : left;
         }
-        keep = surely < a.topk_group;
-        unsure |= b1 > kNegInf && keep != (maybe < a.topk_group);
+        wave_sync();
+        for (int g = l; g < G; g += L) {
+            float b1 = kNegInf, b2 = kNegInf;
+#pragma unroll 4
+            for (int i = 0; i < Eg; ++i) {
+                const float x = group_lds[g * (Eg + 1) + i];
+                b2 = fmaxf(b2, fminf(b1, x));
+                b1 = fmaxf(b1, x);
+            }
+            group_lds[g * (Eg + 1) + Eg] = a.group_best > 1 && b2 > kNegInf ? b1 + b2 : b1;
+        }
+        wave_sync();
+        uint32_t kept = 0;  // bit i: group l + i L (at most V of them)
+        for (int g = l, i = 0; g < G; g += L, ++i)
+            kept |= (uint32_t)stays(group_lds + Eg, Eg + 1, g, group_lds[g * (Eg + 1) + Eg]) << i;
+        wave_sync();
+        for (int g = l, i = 0; g < G; g += L, ++i) group_lds[g * (Eg + 1) + Eg] = (float)((kept >> i) & 1u);
+        wave_sync();
+        at = g_first * (Eg + 1) + Eg;
+        left = Eg - (e0 - g_first * Eg);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            dead |= (uint32_t)(e0 + v < E && group_lds[at] == 0.f) << v;
+            left -= 1;
+            at += left == 0 ? Eg + 1 : 0;
+            left = left == 0 ? Eg : left;
+        }
         wave_sync();  // the next use of group_lds
     }
     if (a.bias == nullptr) {  // ranked by their logits, exactly
         float key[V];
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            key[v] = !keep || lg[v] == kNegInf ? kNegInf : lg[v] != lg[v] ? __builtin_inff() : lg[v];
+            key[v] = (dead >> v) & 1u ? kNegInf : lg[v] != lg[v] ? __builtin_inff() : lg[v];
         select_k<L, V, KR>(key, a.k, l, mine_idx);
         return unsure;
     }
@@ -367,16 +419,19 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const float* lg, 
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const float x = c[v] != c[v] ? __builtin_inff() : c[v];
-        key[v] = !keep || lg[v] == kNegInf ? 0u : (to_ordered(x) & ~kPlace) | (uint32_t)(kPlace - v);
+        key[v] = (dead >> v) & 1u ? 0u : (to_ordered(x) & ~kPlace) | (uint32_t)(kPlace - v);
     }
     float prev = 0.f;
     int prev_e = -1;
+    const auto near = [&](float cur) {  // to the value before it in the order
+        return !(prev - cur > err + (float)(2 * V + 2) * 2.f * u * fmaxf(fabsf(prev), fabsf(cur)));
+    };
 #pragma unroll
-    for (int r = 0; r <= KR; ++r) {  // one round more than k: the first that is left out
-        if (r < KR) mine_idx[r] = -1;
-        for (int q = 0; q < (r < KR ? L : 1); ++q) {
+    for (int r = 0; r < KR; ++r) {
+        mine_idx[r] = -1;
+        for (int q = 0; q < L; ++q) {
             const int j = r * L + q;
-            if (j > a.k) break;
+            if (j >= a.k) break;
             const uint32_t best = tree_max<V>(key), top = best & ~kPlace;
             const uint32_t mx = seg_reduce<L>(top, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
             const int own_e = e0 + (int)(kPlace - (best & kPlace));
@@ -386,17 +441,22 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const float* lg, 
             for (int v = 0; v < V; ++v) key[v] = key[v] == gone ? 0u : key[v];
             if (mx == 0u) break;
             const float cur = from_ordered(mx);
-            if (prev_e >= 0) {
-                const float w = err + (float)(2 * V + 2) * 2.f * u * fmaxf(fabsf(prev), fabsf(cur));
-                if (!(prev - cur > w)) {
-                    const bool same = row_lds[prev_e] == row_lds[e] && a.bias[prev_e] == a.bias[e];
-                    unsure |= !same;
-                }
-            }
+            if (prev_e >= 0 && near(cur))
+                unsure |= row_lds[prev_e] != row_lds[e] || a.bias[prev_e] != a.bias[e];
             prev = cur;
             prev_e = e;
-            if (r < KR && q == l && j < a.k) mine_idx[r] = e;
+            if (q == l) mine_idx[r] = e;
         }
+    }
+    // those left out, every one of them against the last that was chosen: one
+    // that ties with it may have another next to it
+    uint32_t close = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) close |= (uint32_t)(key[v] != 0u && near(from_ordered(key[v] & ~kPlace))) << v;
+    while (close != 0) {
+        const int e = e0 + __builtin_ctz(close);
+        close &= close - 1;
+        unsure |= row_lds[prev_e] != row_lds[e] || a.bias[prev_e] != a.bias[e];
     }
     return unsure;
 }
@@ -414,7 +474,7 @@ __device__ __forceinline__ void keep_row(float* lds, const float* lg) {
 // SCORES: the choice goes by scores (a bias or groups are in play); without,
 // by the logits, and exactly so in fp32.
 template <bool BF16, int L, int V, bool SCORES>
-__global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, bool fast) {
+__global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, bool whole) {
     extern __shared__ double s_dyn[];
     constexpr int TPB = kThreads / L;  // tokens of a block
     constexpr int KR = (int)kMaxTopK < V * L ? ((int)kMaxTopK + L - 1) / L : V;  // slots a lane may hold
@@ -445,19 +505,17 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, bool fast)
 
     int32_t mine_idx[KR];
     if constexpr (SCORES) {
-        bool unsure = true;
-        if (fast) unsure = route_fast<L, V, KR>(a, lg, bias, row_lds, l, row_lds + L * V, mine_idx);
+        const bool unsure = route_fast<L, V, KR>(a, lg, bias, row_lds, l, row_lds + L * V, whole, mine_idx);
         // rare: the tokens in doubt one after another, each by the whole wave
         // (a wave that redid its tokens as they lie would take 12 us more at
         // 256 experts, and some wave always has one)
-        uint64_t some = __ballot(unsure);
+        uint64_t some = __ballot(unsure && real);
         while (some != 0) {
             const int lane = threadIdx.x & 63, at = __builtin_ctzll(some) / L * L;
             constexpr uint64_t kToken = L < 64 ? (1ull << L) - 1 : ~0ull;
             some &= ~(kToken << at);
             const int tw = (threadIdx.x & ~63) / L + at / L;  // the token's place in the block
-            int64_t t = (int64_t)blockIdx.x * TPB + tw;
-            if (t >= a.T) t = a.T - 1;
+            const int64_t t = (int64_t)blockIdx.x * TPB + tw;
             float* const lds = reinterpret_cast<float*>(s_dyn) + tw * a.lds_token;
             constexpr int VW = V * L > 64 ? V * L / 64 : 1;
             int32_t exact[1];
@@ -633,19 +691,23 @@ hipError_t route_lv(RouteArgs a, hipStream_t stream) {
     constexpr int TPB = kThreads / L;
     const dim3 grid((unsigned)((a.T + TPB - 1) / TPB)), block(kThreads);
     const bool scores = a.bias != nullptr || a.n_group > 1;
-    // LDS of a token: its logits and the groups' scores; with groups the exact
-    // path puts E + n_group float64 keys in their place
-    int64_t words = L * V + (a.n_group > 1 ? a.n_group : 0);
-    if (a.n_group > 1 && 2 * (a.E + a.n_group) > words) words = 2 * (a.E + a.n_group);
+    // Every group a power of two of whole lanes: its best are found between
+    // lanes.  LDS of a token: its logits, then the groups' scores, or with
+    // other groups E keys and those; the exact path puts E + n_group float64
+    // keys in the place of all that.
+    const int64_t lanes = a.E / a.n_group / V;
+    const bool whole = lanes * V * a.n_group == a.E && (lanes & (lanes - 1)) == 0;
+    int64_t words = L * V;
+    if (a.n_group > 1) {
+        words += a.n_group + (whole ? 0 : a.E);
+        if (2 * (a.E + a.n_group) > words) words = 2 * (a.E + a.n_group);
+    }
     a.lds_token = (int32_t)((words + 3) / 4 * 4);
     const size_t lds = (size_t)TPB * a.lds_token * sizeof(float);
-    // fp32 first where every group is a power of two of whole lanes
-    const int64_t lanes = a.E / a.n_group / V;
-    const bool fast = a.n_group == 1 || (lanes * V * a.n_group == a.E && (lanes & (lanes - 1)) == 0);
-    if (a.bf16 && scores) hipLaunchKernelGGL((route_kernel<true, L, V, true>), grid, block, lds, stream, a, fast);
-    else if (a.bf16) hipLaunchKernelGGL((route_kernel<true, L, V, false>), grid, block, lds, stream, a, fast);
-    else if (scores) hipLaunchKernelGGL((route_kernel<false, L, V, true>), grid, block, lds, stream, a, fast);
-    else hipLaunchKernelGGL((route_kernel<false, L, V, false>), grid, block, lds, stream, a, fast);
+    if (a.bf16 && scores) hipLaunchKernelGGL((route_kernel<true, L, V, true>), grid, block, lds, stream, a, whole);
+    else if (a.bf16) hipLaunchKernelGGL((route_kernel<true, L, V, false>), grid, block, lds, stream, a, whole);
+    else if (scores) hipLaunchKernelGGL((route_kernel<false, L, V, true>), grid, block, lds, stream, a, whole);
+    else hipLaunchKernelGGL((route_kernel<false, L, V, false>), grid, block, lds, stream, a, whole);
     return hipGetLastError();
 }
 

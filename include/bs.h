@@ -499,8 +499,8 @@ typedef enum bs_score_kind {
  *   bias    [E] float or NULL: added to the scores for the choice only
  *   score   s_e of every expert as above
  *   The choice value of an expert is s_e + bias_e with a bias, and its logit
- *   without one (scores rise with their logits).  An expert whose logit is
- *   -inf is masked: it is never chosen.  With n_group > 1 the experts form
+ *   without one (scores rise with their logits).  An expert whose logit or
+ *   bias is -inf is masked: it is never chosen.  With n_group > 1 the experts form
  *   n_group groups of E / n_group consecutive ones; a group's score is the
  *   sum of the (up to) group_best (1 or 2) largest s_e + bias_e (s_e) of its
  *   unmasked experts, and only the topk_group best groups stay.  The k
@@ -511,7 +511,8 @@ typedef enum bs_score_kind {
  *           scale * s_e / sum of the chosen (for the sigmoid / (sum + 1e-20));
  *           0 where idx is -1.  A token with every logit -inf gets none.
  * Choices between values that differ are exact: they are made on the logits,
- * or on float64 scores.  A NaN logit ranks above every number and its weights
+ * or on scores in fp32 where their error cannot change the choice and in
+ * float64 where it could.  Weights are computed in fp32.  A NaN logit ranks above every number and its weights
  * (with softmax or renormalize: the token's) are NaN; +inf ranks first too,
  * and its softmax is NaN as the formula gives.
  *   1 <= E <= 1024, 1 <= k <= min(E, 32), E % n_group == 0,

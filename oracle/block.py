@@ -50,7 +50,7 @@ def route(logits, k, bias=None, kind=SOFTMAX, n_group=1, topk_group=1, group_bes
     w = np.zeros((T, k))
     size = E // n_group
     for t in range(T):
-        live = [e for e in range(E) if not np.isneginf(l[t, e])]
+        live = [e for e in range(E) if not (np.isneginf(l[t, e]) or np.isneginf(value[t, e]))]
         if n_group > 1:
             ranked = []
             for g in range(n_group):

@@ -160,3 +160,66 @@ def test_route_choices_next_to_one_another(E, G, kind, dtype):
         idx, w = bs.bs_moe_route(l.cuda(), k, bias=bias.cuda(), score=kind, **kw)
         assert np.array_equal(idx.cpu().numpy(), want_idx)
         _weights_close(w.cpu().double().numpy(), want_w)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("kind", [block.SOFTMAX, block.SIGMOID], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,best", [(16, 4, 2), (16, 8, 2), (12, 4, 1), (24, 24, 1), (40, 8, 2), (160, 8, 2), (360, 9, 2),
+                                      (513, 27, 2), (6, 2, 2)])
+def test_route_groups_of_any_size(E, G, best, kind, dtype):
+    """Groups that are no whole lanes: far apart, next to one another, tied."""
+    need_gpu()
+    T, k = 67, min(4, E // G * max(1, G // 2))
+    kw = dict(n_group=G, topk_group=max(1, G // 2), group_best=best)
+    for grid, biased in ((None, True), (2, True), (None, False), (2, False)):
+        l = _logits(T, E, dtype, seed=E + G, grid=grid)
+        bias = None
+        if biased:
+            level = np.where(np.arange(E) % 3 == 0, 0.5, 0.51)
+            bias = torch.from_numpy((level - block.scores(_f64(l), kind)[0]).astype(np.float32))
+        print(f"route groups E={E} G={G} kind={kind} {dtype} grid={grid} bias={biased}", flush=True)
+        want_idx, want_w = block.route(_f64(l), k, bias=None if bias is None else _f64(bias), kind=kind, **kw)
+        idx, w = bs.bs_moe_route(l.cuda(), k, bias=None if bias is None else bias.cuda(), score=kind, **kw)
+        assert np.array_equal(idx.cpu().numpy(), want_idx)
+        _weights_close(w.cpu().double().numpy(), want_w)
+
+
+@pytest.mark.parametrize("E,G", [(16, 1), (16, 4), (64, 8), (256, 1)])
+def test_route_bias_that_masks_experts(E, G):
+    """An expert whose bias is -inf is never chosen, even where too few are left."""
+    need_gpu()
+    l = _logits(19, E, torch.float32, seed=2)
+    bias = torch.zeros(E)
+    bias[:E - 3] = -float("inf")
+    for kind in (block.SOFTMAX, block.SIGMOID):
+        kw = dict(kind=kind, n_group=G, topk_group=max(1, G // 2), group_best=2)
+        want_idx, want_w = block.route(_f64(l), 6 if E > 16 else 4, bias=_f64(bias), **kw)
+        print(f"route masking bias E={E} G={G} kind={kind}", flush=True)
+        kw["score"] = kw.pop("kind")
+        idx, w = bs.bs_moe_route(l.cuda(), 6 if E > 16 else 4, bias=bias.cuda(), **kw)
+        assert (want_idx[:, 3:] == -1).all() and (want_idx[0, :3] >= E - 3).all()
+        assert np.array_equal(idx.cpu().numpy(), want_idx)
+        _weights_close(w.cpu().double().numpy(), want_w)
+
+
+@pytest.mark.parametrize("E,G", [(64, 1), (24, 24), (256, 8)])
+def test_route_tie_at_the_last_place_next_to_a_better_expert(E, G):
+    """The k-th and (k+1)-th by fp32 tie, and a third, better by less than fp32
+    tells, comes after them: ties that are real must not hide it."""
+    need_gpu()
+    T = 40
+    l = torch.full((T, E), -4.0)
+    l[:, :3] = torch.tensor([4.0, 3.0, 2.0])
+    bias = torch.zeros(E)
+    bias[E - 1] = 0.5 - 1.0 / (1.0 + float(np.exp(-0.25)))  # a score of 0.5, plus its rounding
+    for step in (0, 1, 2):
+        b = bias.clone()
+        for _ in range(step):
+            b[E - 1] = torch.nextafter(b[E - 1], torch.tensor(1.0))
+        l[:, 5] = l[:, 9] = 0.0
+        l[:, E - 1] = 0.25
+        kw = dict(n_group=G, topk_group=G, group_best=1)
+        print(f"route hidden tie E={E} G={G} step={step}", flush=True)
+        want_idx, _ = block.route(_f64(l), 4, bias=_f64(b), kind=block.SIGMOID, **kw)
+        idx, _ = bs.bs_moe_route(l.cuda(), 4, bias=b.cuda(), score=bs.BS_SCORE_SIGMOID, **kw)
+        assert np.array_equal(idx.cpu().numpy(), want_idx)
