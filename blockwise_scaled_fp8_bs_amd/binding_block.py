@@ -177,16 +177,16 @@ def bs_moe_plan(idx, E, align=128, M=None, stream=None):
         M = lib.bs_moe_plan_rows(T, k, E, align)
     if E < 1 or M < 0:
         raise ValueError(f"E={E} must be >= 1 and M={M} >= 0")
-    # one allocation: the four arrays, each 16-byte aligned, then the workspace
-    e4, n4, m4 = (E + 3) // 4 * 4, (T * k + 3) // 4 * 4, (M + 3) // 4 * 4
+    # one allocation: the workspace, then the four arrays
     nbytes = lib.bs_moe_plan_workspace_bytes(T, k, E)
-    buf = torch.empty(2 * e4 + n4 + m4 + nbytes // 4, dtype=torch.int32, device=idx.device)
-    at = buf.data_ptr()
-    _check(lib.bs_moe_plan(p_idx, T, k, E, align, M, at, at + 4 * e4, at + 8 * e4, at + 8 * e4 + 4 * n4,
-                           at + 8 * e4 + 4 * (n4 + m4) if nbytes else None, nbytes, _stream_of(idx, stream)),
-           "bs_moe_plan")
-    return MoEPlan(buf[:E], buf[e4:e4 + E], buf.as_strided((T, k), (k, 1), 2 * e4),
-                   buf[2 * e4 + n4:2 * e4 + n4 + M])
+    n, nw = T * k, nbytes // 4
+    buf = torch.empty(nw + 2 * E + n + M, dtype=torch.int32, device=idx.device)
+    base = buf.data_ptr()
+    at = base + nbytes
+    _check(lib.bs_moe_plan(p_idx, T, k, E, align, M, at, at + 4 * E, at + 8 * E, at + 8 * E + 4 * n,
+                           base if nbytes else None, nbytes, _stream_of(idx, stream)), "bs_moe_plan")
+    _, group_end, counts, slot_row, row_slot = buf.split_with_sizes([nw, E, E, n, M])
+    return MoEPlan(group_end, counts, slot_row.view(T, k), row_slot)
 
 
 def bs_moe_gather_quant_1x128(x, row_slot, k, w=None, y=None, q_row=None, s_row=None, q_col=None, s_col=None,

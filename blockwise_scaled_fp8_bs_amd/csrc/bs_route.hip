@@ -11,6 +11,12 @@
 // thousand) whose choice that leaves in doubt.  Equal keys go to the lowest
 // expert: a lane's experts are consecutive, so that is the lowest lane of the
 // ballot and its first maximum.
+//
+// Bound by the latency of a wave's chain of reductions, not by bytes: 256
+// experts in 8 groups with a bias, top 8: one token 6.5 us (an empty launch is
+// 3.8), 16384 tokens 20 us (17 MB would take 3.5) and 9 us back, of them about
+// 2 for the last wave with a token in doubt; without groups or bias the
+// choice is by the logits: 128000 tokens of 8 experts 3.8 us and 3.6 back.
 #include "bs_moe.h"
 #include "bs_device.h"
 
