@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr float kTinySum = 1e-20f;  // added to the sum of the chosen sigmoid scores
+constexpr float kUp = 18446744073709551616.0f;  // 2^64: scores may be far below 1e-20, and fp32 ends at 1e-38
 
 // ---- reductions over the L lanes of a token; every lane gets the result ----
 // Steps 1 and 2 are quad permutes; 4 and 8 mirror halves of a 16-lane row
@@ -117,6 +118,15 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
+
+// 2^64 sigmoid(d), and 1 - sigmoid(d) without its cancellation, in fp32: of
+// h = exp(-|d| / 2), whose square would vanish where the scaled one does not.
+__device__ __forceinline__ float sigmoid_up(float d, float& other) {
+    const float h = expf(-0.5f * fabsf(d)), hu = h * 4294967296.0f;
+    const float r = 1.0f / __builtin_fmaf(h, h, 1.0f);
+    other = d < 0.f ? r : h * h * r;
+    return d < 0.f ? hu * hu * r : kUp * r;
+}
 
 // exp(x) for the choice: the product's rounding makes it err by |x| units of
 // 2^-24 and the hardware exponential by 2 more, where what counts is the error
@@ -558,15 +568,16 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, bool whole
         if (r * L >= a.k) continue;
         if (mine_idx[r] >= 0) {
             const float d = row_lds[mine_idx[r]];
-            s[r] = a.sigmoid ? 1.0f / (1.0f + expf(-d)) : a.renorm ? expf(d - top) : expf(d - m) / z;
+            float other;
+            s[r] = a.sigmoid ? sigmoid_up(d, other) : a.renorm ? expf(d - top) : expf(d - m) / z;
         }
         sum += s[r];
     }
-    float f = a.scale;
+    float f = a.sigmoid ? a.scale * (1.f / kUp) : a.scale;
     if (a.renorm) {
         sum = seg_sum<L>(sum);
-        if (a.sigmoid) sum += kTinySum;
-        f /= sum;
+        if (a.sigmoid) sum += kTinySum * kUp;
+        f = a.scale / sum;
     }
     if (!real) return;
 #pragma unroll
@@ -581,6 +592,11 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, bool whole
 
 // Gradient of the logits.  The k contributions of a token are placed in an
 // LDS row, which the lanes then add to what they hold and write out whole.
+// With p_j the chosen experts' shares of their sum (renormalized weights over
+// scale) it takes g_j - sum p_i g_i, which vanishes for k = 1 and nearly so
+// for an expert with nearly all of the sum.  With g_0 that of the largest
+// share and rest = 1 - sum p_i (of the sigmoid's 1e-20; 0 for the softmax) it
+// is (g_j - g_0) - sum p_i (g_i - g_0) + rest g_0, where nothing cancels.
 template <bool BF16, int L, int V>
 __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a) {
     constexpr int TPB = kThreads / L;
@@ -629,21 +645,39 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a) {
                 g[r] = a.dw[t * a.k + j];
                 if (a.sigmoid) {
                     const float d = load_logit(a.logits, BF16, t * a.ld + x);
-                    s[r] = 1.f / (1.f + expf(-d));
-                    ns[r] = 1.f / (1.f + expf(d));  // 1 - s, without the cancellation
+                    s[r] = sigmoid_up(d, ns[r]);
                 }
             }
         }
-        dot += w[r] * g[r];
         ssum += s[r];
     }
+    float f = a.scale * (1.f / kUp), rest = 0.f;
+    if (a.sigmoid && a.renorm) {
+        const float sum = seg_sum<L>(ssum), total = sum + kTinySum * kUp;
+        f = a.scale / total;
+        rest = (total - sum) / total;  // 0 where the sum does not feel the 1e-20: over 2^-42
+    }
+    float g0 = 0.f;
+    if (a.renorm) {
+        uint64_t top = 0;  // the largest share with its g
+#pragma unroll
+        for (int r = 0; r < KR; ++r) {
+            const uint64_t x = ((uint64_t)__float_as_uint(fabsf(w[r])) << 32) | __float_as_uint(g[r]);
+            if (e[r] >= 0 && x > top) top = x;
+        }
+        top = seg_reduce<L>(top, [](uint64_t x, uint64_t y) { return x > y ? x : y; });
+        g0 = __uint_as_float((uint32_t)top);
+    }
+#pragma unroll
+    for (int r = 0; r < KR; ++r) {
+        g[r] = e[r] >= 0 ? g[r] - g0 : 0.f;
+        dot += w[r] * g[r];
+    }
     dot = seg_sum<L>(dot);
-    float f = a.scale;
-    if (a.sigmoid && a.renorm) f = a.scale / (seg_sum<L>(ssum) + kTinySum);
 #pragma unroll
     for (int r = 0; r < KR; ++r) {
         if (e[r] >= 0) {
-            const float d = a.renorm ? g[r] - dot : g[r];
+            const float d = a.renorm ? (g[r] - dot) + rest * g0 : g[r];
             s_row[tb][e[r]] = a.sigmoid ? f * d * s[r] * ns[r] : a.scale * w[r] * d;
         }
     }

@@ -223,3 +223,57 @@ def test_route_tie_at_the_last_place_next_to_a_better_expert(E, G):
         want_idx, _ = block.route(_f64(l), 4, bias=_f64(b), kind=block.SIGMOID, **kw)
         idx, _ = bs.bs_moe_route(l.cuda(), 4, bias=b.cuda(), score=bs.BS_SCORE_SIGMOID, **kw)
         assert np.array_equal(idx.cpu().numpy(), want_idx)
+
+
+@pytest.mark.parametrize("E", [8, 64, 256])
+def test_route_gradient_where_one_expert_has_all_the_weight(E):
+    """g_j - sum p_i g_i is 0 for k = 1 and tiny for an expert with nearly the
+    whole sum: no rounding of the terms may stand for it."""
+    need_gpu()
+    T = 33
+    rng = np.random.default_rng(E)
+    l = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32))
+    g = torch.from_numpy(rng.standard_normal((T, 3)).astype(np.float32))
+    for kind in (block.SOFTMAX, block.SIGMOID):
+        print(f"route gradient E={E} kind={kind} k=1", flush=True)
+        idx, w = bs.bs_moe_route(l.cuda(), 1, score=kind, scale=2.5)
+        d = bs.bs_moe_route_bwd(l.cuda(), idx, w, g[:, :1].contiguous().cuda(), score=kind, scale=2.5).cpu()
+        # the sigmoid's 1e-20 leaves scale g 1e-20 (1 - s) / s, s >= sigmoid(-6) = 2^-8.7
+        assert d.abs().max() <= 2.5 * 6 * 1e-20 * 2.0 ** 9
+    # softmax over the chosen: dl_j = scale p_j sum p_i (g_j - g_i), which does not cancel
+    l[:, 5] += 30.0
+    print(f"route gradient E={E} one expert dominates", flush=True)
+    idx, w = bs.bs_moe_route(l.cuda(), 3, scale=2.5)
+    d = bs.bs_moe_route_bwd(l.cuda(), idx, w, g.cuda(), scale=2.5).cpu().double().numpy()
+    for t in range(T):
+        e = idx[t].cpu().numpy()
+        p = np.exp(_f64(l)[t, e] - _f64(l)[t, e].max())
+        p /= p.sum()
+        gt = g[t].double().numpy()
+        diff = gt[:, None] - gt[None]
+        want, mag = 2.5 * p * (p * diff).sum(1), 2.5 * p * (p * np.abs(diff)).sum(1)
+        # expf of differences up to 36 (2^-24 of them each) and a few roundings; differences of g are exact to 2^-24
+        # of their terms, which two shares enter at most
+        mag += 2.5 * p * p.max() * np.abs(gt).max() * (p < 0.5) + 2.5 * p * (1 - p) * np.abs(gt).max()
+        assert (np.abs(d[t, e] - want) <= mag * 2.0 ** -17 + 1e-30).all()
+
+
+def test_route_gradient_of_scores_as_small_as_the_added_term():
+    """Sigmoid scores about 1e-20: the term added to their sum takes part."""
+    need_gpu()
+    l = torch.tensor([[-46.0, -47.0, -60.0, -50.0], [-44.0, -44.0, -70.0, -46.0], [-90.0, -91.0, -92.0, -93.0]])
+    g = torch.tensor([[1.0, -0.5], [2.0, 0.25], [0.5, 3.0]])
+    print("route gradient of tiny scores", flush=True)
+    idx, w = bs.bs_moe_route(l.cuda(), 2, score=block.SIGMOID, scale=2.0)
+    d = bs.bs_moe_route_bwd(l.cuda(), idx, w, g.cuda(), score=block.SIGMOID, scale=2.0).cpu().double().numpy()
+    want = block.route_bwd(_f64(l), idx.cpu().numpy(), g.numpy(), kind=block.SIGMOID, scale=2.0)
+    want_idx, want_w = block.route(_f64(l), 2, kind=block.SIGMOID, scale=2.0)
+    assert np.array_equal(idx.cpu().numpy(), want_idx)
+    _weights_close(w.cpu().double().numpy(), want_w)
+    # expf of numbers up to 93 and about 16 more roundings of terms as large as f (|g| + sum p |g|) s
+    s = block.scores(_f64(l), block.SIGMOID)
+    e = idx.cpu().numpy()
+    c = np.take_along_axis(s, e, 1)
+    mag = np.zeros_like(want)
+    np.put_along_axis(mag, e, 2.0 * c / (c.sum(1, keepdims=True) + 1e-20) * 2 * np.abs(g.numpy()).max(1, keepdims=True), 1)
+    assert (np.abs(d - want) <= mag * 2.0 ** -19 + 1e-37).all()
