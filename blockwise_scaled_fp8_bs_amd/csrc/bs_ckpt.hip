@@ -136,6 +136,24 @@ __device__ __forceinline__ void gate_grad(float a, float b, float dh, float& da,
          ((tie_distance(da) - kWindowDa) * fabsf(t) > kWindowDaT * fabsf(an)) & off_tie1(db);
 }
 
+// Each of them alone, by the same operations.
+__device__ __forceinline__ float gate_da(float a, float b, float dh, bool& ok) {
+    const float e = exp_neg(a);
+    const float s = __builtin_amdgcn_rcpf(1.0f + e);
+    const float an = a * (e * s);
+    const float t = 1.0f + an;
+    const float p1 = dh * b;
+    const float da = p1 * s * t, mag = fabsf(da);
+    ok = (a > -69.0f) & ((p1 == 0.0f) | ((mag >= kSafe) & (mag < __builtin_inff()))) &
+         ((tie_distance(da) - kWindowDa) * fabsf(t) > kWindowDaT * fabsf(an));
+    return da;
+}
+__device__ __forceinline__ float gate_db(float a, float dh, bool& ok) {
+    const float db = dh * (a * __builtin_amdgcn_rcpf(1.0f + exp_neg(a)));
+    ok = (a > -69.0f) & off_tie1(db);
+    return db;
+}
+
 // 1x128 codes of row i of a thread's block (columns 8 tc .. +7 of the tile)
 // to q, its scale where this lane is to store it (see quant_tile_rows).
 __device__ __forceinline__ void quant_row(const float* f, int i, __amdgpu_buffer_rsrc_t rq, int voff, int ld, int tc,
@@ -149,10 +167,17 @@ __device__ __forceinline__ void quant_row(const float* f, int i, __amdgpu_buffer
     if ((tc & 7) == i) my_scale = sc.s;
 }
 
-template <bool ROW, bool COL>
-__global__ __launch_bounds__(kThreads) void swiglu_ckpt_kernel(SwigluCkptArgs a) {
-    __shared__ float s_colmax[4][kTile];
-    __shared__ __attribute__((aligned(16))) uint8_t s_tr[COL ? kTile * kTile : 16];
+// ---- passes of few tiles ----
+// One workgroup does what a tile needs where there are tiles enough for the
+// chip.  Up to one a compute unit each is shared by two: the forward's
+// checkpoint codes and its h, the backward's da and its db, of which each
+// recomputes what both need.  Forward and backward at 1152 x 640 (45 tiles):
+// 10.1 and 12.9 us, whole 11.4 and 17.1; at 256 tiles 13.0 and 18.3, 14.8 and
+// 19.1; at 512 19.6 and 29.5, 21.4 and 28.3.
+enum Part { kFirst = 0, kSecond = 1, kBoth = 2 };
+
+template <bool ROW, bool COL, int PART>
+__device__ __forceinline__ void fwd_tile(const SwigluCkptArgs& a, float (*s_colmax)[kTile], uint8_t* s_tr) {
     const int t = threadIdx.x;
     const int tr = t >> 4, tc = t & 15;
     const int64_t col_tiles = a.C / kTile;
@@ -173,24 +198,29 @@ __global__ __launch_bounds__(kThreads) void swiglu_ckpt_kernel(SwigluCkptArgs a)
         float fa[8], fb[8], g[8];
         unpack8(ra.v[i], fa);
         unpack8(rb.v[i], fb);
+        if (PART != kFirst) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            bool ok;
-            g[j] = gate_h(fa[j], fb[j], ok);
-            m[i >> 2] = m[i >> 2] + m[i >> 2] + (ok ? 0u : 1u);  // one add with carry; element 0 ends in bit 31
+            for (int j = 0; j < 8; ++j) {
+                bool ok;
+                g[j] = gate_h(fa[j], fb[j], ok);
+                m[i >> 2] = m[i >> 2] + m[i >> 2] + (ok ? 0u : 1u);  // one add with carry; element 0 ends in bit 31
+            }
+            pin(m[i >> 2]);
         }
-        pin(m[i >> 2]);
-        quant_row(fa, i, ka, voff_k, (int)a.ld_ck, tc, sa);
-        quant_row(fb, i, kb, voff_k, (int)a.ld_ck, tc, sb);
-        pack_row(ph, i, g);
+        if (PART != kSecond) {
+            quant_row(fa, i, ka, voff_k, (int)a.ld_ck, tc, sa);
+            quant_row(fb, i, kb, voff_k, (int)a.ld_ck, tc, sb);
+        }
+        if (PART != kFirst) pack_row(ph, i, g);
         __builtin_amdgcn_sched_barrier(0);
     }
-    if (tc < 8) {  // lanes tc < 8 hold the scales of rows 8 tr + tc
+    if (PART != kSecond && tc < 8) {  // lanes tc < 8 hold the scales of rows 8 tr + tc
         const __amdgpu_buffer_rsrc_t za = rsrc(a.s_ck + (c0 / kTile) * a.ld_sck + r0, rows * 4);
         const __amdgpu_buffer_rsrc_t zb = rsrc(a.s_ck + ((a.C + c0) / kTile) * a.ld_sck + r0, rows * 4);
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sa), za, (8 * tr + tc) * 4, 0, 0);
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sb), zb, (8 * tr + tc) * 4, 0, 0);
     }
+    if (PART == kFirst) return;
     redo_marked(m[0], m[1], ph, [&](int e) {
         const int64_t r = r0 + 8 * tr + (e >> 3), c = c0 + 8 * tc + (e & 7);
         if (r >= a.R) return 0.f;  // rows past the end read as zeros, which are never marked
@@ -204,6 +234,15 @@ __global__ __launch_bounds__(kThreads) void swiglu_ckpt_kernel(SwigluCkptArgs a)
     if (COL)
         quant_tile_cols(tl, a.q_col + c0 * a.ld_qc + r0, a.ld_qc, a.s_col + (r0 / kTile) * a.ld_sc + c0, s_colmax,
                         s_tr, tr, tc, t >> 6);
+}
+
+template <bool ROW, bool COL, bool SPLIT>
+__global__ __launch_bounds__(kThreads) void swiglu_ckpt_kernel(SwigluCkptArgs a) {
+    __shared__ float s_colmax[4][kTile];
+    __shared__ __attribute__((aligned(16))) uint8_t s_tr[COL ? kTile * kTile : 16];
+    if (!SPLIT) fwd_tile<ROW, COL, kBoth>(a, s_colmax, s_tr);
+    else if (blockIdx.y == 0) fwd_tile<ROW, COL, kSecond>(a, s_colmax, s_tr);
+    else fwd_tile<ROW, COL, kFirst>(a, s_colmax, s_tr);
 }
 
 // Two e4m3 codes of a word (its low or high half) -> floats.
@@ -239,6 +278,66 @@ __device__ __forceinline__ void load_ck(const uint8_t* ck, int64_t ld, const flo
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         o.s[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, (8 * tr + i) * 4, 0, 0));
+}
+
+// One of da (kFirst) and db (kSecond) of a tile.
+template <bool ROW, bool COL, int PART>
+__device__ __forceinline__ void bwd_part(const SwigluBwdCkptArgs& a, float (*s_colmax)[kTile], uint8_t* s_tr) {
+    const int t = threadIdx.x;
+    const int tr = t >> 4, tc = t & 15;
+    const int64_t col_tiles = a.C / kTile;
+    const int64_t r0 = (blockIdx.x / col_tiles) * kTile, c0 = (blockIdx.x % col_tiles) * kTile;
+    const int64_t rows = (a.R - r0) < kTile ? (a.R - r0) : kTile;
+    RawCk ka, kb;
+    Raw rd;
+    const float* const sa = a.s_ck + (c0 / kTile) * a.ld_sck + r0;
+    const float* const sb = a.s_ck + ((a.C + c0) / kTile) * a.ld_sck + r0;
+    load_ck(a.ck + r0 * a.ld_ck + c0, a.ld_ck, sa, rows, tr, tc, ka);
+    if (PART == kFirst) load_ck(a.ck + r0 * a.ld_ck + a.C + c0, a.ld_ck, sb, rows, tr, tc, kb);
+    load_raw(a.dh, a.ld_dh, r0, c0, a.R, (8 * tr) * (int)(a.ld_dh * 2) + 16 * tc, rd);
+    Packed p;
+    uint32_t m[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float fa[8], fb[8], fd[8], g[8];
+        decode8(ka.q[i], ka.s[i], fa);
+        if (PART == kFirst) decode8(kb.q[i], kb.s[i], fb);
+        unpack8(rd.v[i], fd);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            bool ok;
+            g[j] = PART == kFirst ? gate_da(fa[j], fb[j], fd[j], ok) : gate_db(fa[j], fd[j], ok);
+            m[i >> 2] = m[i >> 2] + m[i >> 2] + (ok ? 0u : 1u);
+        }
+        pin(m[i >> 2]);
+        pack_row(p, i, g);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    redo_marked(m[0], m[1], p, [&](int e) {
+        const int rl = 8 * tr + (e >> 3);
+        const int64_t r = r0 + rl, c = c0 + 8 * tc + (e & 7);
+        if (r >= a.R) return 0.f;  // rows past the end read as zeros, which are never marked
+        const float2 g = swiglu_grad_bf16_f64(decode1(a.ck[r * a.ld_ck + c], sa[rl]),
+                                              decode1(a.ck[r * a.ld_ck + a.C + c], sb[rl]),
+                                              __uint_as_float((uint32_t)a.dh[r * a.ld_dh + c] << 16));
+        return PART == kFirst ? g.x : g.y;
+    });
+    const int64_t co = (PART == kFirst ? 0 : a.C) + c0;
+    TileRegs tl;
+    unpack_packed(p, tl);
+    if (ROW)
+        quant_tile_rows(tl, rows, a.q_row + r0 * a.ld_qr + co, a.ld_qr, a.s_row + (co / kTile) * a.ld_sr + r0, tr, tc);
+    if (COL)
+        quant_tile_cols(tl, a.q_col + co * a.ld_qc + r0, a.ld_qc, a.s_col + (r0 / kTile) * a.ld_sc + co, s_colmax,
+                        s_tr, tr, tc, t >> 6);
+}
+
+template <bool ROW, bool COL>
+__global__ __launch_bounds__(kThreads) void swiglu_bwd_ckpt_split_kernel(SwigluBwdCkptArgs a) {
+    __shared__ float s_colmax[4][kTile];
+    __shared__ __attribute__((aligned(16))) uint8_t s_tr[COL ? kTile * kTile : 16];
+    if (blockIdx.y == 0) bwd_part<ROW, COL, kFirst>(a, s_colmax, s_tr);
+    else bwd_part<ROW, COL, kSecond>(a, s_colmax, s_tr);
 }
 
 template <bool ROW, bool COL>
@@ -308,19 +407,40 @@ __global__ __launch_bounds__(kThreads, 4) void swiglu_bwd_ckpt_kernel(SwigluBwdC
 
 }  // namespace
 
+namespace {
+// Up to one tile for each of the 256 compute units: two workgroups a tile.
+bool split_tiles(const dim3& tiles) { return tiles.x <= 256; }
+}  // namespace
+
 hipError_t launch_swiglu_ckpt(const SwigluCkptArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)(((a.R + kTile - 1) / kTile) * (a.C / kTile))), block(kThreads);
-    if (a.q_row && a.q_col) hipLaunchKernelGGL((swiglu_ckpt_kernel<true, true>), grid, block, 0, stream, a);
-    else if (a.q_row) hipLaunchKernelGGL((swiglu_ckpt_kernel<true, false>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((swiglu_ckpt_kernel<false, true>), grid, block, 0, stream, a);
+    dim3 grid((unsigned)(((a.R + kTile - 1) / kTile) * (a.C / kTile)));
+    const dim3 block(kThreads);
+    if (split_tiles(grid)) {
+        grid.y = 2;
+        if (a.q_row && a.q_col) hipLaunchKernelGGL((swiglu_ckpt_kernel<true, true, true>), grid, block, 0, stream, a);
+        else if (a.q_row) hipLaunchKernelGGL((swiglu_ckpt_kernel<true, false, true>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((swiglu_ckpt_kernel<false, true, true>), grid, block, 0, stream, a);
+    } else {
+        if (a.q_row && a.q_col) hipLaunchKernelGGL((swiglu_ckpt_kernel<true, true, false>), grid, block, 0, stream, a);
+        else if (a.q_row) hipLaunchKernelGGL((swiglu_ckpt_kernel<true, false, false>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((swiglu_ckpt_kernel<false, true, false>), grid, block, 0, stream, a);
+    }
     return hipGetLastError();
 }
 
 hipError_t launch_swiglu_bwd_ckpt(const SwigluBwdCkptArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)(((a.R + kTile - 1) / kTile) * (a.C / kTile))), block(kThreads);
-    if (a.q_row && a.q_col) hipLaunchKernelGGL((swiglu_bwd_ckpt_kernel<true, true>), grid, block, 0, stream, a);
-    else if (a.q_row) hipLaunchKernelGGL((swiglu_bwd_ckpt_kernel<true, false>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((swiglu_bwd_ckpt_kernel<false, true>), grid, block, 0, stream, a);
+    dim3 grid((unsigned)(((a.R + kTile - 1) / kTile) * (a.C / kTile)));
+    const dim3 block(kThreads);
+    if (split_tiles(grid)) {
+        grid.y = 2;
+        if (a.q_row && a.q_col) hipLaunchKernelGGL((swiglu_bwd_ckpt_split_kernel<true, true>), grid, block, 0, stream, a);
+        else if (a.q_row) hipLaunchKernelGGL((swiglu_bwd_ckpt_split_kernel<true, false>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((swiglu_bwd_ckpt_split_kernel<false, true>), grid, block, 0, stream, a);
+    } else {
+        if (a.q_row && a.q_col) hipLaunchKernelGGL((swiglu_bwd_ckpt_kernel<true, true>), grid, block, 0, stream, a);
+        else if (a.q_row) hipLaunchKernelGGL((swiglu_bwd_ckpt_kernel<true, false>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((swiglu_bwd_ckpt_kernel<false, true>), grid, block, 0, stream, a);
+    }
     return hipGetLastError();
 }
 

@@ -82,3 +82,37 @@ def test_forward_equals_the_form_without_a_checkpoint():
     bs.bs_swiglu_quant_1x128_ckpt(a, b, ck, s_ck, **x)
     bs.bs_swiglu_quant_1x128(a, b, None, **y)
     assert all(torch.equal(x[n], y[n]) for n in x)
+
+
+def test_many_tiles_equal_few():
+    """288 tiles, one workgroup each, against the same rows 48 or 96 tiles at a time, each shared by two."""
+    need_gpu()
+    R, C = 2304, 2048
+    a, b = (t.cuda() for t in _inputs(R, C, seed=21))
+    dh = torch.randn((R, C), generator=torch.Generator().manual_seed(4)).mul_(0.01).to(torch.bfloat16).cuda()
+    new = lambda r, c: dict(q_row=torch.zeros((r, c), dtype=torch.uint8, device="cuda"), s_row=bs.empty_scales(c // 128, r, "cuda"))  # noqa: E731
+
+    def run(lo, hi, cols):
+        n = hi - lo
+        ck, s_ck, h, g = torch.zeros((n, 2 * C), dtype=torch.uint8, device="cuda"), bs.empty_scales(2 * C // 128, n, "cuda"), new(n, C), new(n, 2 * C)
+        if cols:
+            for d, c in ((h, C), (g, 2 * C)):
+                d.update(q_col=torch.zeros((c, n), dtype=torch.uint8, device="cuda"), s_col=bs.empty_scales(n // 128, c, "cuda"))
+        bs.bs_swiglu_quant_1x128_ckpt(a[lo:hi], b[lo:hi], ck, s_ck, **h)
+        bs.bs_swiglu_bwd_quant_1x128_ckpt(ck, s_ck, dh[lo:hi], **g)
+        return ck, s_ck, h, g
+
+    print("ckpt many tiles against few", flush=True)
+    ck, s_ck, h, g = run(0, R, True)
+    for lo in range(0, R, 384):
+        part = run(lo, lo + 384, False)
+        assert torch.equal(ck[lo:lo + 384], part[0]) and torch.equal(s_ck[:, lo:lo + 384], part[1][:, :384])
+        for whole, few in ((h, part[2]), (g, part[3])):
+            assert torch.equal(whole["q_row"][lo:lo + 384], few["q_row"])
+            assert torch.equal(whole["s_row"][:, lo:lo + 384], few["s_row"][:, :384])
+    for lo in range(0, R, 768):
+        part = run(lo, lo + 768, True)
+        for whole, few in ((h, part[2]), (g, part[3])):
+            assert torch.equal(whole["q_col"][:, lo:lo + 768], few["q_col"])
+            assert torch.equal(whole["s_col"][lo // 128:lo // 128 + 6, :whole["q_col"].shape[0]],
+                               few["s_col"][:, :whole["q_col"].shape[0]])
