@@ -7,14 +7,14 @@
 // chunks of 8 bf16 a thread, between its load and its last use; a workgroup
 // walks down consecutive rows with the parameters in registers and the next
 // row's loads under way.  At 16384 rows of 5120, fp32 parameters: r and
-// rstd_r from x and u 109 us (503 MB, 4.6 TB/s), h's codes along rows and
+// rstd_r from x and u 111 us (503 MB, 4.5 TB/s), h's codes along rows and
 // columns from r 61 us, the backward pass 210 us (1.01 GB, 4.8 TB/s); with
 // the parameters read again for every row it took 430 us.
 //
 // r is the float64 value of its formula rounded once to bf16, so that what
 // the later passes and the oracle compute from r starts from the same bits.
-// Sums of squares are exact enough for that in float64 (u) or redone in it
-// where fp32 overflows or vanishes (r): no finite bf16 row does.
+// Sums of squares are exact enough for that in float64 (u), and by fours in
+// fp32 for r, whose rstd errs by at most 2^-23.
 #include "bs_norm.h"
 #include "bs_tile.h"
 
@@ -120,8 +120,7 @@ __device__ __forceinline__ double rsqrt64(double v) {
 // fit beside them) the parameters and the row are read where they are used.
 template <int NC, int MAXT, bool HOLD>
 __global__ __launch_bounds__(MAXT) void resid_norm_kernel(ResidNormArgs a, int64_t per) {
-    __shared__ double s_sum[2][16];
-    __shared__ float s_sumf[2][16];
+    __shared__ double s_sum[3][16];  // of u; of r (without a norm of u the two in turn); of r again
     const int p = threadIdx.x, TP = blockDim.x;
     const int64_t lo = (int64_t)blockIdx.x * per, hi = lo + per < a.R ? lo + per : a.R;
     const int64_t bytes = a.D * 2, b_u = a.u != nullptr ? bytes : 0;
@@ -153,8 +152,7 @@ __global__ __launch_bounds__(MAXT) void resid_norm_kernel(ResidNormArgs a, int64
         in[i] = col[i] < a.D;
         if (HOLD) load_wp(i, wp_held[i]);
     }
-    if (p < 32) (&s_sum[0][0])[p] = 0.0;
-    if (p < 32) (&s_sumf[0][0])[p] = 0.f;
+    if (p < 48) (&s_sum[0][0])[p] = 0.0;
     __syncthreads();
 
     u32x4 cur_x[NC], cur_u[NC], next_x[NC], next_u[NC];
@@ -232,18 +230,21 @@ __global__ __launch_bounds__(MAXT) void resid_norm_kernel(ResidNormArgs a, int64
             if (post) __syncthreads();  // s_sum[0] is written again in the next row
             continue;
         }
-        // fp32 squares, in float64 where their sum leaves fp32's range
-        float fs = 0.f;
+        // squares four by four in fp32 (two roundings: rstd_r errs by half of
+        // them and its own, 2^-23), their sums in float64; all in float64
+        // where four leave fp32's range
+        double ss = 0.0;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             float f[8];
             unpack8(cur_x[i], f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) fs = __builtin_fmaf(f[j], f[j], fs);
+            for (int j = 0; j < 8; j += 4)
+                ss += (double)(__builtin_fmaf(f[j], f[j], f[j + 1] * f[j + 1]) +
+                               __builtin_fmaf(f[j + 2], f[j + 2], f[j + 3] * f[j + 3]));
         }
-        fs = block_sum<MAXT>(fs, s_sumf[post ? 0 : (int)(row & 1)]);
-        double ss = fs;
-        if (!(fs > 1e-25f && fs < 1e38f)) {
+        ss = block_sum<MAXT>(ss, s_sum[post ? 1 : (int)(row & 1)]);
+        if (!(ss > 1e-25 && ss < __builtin_inf())) {
             ss = 0.0;
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
@@ -252,7 +253,7 @@ __global__ __launch_bounds__(MAXT) void resid_norm_kernel(ResidNormArgs a, int64
 #pragma unroll
                 for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)f[j], (double)f[j], ss);
             }
-            ss = block_sum<MAXT>(ss, s_sum[1]);
+            ss = block_sum<MAXT>(ss, s_sum[2]);
         }
         const float rstd = (float)rsqrt64(__builtin_fma(ss, inv_d, eps));
         if (a.rstd_r != nullptr && p == 0) a.rstd_r[row] = rstd;
@@ -503,36 +504,65 @@ __global__ __launch_bounds__(MAXT) void resid_norm_bwd_kernel(ResidNormBwdArgs a
 }
 
 // Column sums of the workgroups' partial sums: block y = 0: dw_pre, 1:
-// dw_post, 2 + s: segment s of dgate.  8 threads of 4 columns by 32 parts of
-// the rows, the parts added in order.  Latency: 5 us for 256 sums of 5120.
-__global__ __launch_bounds__(256) void norm_sum_kernel(const float* p_pre, float* dw_pre, const float* p_post,
-                                                       float* dw_post, const float* p_gate, float* dgate, int64_t D,
-                                                       int64_t blocks, int64_t chunks) {
-    __shared__ double s_part[32][32];
+// dw_post, beyond: 4 segments of dgate each.  A column's rows are summed in
+// 128 parts (of dgate, which has few rows a segment, in 32), and the parts
+// added in order.  Latency: 4 us for 256 sums of 5120, 6 for 1024 of 1024 (12
+// in 32 parts), 9 for 2048 of 512 (22).
+constexpr int kSumParts = 128, kSumSegs = 4;
+__global__ __launch_bounds__(8 * kSumParts) void norm_sum_kernel(const float* p_pre, float* dw_pre,
+                                                                 const float* p_post, float* dw_post,
+                                                                 const float* p_gate, float* dgate, int64_t D,
+                                                                 int64_t blocks, int64_t chunks, int64_t segs) {
+    __shared__ double s_part[kSumParts][32];
     const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
     const int64_t c = (int64_t)blockIdx.x * 32 + 4 * x;
-    const int64_t kind = blockIdx.y;
-    const float* src = kind == 0 ? p_pre : kind == 1 ? p_post : p_gate + (kind - 2) * chunks * D;
-    float* dst = kind == 0 ? dw_pre : kind == 1 ? dw_post : dgate + (kind - 2) * D;
-    const int64_t n = kind < 2 ? blocks : chunks;
+    const bool gate = blockIdx.y >= 2;
+    const int64_t seg0 = gate ? (int64_t)(blockIdx.y - 2) * kSumSegs : 0;
+    float* const dst = blockIdx.y == 0 ? dw_pre : blockIdx.y == 1 ? dw_post : dgate;
     if (dst == nullptr) return;
     double s[4] = {0.0, 0.0, 0.0, 0.0};
-    if (c < D) {
-        for (int64_t i = y; i < n; i += 32) {
-            const float4 v = *reinterpret_cast<const float4*>(src + i * D + c);
-            s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+    // rows first, first + step, ... of src: four loads under way at a time, the last row in the place of those past it
+    const auto add = [&](const float* src, int64_t first, int64_t step, int64_t n) {
+        for (int64_t i = first; i < n; i += 4 * step) {
+            float4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t at = i + k * step < n ? i + k * step : n - 1;
+                v[k] = *reinterpret_cast<const float4*>(src + at * D + c);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (i + k * step >= n) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                s[0] += v[k].x; s[1] += v[k].y; s[2] += v[k].z; s[3] += v[k].w;
+            }
         }
+    };
+    if (c < D && gate) {
+        constexpr int kParts = kSumParts / kSumSegs;
+        const int64_t seg = seg0 + y / kParts;
+        if (seg < segs) add(p_gate + seg * chunks * D, y % kParts, kParts, chunks);
+    } else if (c < D) {
+        add(blockIdx.y == 0 ? p_pre : p_post, y, kSumParts, blocks);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) s_part[y][4 * x + j] = s[j];
     __syncthreads();
-    const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
-    if (threadIdx.x < 32 && col < D) {
+    const int q = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int64_t col = (int64_t)blockIdx.x * 32 + q;
+    if (!gate) {  // 32 columns by 32 groups of 4 parts first
+        const double four = ((s_part[4 * g][q] + s_part[4 * g + 1][q]) + s_part[4 * g + 2][q]) + s_part[4 * g + 3][q];
+        __syncthreads();
+        s_part[g][q] = four;
+        __syncthreads();
+    }
+    if (g < (gate ? kSumSegs : 1) && col < D && seg0 + g < (gate ? segs : 1)) {
         double v = 0.0;
-        for (int i = 0; i < 32; ++i) v += s_part[i][threadIdx.x];
-        dst[col] = (float)v;
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) v += s_part[32 * g + i][q];
+        dst[(seg0 + g) * D + col] = (float)v;
     }
 }
+static_assert(kSumParts / kSumSegs == 32 && kSumParts / 4 == 32, "32 sums are left for the last step");
 
 // Threads of a workgroup: the chunks of a row over NC, in whole waves.
 template <int NC>
@@ -561,7 +591,7 @@ void norm_bwd(const ResidNormBwdArgs& a, const NormBwdSplit& sp, float* pp, floa
 }  // namespace
 
 hipError_t launch_resid_norm(const ResidNormArgs& a, hipStream_t stream) {
-    // D = 5120 at 16384 rows, r alone: 109 us in three chunks, 118 in one, 129 in two (640 threads
+    // D = 5120 at 16384 rows, r alone: 111 us in three chunks, 118 in one, 129 in two (640 threads
     // are ten waves on four SIMDs, and a second workgroup of them does not fit beside the first)
     if (a.D <= 2048) norm_fwd<1, 256>(a, stream);
     else if (a.D <= 4096) norm_fwd<1, 512>(a, stream);
@@ -580,7 +610,11 @@ NormBwdSplit norm_bwd_split(int64_t R, int64_t D, int64_t rows_per_gate) {
     // workgroups for 8 waves on each of 256 CUs (at 16384 rows of 1024 columns:
     // 48 us, 62 with 2 waves; of 4096: 165 us, 175 with 16; more of them write
     // more partial sums); a chunk never crosses a gate's segment
-    const int64_t waves = (D + 511) / 512, blocks = 256 * (waves < 8 ? 8 / waves : 1);
+    const int64_t waves = (D + 511) / 512;
+    int64_t blocks = 256 * (waves < 8 ? 8 / waves : 1);
+    // where that leaves less than 4 rows each, half of them: 2048 rows of 512
+    // 14.6 us (19.4), 1000 of 1024 15.0 (17.6), 693 of 2048 15.1 (16.5)
+    if (R < 4 * blocks && waves < 8) blocks /= 2;
     const int64_t S = rows_per_gate, want = (R + blocks - 1) / blocks;
     NormBwdSplit sp{};
     sp.segs = R / S;
@@ -614,9 +648,9 @@ hipError_t launch_resid_norm_bwd(const ResidNormBwdArgs& a, hipStream_t stream) 
     else if (a.D <= 6144) norm_bwd<1, 768>(a, sp, pp, pq, pg, stream);
     else if (a.D <= 8192) norm_bwd<1, 1024>(a, sp, pp, pq, pg, stream);
     else norm_bwd<2, 1024>(a, sp, pp, pq, pg, stream);
-    const int64_t kinds = a.dgate != nullptr && sp.chunks > 1 ? 2 + sp.segs : 2;
-    hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((a.D + 31) / 32), (unsigned)kinds), dim3(256), 0, stream, pp,
-                       a.dw_pre, pq, a.dw_post, pg, a.dgate, a.D, sp.blocks, sp.chunks);
+    const int64_t kinds = a.dgate != nullptr && sp.chunks > 1 ? 2 + (sp.segs + kSumSegs - 1) / kSumSegs : 2;
+    hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((a.D + 31) / 32), (unsigned)kinds), dim3(8 * kSumParts), 0, stream, pp,
+                       a.dw_pre, pq, a.dw_post, pg, a.dgate, a.D, sp.blocks, sp.chunks, sp.segs);
     return hipGetLastError();
 }
 

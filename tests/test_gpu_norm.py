@@ -211,3 +211,11 @@ def test_extreme_rows_in_place_and_many_rows():
                           _np(c["w_post"]), _np(c["gate"]), ALPHA, float(np.float32(EPS)))
     _check_grads(runs[0], want, block.f64(bits16(r)), _np(c["w_pre"]), _np(c["dh"]), _np(c["dr"]), _np(c["u"]),
                  _np(c["w_post"]), _np(c["gate"]), float(np.float32(EPS)), R, D, 1)
+
+
+@pytest.mark.parametrize("case", [(6, 300, 256, 1, 1, torch.float32, ""), (9, 1000, 64, 1, 1, torch.bfloat16, ""),
+                                  (1, 5000, 72, 1, 1, torch.float32, ""), (2, 9000, 40, 1, 1, torch.float32, ""),
+                                  (1, 4100, 1040, 1, 0, torch.float32, "")], ids=str)
+def test_many_partial_sums(case):
+    """More workgroups than parts of a column sum, a number of gate segments that fills no whole workgroup."""
+    test_forward_and_backward(case)
