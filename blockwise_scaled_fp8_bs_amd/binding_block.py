@@ -5,7 +5,8 @@ the gated activation with an 8-bit checkpoint.
 Same conventions as ``binding``: argument marshalling only, tensors in the
 wrong layout raise ``ValueError`` instead of being copied.  Outputs that are
 not passed are allocated; workspaces are allocated per call, so that calls on
-different streams never share one.
+different streams never share one.  Both come from the pool of the stream that
+is passed, the current one without.
 """
 
 from collections import namedtuple
@@ -35,6 +36,16 @@ ResidNormGrads = namedtuple("ResidNormGrads", ["dx", "du", "dw_pre", "dw_post", 
 def _stream_of(t, stream):
     """Raw stream: the given one, or the current one of t's device."""
     return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+def _new(stream, shape, dtype, device, zero=False):
+    """A tensor from the pool of the stream that the kernel will run on, so
+    that its memory is not handed out again before the kernel is through."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
 
 
 def _fail_matrix(t, name, dtype, R, C):
@@ -130,9 +141,9 @@ def bs_moe_route(logits, k, bias=None, score=BS_SCORE_SOFTMAX, n_group=1, topk_g
     if k < 1:
         raise ValueError(f"k={k} must be >= 1")
     if idx is None:
-        idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+        idx = _new(stream, (T, k), torch.int32, logits.device)
     if w is None:
-        w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+        w = _new(stream, (T, k), torch.float32, logits.device)
     _check(_lib.load().bs_moe_route(
         p, _DT[logits.dtype], T, E, ld, None if bias is None else _flat(bias, "bias", torch.float32, (E,)), score, k,
         n_group, topk_group, group_best, int(renormalize), scale, _flat(idx, "idx", torch.int32, (T, k)),
@@ -146,7 +157,7 @@ def bs_moe_route_bwd(logits, idx, w, dw, score=BS_SCORE_SOFTMAX, renormalize=Tru
     (_, k), p_idx = _index(idx, "idx", 2)
     shape = (T, k)
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        out = _new(stream, (T, E), logits.dtype, logits.device)
     if idx.shape[0] != T:
         _fail_flat(idx, "idx", torch.int32, shape)
     _check(_lib.load().bs_moe_route_bwd(
@@ -180,7 +191,7 @@ def bs_moe_plan(idx, E, align=128, M=None, stream=None):
     # one allocation: the workspace, then the four arrays
     nbytes = lib.bs_moe_plan_workspace_bytes(T, k, E)
     n, nw = T * k, nbytes // 4
-    buf = torch.empty(nw + 2 * E + n + M, dtype=torch.int32, device=idx.device)
+    buf = _new(stream, nw + 2 * E + n + M, torch.int32, idx.device)
     base = buf.data_ptr()
     at = base + nbytes
     _check(lib.bs_moe_plan(p_idx, T, k, E, align, M, at, at + 4 * E, at + 8 * E, at + 8 * E + 4 * n,
@@ -211,7 +222,7 @@ def bs_moe_combine(y, slot_row, w=None, residual=None, out=None, stream=None):
     M, D = _first(y, "y", bf16)
     (T, k), p_row = _index(slot_row, "slot_row", 2)
     if out is None:
-        out = torch.empty((T, D), dtype=bf16, device=y.device)
+        out = _new(stream, (T, D), bf16, y.device)
     p, ld = _matrix(y, "y", bf16, M, D)
     _check(_lib.load().bs_moe_combine(
         p, M, D, ld, p_row, None if w is None else _flat(w, "w", torch.float32, (T, k)), T, k,
@@ -226,7 +237,7 @@ def bs_moe_combine_dw(dout, y, slot_row, dw=None, stream=None):
     M, D = _first(y, "y", bf16)
     (T, k), p_row = _index(slot_row, "slot_row", 2)
     if dw is None:
-        dw = torch.empty((T, k), dtype=torch.float32, device=y.device)
+        dw = _new(stream, (T, k), torch.float32, y.device)
     p_dout, ld_dout = _matrix(dout, "dout", bf16, T, D)
     p, ld = _matrix(y, "y", bf16, M, D)
     _check(_lib.load().bs_moe_combine_dw(p_dout, T, D, ld_dout, p, M, ld, p_row, k,
@@ -289,18 +300,18 @@ def bs_resid_norm_bwd(r, rstd_r, w_pre, dh, dr=None, u=None, rstd_u=None, w_post
     R, D = _first(some, "dr" if r is None else "r", bf16)
     p_pre, p_post, p_gate, ld_gate, per, dt = _norm_params(R, D, w_pre, w_post, gate)
     dev = some.device
-    dx = torch.empty((R, D), dtype=bf16, device=dev)
-    du = torch.empty((R, D), dtype=bf16, device=dev) if u is not None else None
-    make = torch.empty if R > 0 else torch.zeros     # no rows: the sums are zero
-    dw_pre = make(D, dtype=f32, device=dev) if w_pre is not None else None
-    dw_post = make(D, dtype=f32, device=dev) if w_post is not None else None
-    dgate = make((gate.shape[0], D), dtype=f32, device=dev) if gate is not None else None
+    dx = _new(stream, (R, D), bf16, dev)
+    du = _new(stream, (R, D), bf16, dev) if u is not None else None
+    none = R == 0     # no rows: the sums are zero
+    dw_pre = _new(stream, D, f32, dev, none) if w_pre is not None else None
+    dw_post = _new(stream, D, f32, dev, none) if w_post is not None else None
+    dgate = _new(stream, (gate.shape[0], D), f32, dev, none) if gate is not None else None
     grads = ResidNormGrads(dx, du, dw_pre, dw_post, dgate)
-    if R == 0:
+    if none:
         return grads
     lib = _lib.load()
     nbytes = lib.bs_resid_norm_bwd_workspace_bytes(R, D, per)
-    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    ws = _new(stream, max(nbytes, 16), torch.uint8, dev)
     p_r, ld_r = _optional(r, "r", bf16, R, D)
     p_u, ld_u = _optional(u, "u", bf16, R, D)
     p_dh, ld_dh = _optional(dh, "dh", bf16, R, D)
