@@ -29,6 +29,10 @@ tensor kept for the backward, as 1x128 codes (``checkpoint="fp8"``) or bf16.
             dxs = [da | db] [w1; w2]_e, d[w1; w2]_e = [da | db]^T xs;
             dx = sum dxs
 
+Nothing here waits for the device, so a forward, and a training step with its
+backward, can be captured into a HIP graph (no eager autograd graph of the same
+parameters may be alive while a backward is captured).
+
 Rows of the expert-ordered matrices past the last group (padding, and slots
 that were not routed) are computed by the elementwise kernels but read by no
 GEMM, and combined into no token.

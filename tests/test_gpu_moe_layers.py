@@ -339,6 +339,44 @@ def test_serving_pass_replays_from_a_graph():
             assert torch.equal(y.view(torch.int16), want.view(torch.int16))
 
 
+def test_training_step_replays_from_a_graph():
+    """Forward and backward of the block captured once; every replay equals the
+    eager step of a copy on the same inputs.  (The copy, so that no eager graph
+    of the captured leaves lives while the backward is captured.)"""
+    need_gpu()
+    import copy
+
+    ex = _example()
+    torch.manual_seed(2)
+    b = ex.MoEBlock(256, 128, 8, 2)
+    eager = copy.deepcopy(b)
+    new = lambda: torch.randn(300, 256, device="cuda").to(torch.bfloat16)  # noqa: E731
+    x, u, dy = new(), new(), new()
+
+    def step(m):
+        y = m(x, u)
+        return [y.detach()] + list(torch.autograd.grad(y, list(m.parameters()), dy))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(b)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(b)
+    for i in range(4):
+        print(f"training step replay {i}", flush=True)
+        for t in (x, u, dy):
+            t.copy_(new())
+        want = step(eager)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, w in zip(got, want):
+            assert torch.equal(a, w)
+        del want
+
+
 def test_layer_refusals():
     need_gpu()
     x = torch.zeros((4, 256), dtype=torch.bfloat16, device="cuda")
