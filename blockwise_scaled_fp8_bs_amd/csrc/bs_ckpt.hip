@@ -30,13 +30,32 @@ namespace {
 // index costs 128.)
 typedef uint32_t Packed __attribute__((ext_vector_type(32)));  // word 4 i + j / 2: row i, columns j, j + 1 (bf16)
 
-// Makes the mask a value at this point: left alone, the compiler keeps the 64
-// comparisons' lane masks until the end instead.
-__device__ __forceinline__ void pin(uint32_t& m) { asm volatile("" : "+v"(m)); }
+// Conditions on the wave's elements as 64-bit lane masks in scalar registers,
+// combined there: as per-lane booleans they come back through a select and a
+// compare when they are collected.  (The comparisons of the checks below run
+// with every lane of the wave active.)
+enum Cmp { kLess = 12, kGreaterEq = 11, kLessEq = 13, kNotEq = 14, kLessEqU = 37 };  // floats: or unordered
+template <Cmp C>
+__device__ __forceinline__ uint64_t lanes_where(float x, float y) {
+    return __builtin_amdgcn_fcmpf(x, y, C);
+}
+
+// Shifts the mask left by one with the lane's bit of `lanes` as its lowest.
+__device__ __forceinline__ void mark(uint32_t& m, uint64_t lanes) {
+    uint64_t carry;
+    asm("v_addc_co_u32_e64 %0, %1, %0, %0, %2" : "+v"(m), "=s"(carry) : "s"(lanes));
+}
+
+// Two values to a word of bf16 in one instruction.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
 
 __device__ __forceinline__ void pack_row(Packed& p, int i, const float* f) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) p[4 * i + j] = pack_bf16(f[2 * j], f[2 * j + 1]);
+    for (int j = 0; j < 4; ++j) p[4 * i + j] = pack2(f[2 * j], f[2 * j + 1]);
 }
 __device__ __forceinline__ void unpack_packed(const Packed& p, TileRegs& t) {
 #pragma unroll
@@ -93,8 +112,18 @@ __device__ __forceinline__ void set_pair(Raw& x, Raw& y, int e, float vx, float 
     }
 }
 
+// exp(-a) in fp32: 2^ph by the hardware, ph = -a log2(e) rounded, times 1 + d
+// with d = -a - ph ln 2, what that rounding left out (ln 2 in two parts).  As
+// exp_neg in five instructions instead of six; a below 2.3e38, where ph is finite.
+__device__ __forceinline__ float exp_minus(float a) {
+    const float ph = -a * kLog2e;
+    const float e = __builtin_amdgcn_exp2f(ph);
+    const float d = __builtin_fmaf(ph, 1.90465421e-9f, __builtin_fmaf(-ph, kLn2, -a));
+    return __builtin_fmaf(e, d, e);
+}
+
 // Windows, in fp32 ulps around a bf16 rounding tie, inside which a value is
-// redone.  With u = 2^-24: exp_neg errs by 3.2 u (the hardware exponential's
+// redone.  With u = 2^-24: exp_minus errs by 3.2 u (the hardware exponential's
 // 2 u and an fma), s = rcp(1 + e) by 3.2 + 1 + 2 u, e s by 7.2 u, products by
 // 1 u more each, so da by 10.2 u + 7.2 u |a (1 - s)| / |t|, db and h by 8.2 u;
 // k u of a value is less than k of its ulps.
@@ -104,54 +133,46 @@ constexpr uint32_t kWindow1 = 9;
 // those errors, and is the infinity that the float64 value rounds to.
 constexpr float kSafe = 7.9e-31f;  // 2^-100
 
-// |low half-word of r - 0x8000| > kWindow1
-__device__ __forceinline__ bool off_tie1(float r) {
-    return (uint16_t)(__float_as_uint(r) - (0x8000u - kWindow1)) > 2 * kWindow1;
+// |low half-word of r - 0x8000| <= kWindow1
+__device__ __forceinline__ uint64_t near_tie(float r) {
+    return __builtin_amdgcn_uicmp((uint32_t)(uint16_t)(__float_as_uint(r) - (0x8000u - kWindow1)), 2 * kWindow1, kLessEqU);
 }
 
-// h = silu(a) b in fp32 and whether its bf16 rounding is certain: as
-// swiglu_fast, with the window above.
-__device__ __forceinline__ float gate_h(float a, float b, bool& ok) {
-    const float silu = a * __builtin_amdgcn_rcpf(1.0f + exp_neg(a));
+// h = silu(a) b in fp32 and the lanes where its bf16 rounding is not certain:
+// as swiglu_fast, with the window above.
+__device__ __forceinline__ float gate_h(float a, float b, uint64_t& redo) {
+    const float silu = a * __builtin_amdgcn_rcpf(1.0f + exp_minus(a));
     const float r = silu * b;
-    ok = (a > -69.0f) & ((silu == 0.0f) | (fabsf(silu) >= kMinNormal)) & off_tie1(r);
+    redo = lanes_where<kLessEq>(a, -69.0f) |
+           (lanes_where<kNotEq>(silu, 0.0f) & lanes_where<kLess>(fabsf(silu), kMinNormal)) | near_tie(r);
     return r;
 }
 
-// da and db in fp32 and whether both roundings are certain.  |da| >= 2^-100
-// leaves no factor of it below the normal range (|t| < 1.1, s < 1), so one
-// comparison stands for theirs; a checkpointed a is 0 or over 2^-9 1e-12 / 448,
-// so silu(a) is 0 or normal.
-__device__ __forceinline__ void gate_grad(float a, float b, float dh, float& da, float& db, bool& ok) {
-    const float e = exp_neg(a);
+// da and db in fp32 and the lanes where one of their roundings is not certain.
+// |da| >= 2^-100 leaves no factor of it below the normal range (|t| < 1.1, s <
+// 1), so one comparison stands for theirs; a checkpointed a is 0 or over
+// 2^-9 1e-12 / 448, so silu(a) is 0 or normal.  Where exp_minus ends (2.3e38)
+// it is NaN, which da's checks find.
+template <bool DA, bool DB>
+__device__ __forceinline__ void gate_grad(float a, float b, float dh, float& da, float& db, uint64_t& redo) {
+    const float e = exp_minus(a);
     const float s = __builtin_amdgcn_rcpf(1.0f + e);
-    const float an = a * (e * s);  // a (1 - s)
-    const float t = 1.0f + an;
-    const float p1 = dh * b;
-    da = p1 * s * t;
-    const float silu = a * s;
-    db = dh * silu;
-    const float mag = fabsf(da);
-    ok = (a > -69.0f) & ((p1 == 0.0f) | ((mag >= kSafe) & (mag < __builtin_inff()))) &
-         ((tie_distance(da) - kWindowDa) * fabsf(t) > kWindowDaT * fabsf(an)) & off_tie1(db);
-}
-
-// Each of them alone, by the same operations.
-__device__ __forceinline__ float gate_da(float a, float b, float dh, bool& ok) {
-    const float e = exp_neg(a);
-    const float s = __builtin_amdgcn_rcpf(1.0f + e);
-    const float an = a * (e * s);
-    const float t = 1.0f + an;
-    const float p1 = dh * b;
-    const float da = p1 * s * t, mag = fabsf(da);
-    ok = (a > -69.0f) & ((p1 == 0.0f) | ((mag >= kSafe) & (mag < __builtin_inff()))) &
-         ((tie_distance(da) - kWindowDa) * fabsf(t) > kWindowDaT * fabsf(an));
-    return da;
-}
-__device__ __forceinline__ float gate_db(float a, float dh, bool& ok) {
-    const float db = dh * (a * __builtin_amdgcn_rcpf(1.0f + exp_neg(a)));
-    ok = (a > -69.0f) & off_tie1(db);
-    return db;
+    redo = lanes_where<kLessEq>(a, -69.0f);
+    if (!DA) redo |= lanes_where<kGreaterEq>(a, 2e38f);
+    if (DA) {
+        const float an = a * (e * s);  // a (1 - s)
+        const float t = 1.0f + an;
+        const float p1 = dh * b;
+        da = p1 * s * t;
+        const float mag = fabsf(da);
+        redo |= lanes_where<kNotEq>(p1, 0.0f) &
+                (lanes_where<kLess>(mag, kSafe) | lanes_where<kGreaterEq>(mag, __builtin_inff()));
+        redo |= lanes_where<kLessEq>((tie_distance(da) - kWindowDa) * fabsf(t), kWindowDaT * fabsf(an));
+    }
+    if (DB) {
+        db = dh * (a * s);
+        redo |= near_tie(db);
+    }
 }
 
 // 1x128 codes of row i of a thread's block (columns 8 tc .. +7 of the tile)
@@ -201,11 +222,10 @@ __device__ __forceinline__ void fwd_tile(const SwigluCkptArgs& a, float (*s_colm
         if (PART != kFirst) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                bool ok;
-                g[j] = gate_h(fa[j], fb[j], ok);
-                m[i >> 2] = m[i >> 2] + m[i >> 2] + (ok ? 0u : 1u);  // one add with carry; element 0 ends in bit 31
+                uint64_t redo;
+                g[j] = gate_h(fa[j], fb[j], redo);
+                mark(m[i >> 2], redo);  // element 0 ends in bit 31
             }
-            pin(m[i >> 2]);
         }
         if (PART != kSecond) {
             quant_row(fa, i, ka, voff_k, (int)a.ld_ck, tc, sa);
@@ -305,11 +325,12 @@ __device__ __forceinline__ void bwd_part(const SwigluBwdCkptArgs& a, float (*s_c
         unpack8(rd.v[i], fd);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            bool ok;
-            g[j] = PART == kFirst ? gate_da(fa[j], fb[j], fd[j], ok) : gate_db(fa[j], fd[j], ok);
-            m[i >> 2] = m[i >> 2] + m[i >> 2] + (ok ? 0u : 1u);
+            uint64_t redo;
+            float other;
+            if (PART == kFirst) gate_grad<true, false>(fa[j], fb[j], fd[j], g[j], other, redo);
+            else gate_grad<false, true>(fa[j], 0.f, fd[j], other, g[j], redo);
+            mark(m[i >> 2], redo);
         }
-        pin(m[i >> 2]);
         pack_row(p, i, g);
         __builtin_amdgcn_sched_barrier(0);
     }
@@ -366,19 +387,13 @@ __global__ __launch_bounds__(kThreads, 4) void swiglu_bwd_ckpt_kernel(SwigluBwdC
         unpack8(rd.v[i], fd);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            bool ok;
-            gate_grad(fa[j], fb[j], fd[j], ga[j], gb[j], ok);
-            m[i >> 2] = m[i >> 2] + m[i >> 2] + (ok ? 0u : 1u);  // one add with carry; element 0 ends in bit 31
-            if (j == 3) {
-                pin(m[i >> 2]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            uint64_t redo;
+            gate_grad<true, true>(fa[j], fb[j], fd[j], ga[j], gb[j], redo);
+            mark(m[i >> 2], redo);  // element 0 ends in bit 31
+            if (j == 3) __builtin_amdgcn_sched_barrier(0);
         }
-        pin(m[i >> 2]);
-        pd[0].v[i] = make_uint4(pack_bf16(ga[0], ga[1]), pack_bf16(ga[2], ga[3]), pack_bf16(ga[4], ga[5]),
-                                pack_bf16(ga[6], ga[7]));
-        pd[1].v[i] = make_uint4(pack_bf16(gb[0], gb[1]), pack_bf16(gb[2], gb[3]), pack_bf16(gb[4], gb[5]),
-                                pack_bf16(gb[6], gb[7]));
+        pd[0].v[i] = make_uint4(pack2(ga[0], ga[1]), pack2(ga[2], ga[3]), pack2(ga[4], ga[5]), pack2(ga[6], ga[7]));
+        pd[1].v[i] = make_uint4(pack2(gb[0], gb[1]), pack2(gb[2], gb[3]), pack2(gb[4], gb[5]), pack2(gb[6], gb[7]));
         __builtin_amdgcn_sched_barrier(0);
     }
     while ((m[0] | m[1]) != 0) {

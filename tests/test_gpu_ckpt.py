@@ -116,3 +116,33 @@ def test_many_tiles_equal_few():
             assert torch.equal(whole["q_col"][:, lo:lo + 768], few["q_col"])
             assert torch.equal(whole["s_col"][lo // 128:lo // 128 + 6, :whole["q_col"].shape[0]],
                                few["s_col"][:, :whole["q_col"].shape[0]])
+
+
+@pytest.mark.parametrize("C", [128, 33 * 1024])
+def test_gate_values_near_the_largest_bf16(C):
+    """a from 1e38 to the largest bf16, where the fp32 exponential's exponent overflows, and their negatives: both
+    outputs against the float64 formula, with few tiles and (C = 33 * 1024, 264 of them) with many."""
+    need_gpu()
+    R = 128
+    big = np.array([1e38, 2.3e38, 2.4e38, 3.3895e38], dtype=np.float32)
+    a = torch.from_numpy(np.tile(np.concatenate([big, -big]), R * C // 8).reshape(R, C)).to(torch.bfloat16)
+    b, dh = inputs_like(a, 1e-20, 5), inputs_like(a, 1e-20, 6)
+    ck, s_ck = torch.empty((R, 2 * C), dtype=torch.uint8, device="cuda"), bs.empty_scales(2 * C // 128, R, "cuda")
+    q, s = torch.empty((R, C), dtype=torch.uint8, device="cuda"), bs.empty_scales(C // 128, R, "cuda")
+    print(f"ckpt large gates C={C}", flush=True)
+    bs.bs_swiglu_quant_1x128_ckpt(a.cuda(), b.cuda(), ck, s_ck, q_row=q, s_row=s)
+    hr, hs = quant.quant_1x128_rowwise(swiglu.swiglu(bits16(a), bits16(b)))
+    assert np.array_equal(u8(q), hr) and np.array_equal(f32bits(s)[:, :R], hs.T.copy().view(np.uint32))
+    kr, ks = quant.quant_1x128_rowwise(np.concatenate([bits16(a), bits16(b)], 1))
+    assert np.array_equal(u8(ck), kr)
+    kept = block.dequant_rows(kr, ks)
+    with np.errstate(over="ignore"):
+        want = swiglu.round_to_bf16(np.concatenate(block.swiglu_grad(kept[:, :C], kept[:, C:], block.f64(bits16(dh))), 1))
+    q, s = torch.empty((R, 2 * C), dtype=torch.uint8, device="cuda"), bs.empty_scales(2 * C // 128, R, "cuda")
+    bs.bs_swiglu_bwd_quant_1x128_ckpt(ck, s_ck, dh.cuda(), q_row=q, s_row=s)
+    qr, sr = quant.quant_1x128_rowwise(want)
+    assert np.array_equal(f32bits(s)[:, :R], sr.T.copy().view(np.uint32)) and np.array_equal(u8(q), qr)
+
+
+def inputs_like(t, sigma, seed):
+    return (torch.randn(t.shape, generator=torch.Generator().manual_seed(seed)) * sigma).to(torch.bfloat16)
