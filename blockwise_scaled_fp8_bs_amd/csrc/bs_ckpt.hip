@@ -9,11 +9,11 @@
 // result lies near a bf16 rounding tie, so h, da and db are the float64
 // values of their formulas rounded once.
 //
-// At 16384 x 8192 the forward takes 225 us in a step (1.10 GB, 4.9 TB/s: HBM;
-// its vector instructions would take 183), the backward 295 (3.7 TB/s; 314
-// with a wave less on each SIMD): 72 vector instructions an element, 255 us
-// at 2.2 GHz, of them 26 the two quantizations of da and of db, about 20 the
-// gradient and 12 the proof that its rounding is certain.
+// At 16384 x 8192 the forward takes 225 us in a step (1.10 GB, 4.9 TB/s: HBM),
+// the backward 279 (3.9 TB/s; 314 with a wave less on each SIMD): 67 vector
+// instructions an element, 238 us at 2.2 GHz, of them 26 the two quantizations
+// of da and of db, about 19 the gradient and 9 the proof that its rounding is
+// certain.
 #include "bs_norm.h"
 #include "bs_tile.h"
 
