@@ -160,11 +160,15 @@ constexpr int kGatherSpan = 4;
 // ---- gather fused with the 1x128 quantizer ----
 // Row r of the result is row row_slot[r] / k of x (times w[row_slot[r]]), zero
 // where the slot is negative.  As the quantizer's one-workgroup-per-tile form,
-// with the tile's rows taken from wherever their tokens lie.  Bound by HBM and
-// the caches: 128000 slots of 5120 in rows and columns 530 us, 512 weighted
-// (every slot's row read, 1.3 GB, and 1.3 GB of codes: 5.1 TB/s, what the
-// quantizer reaches on rows in order).
-template <bool ROW, bool COL, bool W>
+// with the tile's rows taken from wherever their tokens lie.  Bound by HBM: at
+// 128000 slots of 64000 tokens of 5120 in rows and columns 455 us (0.66 GB read
+// once, 1.36 GB written: 4.4 TB/s), 472 weighted, 306 in rows alone; with the
+// blocks of rows outermost, so that every slot's row comes from HBM, 522, 525
+// and 367.  One slot a token the other way: 526, and 542.
+// NEAR: x within 2 GiB, its rows addressed by 32-bit offsets into one buffer
+// (absent rows past its end, where loads give zeros): registers for four waves
+// on a SIMD instead of three.
+template <bool ROW, bool COL, bool W, bool NEAR>
 __global__ __launch_bounds__(kThreads) void moe_gather_quant_kernel(GatherArgs a, int32_t span) {
     __shared__ float s_colmax[4][kTile];
     __shared__ __attribute__((aligned(16))) uint8_t s_tr[COL ? kTile * kTile : 16];
@@ -172,24 +176,34 @@ __global__ __launch_bounds__(kThreads) void moe_gather_quant_kernel(GatherArgs a
     const int t = threadIdx.x;
     const int tr = t >> 4, tc = t & 15;
     const int wave = t >> 6;
-    const int col_tiles = (int)(a.D / kTile), strips = (col_tiles + span - 1) / span;
-    const int64_t r0 = (int64_t)(blockIdx.x / (unsigned)strips) * kTile;
-    const int first = (int)(blockIdx.x % (unsigned)strips) * span;
+    const int col_tiles = (int)(a.D / kTile);
+    // with several slots a token all row blocks of one strip of columns before
+    // the next strip: its rows are read again, by other experts' blocks, while
+    // the strip is still in the last-level cache
+    const unsigned blocks = (unsigned)((a.M + kTile - 1) / kTile), strips = (unsigned)((col_tiles + span - 1) / span);
+    const unsigned rb = a.k > 1 ? blockIdx.x % blocks : blockIdx.x / strips;
+    const unsigned strip = a.k > 1 ? blockIdx.x / blocks : blockIdx.x % strips;
+    const int64_t r0 = (int64_t)rb * kTile;
+    const int first = (int)strip * span;
     const int last = first + span < col_tiles ? first + span : col_tiles;
     const int64_t rows = (a.M - r0) < kTile ? (a.M - r0) : kTile;
     const int64_t n = a.T * a.k;
 
+    const __amdgpu_buffer_rsrc_t rx = rsrc(a.x, NEAR ? a.T * a.ld_x * 2 : 0);
+    uint32_t off[8];
     const uint16_t* src[8];
     float w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t r = r0 + 8 * tr + i;
         const int32_t slot = r < a.M ? a.row_slot[r] : -1;
-        src[i] = nullptr;
+        if (NEAR) off[i] = 0x80000000u;
+        else src[i] = nullptr;
         if (W) w[i] = 0.f;
         if (slot >= 0 && slot < n) {
             const uint32_t tok = a.k_mul ? __umulhi((uint32_t)slot, a.k_mul) >> a.k_shift : (uint32_t)slot;
-            src[i] = a.x + (int64_t)tok * a.ld_x + 8 * tc;
+            if (NEAR) off[i] = tok * (uint32_t)(a.ld_x * 2) + 16 * tc;
+            else src[i] = a.x + (int64_t)tok * a.ld_x + 8 * tc;
             if (W) w[i] = a.w[slot];
         }
     }
@@ -197,8 +211,15 @@ __global__ __launch_bounds__(kThreads) void moe_gather_quant_kernel(GatherArgs a
         const int64_t c0 = (int64_t)ct * kTile;
         Raw raw;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            raw.v[i] = src[i] != nullptr ? *reinterpret_cast<const uint4*>(src[i] + c0) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 8; ++i) {
+            if (NEAR) {
+                const u32x4 v =
+                    __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)off[i], (int)(c0 * 2), 0));
+                raw.v[i] = make_uint4(v[0], v[1], v[2], v[3]);
+            } else {
+                raw.v[i] = src[i] != nullptr ? *reinterpret_cast<const uint4*>(src[i] + c0) : make_uint4(0, 0, 0, 0);
+            }
+        }
         TileRegs tl;
         unpack_tile(raw, tl);
         if (W) {
@@ -336,19 +357,24 @@ hipError_t launch_plan(const PlanArgs& a, hipStream_t stream) {
 hipError_t launch_gather(const GatherArgs& a, hipStream_t stream) {
     const int64_t blocks = (a.M + kTile - 1) / kTile, tiles = a.D / kTile;
     // several column tiles per workgroup share one reading of the row list (at
-    // 1007 x 40 tiles: 522 us with 4, 538 with 1, 540 with 20) where that still
-    // leaves a few workgroups for every place on the GPU
+    // 1007 x 40 tiles: 455 us with 4, 500 with 1, 457 with 2, 476 with 8) where
+    // that still leaves a few workgroups for every place on the GPU
     const int span = blocks * tiles >= 4 * kGatherSpan * 1024 ? kGatherSpan : 1;
     const dim3 grid((unsigned)(blocks * ((tiles + span - 1) / span))), block(kThreads);
     const bool row = a.q_row != nullptr, col = a.q_col != nullptr;
-#define BS_GATHER(R, C)                                                                                          \
-    if (a.w != nullptr) hipLaunchKernelGGL((moe_gather_quant_kernel<R, C, true>), grid, block, 0, stream, a, span); \
-    else hipLaunchKernelGGL((moe_gather_quant_kernel<R, C, false>), grid, block, 0, stream, a, span);
+    const bool near = a.T * a.ld_x * 2 < (int64_t)0x7fffffff;
+#define BS_GATHER_W(R, C, W)                                                                                        \
+    if (near) hipLaunchKernelGGL((moe_gather_quant_kernel<R, C, W, true>), grid, block, 0, stream, a, span);        \
+    else hipLaunchKernelGGL((moe_gather_quant_kernel<R, C, W, false>), grid, block, 0, stream, a, span);
+#define BS_GATHER(R, C)                             \
+    if (a.w != nullptr) { BS_GATHER_W(R, C, true) } \
+    else { BS_GATHER_W(R, C, false) }
     if (row && col) { BS_GATHER(true, true) }
     else if (row) { BS_GATHER(true, false) }
     else if (col) { BS_GATHER(false, true) }
     else { BS_GATHER(false, false) }
 #undef BS_GATHER
+#undef BS_GATHER_W
     return hipGetLastError();
 }
 

@@ -218,3 +218,28 @@ def test_on_a_side_stream_and_in_a_graph():
         for n, (a, b) in enumerate(zip(outs, ref)):
             assert torch.equal(a, b), (r, n)
     graph.reset()
+
+
+def test_gather_from_rows_more_than_2_gib_apart():
+    """Row strides that put the last rows past 32-bit offsets, against the same rows side by side."""
+    need_gpu()
+    T, D, k, ld = 300, 256, 2, 2 ** 22 - 64
+    big = torch.empty(((T - 1) * ld + D,), dtype=torch.bfloat16, device="cuda")
+    x = big.as_strided((T, D), (ld, 1))
+    x.copy_(inputs.bf16_normal((T, D), 1.0, 1))
+    g = torch.Generator().manual_seed(2)
+    idx = torch.randint(0, 4, (T, k), generator=g).to(torch.int32).cuda()
+    w = torch.rand((T, k), generator=g).cuda()
+    p = bs.bs_moe_plan(idx, 4)
+    M = p.row_slot.shape[0]
+    got = []
+    for src in (x, x.contiguous()):
+        for weight in (None, w):
+            print(f"gather stride {src.stride(0)} weighted {weight is not None}", flush=True)
+            o = dict(y=torch.empty((M, D), dtype=torch.bfloat16, device="cuda"), q_row=torch.empty((M, D), dtype=torch.uint8, device="cuda"),
+                     s_row=bs.empty_scales(D // 128, M, "cuda"), q_col=torch.empty((D, M), dtype=torch.uint8, device="cuda"),
+                     s_col=bs.empty_scales(M // 128, D, "cuda"))
+            bs.bs_moe_gather_quant_1x128(src, p.row_slot, k, w=weight, **o)
+            got.append([t[:, :M] if n == "s_row" else t[:, :D] if n == "s_col" else t for n, t in o.items()])
+    for a, b in zip(got[:2], got[2:]):
+        assert all(torch.equal(s.contiguous().view(torch.uint8), t.contiguous().view(torch.uint8)) for s, t in zip(a, b))
