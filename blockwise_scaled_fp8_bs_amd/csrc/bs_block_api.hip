@@ -133,7 +133,7 @@ bs_status bs_moe_route_bwd(const void* logits, bs_dtype dtype, int64_t T, int64_
 
 int64_t bs_moe_plan_rows(int64_t T, int64_t k, int64_t E, int64_t align) {
     if (T < 0 || k < 1 || k > bs::kMaxTopK || E < 1 || E > bs::kMaxExperts || align < 1 || T > kMaxI32 / k ||
-        align > kMaxI32)
+        align > bs::kMaxAlign)
         return 0;
     const int64_t n = T * k, groups = n < E ? n : E;
     return (n + groups * (align - 1)) / align * align;
@@ -153,7 +153,7 @@ bs_status bs_moe_plan(const int32_t* idx, int64_t T, int64_t k, int64_t E, int64
     REQUIRE(E >= 1 && E <= bs::kMaxExperts, BS_ERR_SHAPE, "E=%lld must be in [1, 1024]", (ll)E);
     REQUIRE(k >= 1 && k <= bs::kMaxTopK, BS_ERR_SHAPE, "k=%lld must be in [1, 32]", (ll)k);
     REQUIRE(T >= 0 && T <= kMaxI32 / k, BS_ERR_SHAPE, "T=%lld must be >= 0 with T * k < 2^31", (ll)T);
-    REQUIRE(align >= 1 && align <= kMaxI32, BS_ERR_SHAPE, "align=%lld must be >= 1", (ll)align);
+    REQUIRE(align >= 1 && align <= bs::kMaxAlign, BS_ERR_SHAPE, "align=%lld must be in [1, 65536]", (ll)align);
     const int64_t need = bs_moe_plan_rows(T, k, E, align);
     REQUIRE(M >= need && M <= kMaxI32, BS_ERR_SHAPE,
             "M=%lld must be >= %lld (every group padded to %lld, whatever the routing) and < 2^31", (ll)M, (ll)need,

@@ -10,6 +10,7 @@ namespace bs {
 
 constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxTopK = 32;
+constexpr int64_t kMaxAlign = 65536;  // rows that a group is padded to a multiple of
 
 struct RouteArgs {
     const void* logits;  // [T, ld] fp32 or bf16

@@ -20,6 +20,11 @@ namespace {
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWaves = kPlanThreads / 64;
 
+// Rows of a group; unsigned, since the sum may pass 2^31 where its result does not.
+__device__ __forceinline__ int32_t padded(int32_t slots, int32_t align) {
+    return (int32_t)(((uint32_t)slots + (uint32_t)align - 1u) / (uint32_t)align * (uint32_t)align);
+}
+
 __global__ __launch_bounds__(kPlanThreads) void plan_hist_kernel(PlanArgs a) {
     __shared__ int32_t cnt[kMaxExperts];
     for (int e = threadIdx.x; e < a.E; e += kPlanThreads) cnt[e] = 0;
@@ -88,7 +93,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
         int32_t own = 0;
         for (int i = 0; i < per; ++i) {
             const int e = lane * per + i;
-            if (e < E) own += (tot[e] + a.align - 1) / a.align * a.align;
+            if (e < E) own += padded(tot[e], a.align);
         }
         int32_t upto = own;
 #pragma unroll
@@ -101,7 +106,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
             const int e = lane * per + i;
             if (e < E) {
                 start[e] = at;
-                at += (tot[e] + a.align - 1) / a.align * a.align;
+                at += padded(tot[e], a.align);
                 if (blockIdx.x == 0) {
                     a.group_end[e] = at;
                     a.counts[e] = tot[e];
@@ -147,7 +152,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
     // rows that no slot takes: the padding of this block's share of the groups, and of the end
     for (int e = blockIdx.x + wave * a.blocks; e < E; e += a.blocks * kPlanWaves) {
         const int32_t from = start[e] + tot[e];
-        const int32_t to = start[e] + (tot[e] + a.align - 1) / a.align * a.align;
+        const int32_t to = start[e] + padded(tot[e], a.align);
         for (int32_t r = from + lane; r < to; r += 64)
             if (r < a.M) a.row_slot[r] = -1;
     }

@@ -554,7 +554,7 @@ bs_status bs_moe_route_bwd(const void* logits, bs_dtype dtype, int64_t T, int64_
  *   workspace  bs_moe_plan_workspace_bytes(T, k, E) bytes of DEVICE memory,
  *              16-byte aligned (NULL when that is 0)
  * Everything stays on the device; the result does not depend on any order of
- * execution.  T * k and M < 2^31, 1 <= E <= 1024, 1 <= k <= 32, align >= 1.
+ * execution.  T * k and M < 2^31, 1 <= E <= 1024, 1 <= k <= 32, 1 <= align <= 65536.
  */
 bs_status bs_moe_plan(const int32_t* idx, int64_t T, int64_t k, int64_t E, int64_t align, int64_t M,
                       int32_t* group_end, int32_t* counts, int32_t* slot_row, int32_t* row_slot, void* workspace,

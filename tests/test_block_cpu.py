@@ -297,3 +297,9 @@ def test_loader_knows_the_float_arguments():
     assert ctypes.c_float in _lib.SIGNATURES["bs_moe_route"][1]
     assert _lib.SIGNATURES["bs_resid_norm"][1].count(ctypes.c_float) == 2
     assert _lib.SIGNATURES["bs_resid_norm_bwd"][1].count(ctypes.c_float) == 1
+
+
+@pytest.mark.parametrize("align", [65537, 2 ** 31 - 1])
+def test_plan_refuses_alignments_whose_sums_could_overflow(lib, align):
+    call(lib, "bs_moe_plan", PLAN, dict(align=align, M=2 ** 31 - 1), SHAPE, "align")
+    assert lib.bs_moe_plan_rows(64, 2, 8, align) == 0

@@ -391,6 +391,9 @@ def test_layer_refusals():
         args.update(kw)
         with pytest.raises(ValueError, match=match):
             bs.float8_blockwise_moe_ffn(**args)
+    for wrong in (bs.bs_moe_plan(idx, 2, align=1), bs.bs_moe_plan(idx, 3), bs.bs_moe_plan(idx[:3], 2)):
+        with pytest.raises(ValueError, match="the plan is for"):
+            bs.float8_blockwise_moe_ffn(x, idx, w, w12, wo, plan=wrong)
     plan = bs.bs_moe_plan(idx, 2)
     with pytest.raises(ValueError, match="slots"):
         bs.moe_dispatch(x[:3], plan)
