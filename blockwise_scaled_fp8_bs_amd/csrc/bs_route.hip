@@ -12,10 +12,11 @@
 // expert: a lane's experts are consecutive, so that is the lowest lane of the
 // ballot and its first maximum.
 //
-// Bound by the latency of a wave's chain of reductions, not by bytes: 256
-// experts in 8 groups with a bias, top 8: one token 6.5 us (an empty launch is
-// 3.8), 16384 tokens 20 us (17 MB would take 3.5) and 9 us back, of them about
-// 2 for the last wave with a token in doubt; without groups or bias the
+// Bound by a wave's vector instructions and chain of reductions, not by bytes:
+// 256 experts in 8 groups with a bias, top 8: one token 5.6 us (an empty launch
+// is 3.8), 16384 tokens 18 us (17 MB would take 3.5; 1200 vector instructions a
+// wave of 4 tokens, 9 us) and 9 us back, of them about 2 for the last wave with
+// a token in doubt; without groups or bias the
 // choice is by the logits: 128000 tokens of 8 experts 3.8 us and 3.6 back.
 #include "bs_moe.h"
 #include "bs_device.h"
@@ -334,10 +335,10 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const float* lg, 
 #pragma unroll
         for (int v = 0; v < V; ++v) c[v] += bias[v];
     }
-    uint32_t dead = 0;  // bit v: masked
+    // masked experts at -inf (where a bias of -inf puts them by itself)
 #pragma unroll
-    for (int v = 0; v < V; ++v) dead |= (uint32_t)(lg[v] == kNegInf || c[v] == kNegInf) << v;
-    bool unsure = false;
+    for (int v = 0; v < V; ++v) c[v] = lg[v] == kNegInf ? kNegInf : c[v];
+    bool unsure = false, out = false;  // out: this lane's group does not stay
     // Groups better than g, surely and maybe, from their scores `stride` apart:
     // true if g stays.
     const auto stays = [&](const float* score, int stride, int g, float own) {
@@ -359,10 +360,9 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const float* lg, 
         float b1 = kNegInf, b2 = kNegInf;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float x = (dead >> v) & 1u ? kNegInf : c[v];
-            unsure |= x != x;
-            b2 = __builtin_amdgcn_fmed3f(b1, b2, x);
-            b1 = fmaxf(b1, x);
+            unsure |= c[v] != c[v];
+            b2 = __builtin_amdgcn_fmed3f(b1, b2, c[v]);
+            b1 = fmaxf(b1, c[v]);
         }
 #define BS_MERGE(STEP)                                                            \
         if constexpr (L > STEP) {                                                 \
@@ -377,7 +377,7 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const float* lg, 
         const float own = a.group_best > 1 && b2 > kNegInf ? b1 + b2 : b1;
         if (g < G) group_lds[g] = own;
         wave_sync();
-        if (!stays(group_lds, 1, g, own)) dead = ~0u;
+        out = !stays(group_lds, 1, g, own);
         wave_sync();  // the next use of group_lds
     } else if (a.n_group > 1) {
         // groups of any size: through LDS, laid out as in route_exact (16
@@ -386,9 +386,8 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const float* lg, 
         int at = e0 + g_first, left = Eg - (e0 - g_first * Eg);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float x = (dead >> v) & 1u ? kNegInf : c[v];
-            unsure |= x != x;
-            if (e0 + v < E) group_lds[at] = x;
+            unsure |= c[v] != c[v];
+            if (e0 + v < E) group_lds[at] = c[v];
             left -= 1;
             at += left == 0 ? 2 : 1;
             left = left == 0 ? Eg : left;
@@ -415,7 +414,7 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const float* lg, 
         left = Eg - (e0 - g_first * Eg);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            dead |= (uint32_t)(e0 + v < E && group_lds[at] == 0.f) << v;
+            if (e0 + v < E && group_lds[at] == 0.f) c[v] = kNegInf;
             left -= 1;
             at += left == 0 ? Eg + 1 : 0;
             left = left == 0 ? Eg : left;
@@ -426,17 +425,29 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const float* lg, 
         float key[V];
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            key[v] = (dead >> v) & 1u ? kNegInf : lg[v] != lg[v] ? __builtin_inff() : lg[v];
+            key[v] = out || c[v] == kNegInf ? kNegInf : lg[v] != lg[v] ? __builtin_inff() : lg[v];
         select_k<L, V, KR>(key, a.k, l, mine_idx);
         return unsure;
     }
-    constexpr uint32_t kPlace = V - 1;
+    constexpr uint32_t kPlace = V - 1, kNone = 0x007FFFFFu;  // kNone: to_ordered(-inf); its keys are not over it
     uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const float x = c[v] != c[v] ? __builtin_inff() : c[v];
-        key[v] = (dead >> v) & 1u ? 0u : (to_ordered(x) & ~kPlace) | (uint32_t)(kPlace - v);
+        unsure |= c[v] != c[v];
+        key[v] = (to_ordered(c[v]) & ~kPlace) | (uint32_t)(kPlace - v);
     }
+    // A lane's keys differ, and they are taken in descending order: those left
+    // are the ones below the last that was taken (limit; 0: none yet), and
+    // since key - limit wraps for just those, the largest of the differences
+    // finds the best of them.
+    uint32_t limit = 0;
+    const auto best_left = [&] {
+        uint32_t d[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] = key[v] - limit;
+        const uint32_t t = tree_max<V>(d);
+        return out || t < 0u - limit ? 0u : t + limit;
+    };
     float prev = 0.f;
     int prev_e = -1;
     const auto near = [&](float cur) {  // to the value before it in the order
@@ -448,14 +459,12 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const float* lg, 
         for (int q = 0; q < L; ++q) {
             const int j = r * L + q;
             if (j >= a.k) break;
-            const uint32_t best = tree_max<V>(key), top = best & ~kPlace;
+            const uint32_t best = best_left(), top = best & ~kPlace;
             const uint32_t mx = seg_reduce<L>(top, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+            if (mx <= kNone) break;
             const int own_e = e0 + (int)(kPlace - (best & kPlace));
             const int e = lowest<L>(top == mx, own_e);
-            const uint32_t gone = e == own_e ? best : 0xFFFFFFFFu;
-#pragma unroll
-            for (int v = 0; v < V; ++v) key[v] = key[v] == gone ? 0u : key[v];
-            if (mx == 0u) break;
+            limit = e == own_e ? best : limit;
             const float cur = from_ordered(mx);
             if (prev_e >= 0 && near(cur))
                 unsure |= row_lds[prev_e] != row_lds[e] || a.bias[prev_e] != a.bias[e];
@@ -464,15 +473,15 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const float* lg, 
             if (q == l) mine_idx[r] = e;
         }
     }
-    // those left out, every one of them against the last that was chosen: one
-    // that ties with it may have another next to it
-    uint32_t close = 0;
+    // those left out against the last that was chosen, every one that is near
+    // it: one that ties with it may have another next to it
+    const uint32_t left = best_left();
+    if (left > kNone && near(from_ordered(left & ~kPlace))) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) close |= (uint32_t)(key[v] != 0u && near(from_ordered(key[v] & ~kPlace))) << v;
-    while (close != 0) {
-        const int e = e0 + __builtin_ctz(close);
-        close &= close - 1;
-        unsure |= row_lds[prev_e] != row_lds[e] || a.bias[prev_e] != a.bias[e];
+        for (int v = 0; v < V; ++v) {
+            if (key[v] <= left && key[v] > kNone && near(from_ordered(key[v] & ~kPlace)))
+                unsure |= row_lds[prev_e] != row_lds[e0 + v] || a.bias[prev_e] != a.bias[e0 + v];
+        }
     }
     return unsure;
 }
