@@ -267,6 +267,7 @@ class _MoEFFNFn(torch.autograd.Function):
         _k.bs_moe_gather_quant_1x128(x2, row_slot, slot_row.shape[1], **qx)
         q12, s12, q12t, s12t = _expert_weights(w12)
         ab = _group_m(ends, qx, q12, s12, zeros=True)
+        del qx["q_row"], qx["s_row"], q12  # (memory that the rest of the pass can have)
         qh = _codes(M, H, True, dev)
         if fp8_checkpoint:
             kept = (torch.empty((M, H2), dtype=torch.uint8, device=dev), _b.empty_scales(H2 // 128, M, dev))
@@ -274,6 +275,7 @@ class _MoEFFNFn(torch.autograd.Function):
         else:
             kept = (ab, None)
             _b.bs_swiglu_quant_1x128(ab[:, :H], ab[:, H:], None, **qh)
+        del ab
         qo, so, qot, sot = _expert_weights(wo)
         y = _group_m(ends, qh, qo, so)
         ctx.save_for_backward(w, ends, slot_row, row_slot, qx["q_col"], qx["s_col"], q12t, s12t, *kept, qh["q_col"],
@@ -298,11 +300,13 @@ class _MoEFFNFn(torch.autograd.Function):
         dx = dw12 = None
         if need[0] or need[2]:
             dh = _group_m(ends, qd, qot, sot, zeros=True)
+            del qd
             qab = _codes(M, H2, True, dev)
             if kept_s is not None:
                 _k.bs_swiglu_bwd_quant_1x128_ckpt(kept, kept_s, dh, **qab)
             else:
                 _b.bs_swiglu_bwd_quant_1x128(kept[:, :H], kept[:, H:], dh, None, **qab)
+            del dh
             if need[2]:
                 dw12 = _group_k(ends, qab, dict(q_col=qxt, s_col=sxt))
             if need[0]:
