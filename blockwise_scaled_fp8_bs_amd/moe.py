@@ -364,8 +364,13 @@ class Float8BlockwiseMoE(torch.nn.Module):
     For serving, ``prepare_serving()`` lays the weights out once in FP8; while
     that layout is there and gradients are off, forward takes it: the rows are
     sorted without padding and quantized along rows only.  train(), moving the
-    module and loading a state drop the layout; a forward after any other
-    in-place change of the weights raises.
+    module and loading a state drop the layout, and a copy has none.  Other
+    weights than those laid out (assigned since, or passed for one call by
+    ``torch.func.functional_call``) are quantized by the forward that they are
+    there for.  Where the weights laid out have been written in place or given
+    other memory, forward raises.  It goes by autograd's version counter: what
+    writes past that (through ``.data``, in a collective, in a kernel of one's
+    own) is not seen, and needs prepare_serving() again.
     """
 
     def __init__(self, dim, hidden, experts, top_k, score="sigmoid", n_group=1, topk_group=1, group_best=1,
@@ -387,35 +392,48 @@ class Float8BlockwiseMoE(torch.nn.Module):
             for p in (self.router, self.w12, self.out_proj):
                 p.uniform_(-p.shape[-1] ** -0.5, p.shape[-1] ** -0.5)
         self.last_counts = None
-        self._serving = None
-
-    def _versions(self):
-        return [None if p.is_inference() else p._version for p in (self.w12, self.out_proj)]
+        self._serving = self._served = None
 
     def prepare_serving(self):
-        """Quantizes the expert weights for the forward; call again after they change."""
+        """Quantizes the expert weights for the forward; call again after they
+        change.  Not for inference tensors, whose changes nothing counts."""
+        weights = self.w12, self.out_proj
+        if any(p.is_inference() for p in weights):
+            raise RuntimeError("the expert weights are inference tensors, whose changes nothing counts: make or load the "
+                               "module outside torch.inference_mode()")
         with torch.no_grad():
-            self._serving = _expert_weights(self.w12)[:2] + _expert_weights(self.out_proj)[:2]
-        self._served_versions = self._versions()
+            self._serving = _expert_weights(weights[0])[:2] + _expert_weights(weights[1])[:2]
+        # what the layout is of: the tensors, their memory (an alias, so that its address is not handed out again) and
+        # their versions
+        self._served = [(p, p.detach(), p._version) for p in weights]
         return self
+
+    def _layout(self):
+        """The layout if it is that of the present weights, None if there is none of them."""
+        if self._serving is None or self.w12 is not self._served[0][0] or self.out_proj is not self._served[1][0]:
+            return None
+        if any(p._version != version or not p.is_set_to(memory) for p, memory, version in self._served):
+            raise RuntimeError("the expert weights changed after prepare_serving(): call it again")
+        return self._serving
+
+    def __getstate__(self):
+        return dict(self.__dict__, _serving=None, _served=None)
 
     def train(self, mode=True):
         if mode:
-            self._serving = None
+            self._serving = self._served = None
         return super().train(mode)
 
     def _apply(self, fn, *args, **kw):
-        self._serving = None
+        self._serving = self._served = None
         return super()._apply(fn, *args, **kw)
 
     def _load_from_state_dict(self, *args, **kw):
-        self._serving = None
+        self._serving = self._served = None
         return super()._load_from_state_dict(*args, **kw)
 
-    def _serve(self, x2, idx, w, residual):
-        if self._served_versions != self._versions():
-            raise RuntimeError("the expert weights changed after prepare_serving(): call it again")
-        q12, s12, qo, so = self._serving
+    def _serve(self, layout, x2, idx, w, residual):
+        q12, s12, qo, so = layout
         plan = _k.bs_moe_plan(idx, self.experts, align=1)
         M, H, dev = plan.row_slot.shape[0], self.hidden, x2.device
         qx = _codes(M, self.dim, False, dev)
@@ -431,8 +449,9 @@ class Float8BlockwiseMoE(torch.nn.Module):
             raise ValueError(f"x has {x2.shape[1]} features, the experts expect {self.dim}")
         logits = torch.nn.functional.linear(x2, self.router)
         idx, w = moe_route(logits, self.top_k, bias=self.balance, **self.how)
-        if self._serving is not None and x2.shape[0] > 0 and not torch.is_grad_enabled():
-            plan, y = self._serve(x2, idx, w, None if residual is None else _rows(residual, "residual"))
+        layout = None if torch.is_grad_enabled() or x2.shape[0] == 0 else self._layout()
+        if layout is not None:
+            plan, y = self._serve(layout, x2, idx, w, None if residual is None else _rows(residual, "residual"))
             y = y.view(x.shape)
         else:
             plan = _k.bs_moe_plan(idx, self.experts)
