@@ -21,8 +21,19 @@ BS_SCORE_SIGMOID = 1
 
 _DT = {torch.bfloat16: BS_OUT_BF16, torch.float32: BS_OUT_F32}
 
-#: group_end, counts [E]; slot_row [T, k]; row_slot [M] -- int32, see bs_moe_plan
-MoEPlan = namedtuple("MoEPlan", ["group_end", "counts", "slot_row", "row_slot"])
+
+class MoEPlan(namedtuple("MoEPlan", ["group_end", "counts", "slot_row", "row_slot"])):
+    """group_end, counts [E]; slot_row [T, k]; row_slot [M] -- int32, see
+    bs_moe_plan.  ``align``: the rows that each group is padded to a multiple
+    of (None where that is not known); no element of the tuple."""
+
+    align = None
+
+    def __new__(cls, group_end, counts, slot_row, row_slot, align=None):
+        plan = super().__new__(cls, group_end, counts, slot_row, row_slot)
+        plan.align = align
+        return plan
+
 
 #: gradients of bs_resid_norm; None for what was not asked for
 ResidNormGrads = namedtuple("ResidNormGrads", ["dx", "du", "dw_pre", "dw_post", "dgate"])
@@ -197,7 +208,7 @@ def bs_moe_plan(idx, E, align=128, M=None, stream=None):
     _check(lib.bs_moe_plan(p_idx, T, k, E, align, M, at, at + 4 * E, at + 8 * E, at + 8 * E + 4 * n,
                            base if nbytes else None, nbytes, _stream_of(idx, stream)), "bs_moe_plan")
     _, group_end, counts, slot_row, row_slot = buf.split_with_sizes([nw, E, E, n, M])
-    return MoEPlan(group_end, counts, slot_row.view(T, k), row_slot)
+    return MoEPlan(group_end, counts, slot_row.view(T, k), row_slot, align)
 
 
 def bs_moe_gather_quant_1x128(x, row_slot, k, w=None, y=None, q_row=None, s_row=None, q_col=None, s_col=None,

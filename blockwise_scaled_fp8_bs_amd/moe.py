@@ -314,6 +314,17 @@ class _MoEFFNFn(torch.autograd.Function):
         return dx, dw, dw12, dwo, (dout if need[4] else None), None, None, None, None
 
 
+def _check_plan(plan, slots, E):
+    """The weight gradients contract whole 128-row blocks of each group, so that
+    a group that ends inside one would lose rows or take another expert's."""
+    M, need, align = plan.row_slot.shape[0], _k.bs_moe_plan_rows(*slots, E), getattr(plan, "align", None)
+    if tuple(plan.slot_row.shape) != tuple(slots) or plan.group_end.shape[0] != E or M % 128 != 0 or M < need \
+            or align is None or align % 128 != 0:
+        raise ValueError(f"the plan is for {list(plan.slot_row.shape)} slots, {plan.group_end.shape[0]} experts and {M} "
+                         f"rows in groups of a multiple of {align}: this needs {list(slots)}, {E} and groups padded to "
+                         f"128 rows (at least {need}; a MoEPlan made by hand says so by its align)")
+
+
 def float8_blockwise_moe_ffn(x, idx, w, w12, out_proj, residual=None, checkpoint="fp8", plan=None):
     """residual + sum_j w_j out_e(silu(a) b), [a | b] = x [w1; w2]_e^T, over the
     experts e = idx[t, j] of each token, every GEMM in blockwise FP8.
@@ -322,7 +333,8 @@ def float8_blockwise_moe_ffn(x, idx, w, w12, out_proj, residual=None, checkpoint
     fp32, as moe_route gives them; w12 [E, 2H, D] (w1's rows, then w2's) and
     out_proj [E, D, H] bf16; D and H multiples of 128.  checkpoint: how [a | b]
     is kept for the backward, "fp8" (1x128 codes) or "bf16".  plan: that of
-    bs_moe_plan(idx, E), every group padded to 128 rows (made here if None).
+    bs_moe_plan(idx, E), every group padded to 128 rows or a multiple (made
+    here if None).
     """
     if checkpoint not in ("fp8", "bf16"):
         raise ValueError(f'checkpoint must be "fp8" or "bf16", got {checkpoint!r}')
@@ -344,10 +356,7 @@ def float8_blockwise_moe_ffn(x, idx, w, w12, out_proj, residual=None, checkpoint
         raise ValueError(f"idx and w must be [{x2.shape[0]}, k], got {list(idx.shape)} and {list(w.shape)}")
     if plan is None:
         plan = _k.bs_moe_plan(idx, E)
-    M, need = plan.row_slot.shape[0], _k.bs_moe_plan_rows(idx.shape[0], idx.shape[1], E)
-    if plan.slot_row.shape != idx.shape or plan.group_end.shape[0] != E or M % 128 != 0 or M < need:
-        raise ValueError(f"the plan is for {list(plan.slot_row.shape)} slots, {plan.group_end.shape[0]} experts and {M} "
-                         f"rows: this needs {list(idx.shape)}, {E} and groups padded to 128 rows (at least {need})")
+    _check_plan(plan, idx.shape, E)
     r2 = None if residual is None else _rows(residual, "residual")
     y = _MoEFFNFn.apply(x2, w, w12, out_proj, r2, plan.group_end, plan.slot_row, plan.row_slot, checkpoint == "fp8")
     return y.view(x.shape)
