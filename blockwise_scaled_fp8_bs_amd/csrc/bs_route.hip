@@ -606,6 +606,10 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, bool whole
 // for an expert with nearly all of the sum.  With g_0 that of the largest
 // share and rest = 1 - sum p_i (of the sigmoid's 1e-20; 0 for the softmax) it
 // is (g_j - g_0) - sum p_i (g_i - g_0) + rest g_0, where nothing cancels.
+// Not renormalized, the softmax's shares are of all experts, g of those that
+// were not chosen 0: for the largest share that was chosen it is (1 - p_0) g_0
+// less the others' p_i g_i, with 1 - p_0 from the exponentials of all others;
+// the rest have p_j <= 1/2, and g_j - sum p_i g_i loses no more than a bit.
 template <bool BF16, int L, int V>
 __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a) {
     constexpr int TPB = kThreads / L;
@@ -616,13 +620,15 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a) {
     const bool real = tok < a.T;
     const int64_t t = real ? tok : a.T - 1;
     const int E = (int)a.E, e0 = l * V;
+    const bool all = !a.sigmoid && !a.renorm;  // every logit of the row has a gradient
+    // an expert that was not chosen: no result of arithmetic has these bits (a signalling NaN)
+    constexpr uint32_t kNotChosen = 0x7FBADBADu;
 #pragma unroll
-    for (int v = 0; v < V; ++v) s_row[tb][e0 + v] = 0.f;
+    for (int v = 0; v < V; ++v) s_row[tb][e0 + v] = all ? __uint_as_float(kNotChosen) : 0.f;
     __syncthreads();
 
     float m = kNegInf, z = 1.f;
     float lg[V];
-    const bool all = !a.sigmoid && !a.renorm;  // every logit of the row has a gradient
     if (all) {
         load_logits<BF16, V>(a.logits, t * a.ld, e0, E, a.vec, lg);
 #pragma unroll
@@ -677,16 +683,37 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a) {
         top = seg_reduce<L>(top, [](uint64_t x, uint64_t y) { return x > y ? x : y; });
         g0 = __uint_as_float((uint32_t)top);
     }
+    int e_top = -1;  // the largest share that was chosen, of all experts
+    float p0 = 0.f, others = 0.f;  // it, and 1 - p_0
+    if (all) {
+        uint64_t top = 0;
+#pragma unroll
+        for (int r = 0; r < KR; ++r) {
+            const uint64_t x = ((uint64_t)__float_as_uint(fabsf(w[r])) << 32) | (uint32_t)(e[r] + 1);
+            if (x > top) top = x;
+        }
+        top = seg_reduce<L>(top, [](uint64_t x, uint64_t y) { return x > y ? x : y; });
+        p0 = __uint_as_float((uint32_t)(top >> 32));
+        e_top = (int)(uint32_t)top - 1;
+#pragma unroll
+        for (int v = 0; v < V; ++v) others += e0 + v == e_top ? 0.f : lg[v];
+        others = seg_sum<L>(others) / z;
+    }
+    float g_top = 0.f;
 #pragma unroll
     for (int r = 0; r < KR; ++r) {
         g[r] = e[r] >= 0 ? g[r] - g0 : 0.f;
-        dot += w[r] * g[r];
+        if (all && e[r] == e_top) g_top = g[r];
+        else dot += w[r] * g[r];
     }
-    dot = seg_sum<L>(dot);
+    dot = seg_sum<L>(dot);  // all: without the largest share's
+    const float mean = all ? dot + p0 * seg_sum<L>(g_top) : dot;
 #pragma unroll
     for (int r = 0; r < KR; ++r) {
         if (e[r] >= 0) {
-            const float d = a.renorm ? (g[r] - dot) + rest * g0 : g[r];
+            float d = g[r];
+            if (a.renorm) d = (g[r] - dot) + rest * g0;
+            else if (all) d = e[r] == e_top ? others * g[r] - dot : g[r] - mean;
             s_row[tb][e[r]] = a.sigmoid ? f * d * s[r] * ns[r] : a.scale * w[r] * d;
         }
     }
@@ -696,9 +723,9 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] = s_row[tb][e0 + v];
     if (all) {
-        const float c = z != 0.f ? a.scale * dot / z : 0.f;  // 0: every expert is masked
+        const float c = z != 0.f ? a.scale * mean / z : 0.f;  // 0: every expert is masked
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[v] -= c * lg[v];
+        for (int v = 0; v < V; ++v) o[v] = __float_as_uint(o[v]) == kNotChosen ? 0.f - c * lg[v] : o[v];
     }
     const int64_t at = tok * a.ld_d + e0;
     if constexpr (BF16) {

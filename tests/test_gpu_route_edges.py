@@ -1,4 +1,5 @@
-"""GPU router where fp32 alone would answer wrongly: ties hidden behind ties."""
+"""GPU router where fp32 alone would answer wrongly: ties hidden behind ties,
+and gradients that are what is left of a cancellation."""
 
 import numpy as np
 import pytest
@@ -41,3 +42,38 @@ def test_route_hidden_tie_after_the_groups_are_chosen(E, G, tg):
         assert (np.abs(w.cpu().double().numpy() - want_w) <= want_w * 2.0 ** -19).all()
         seen.add(int(want_idx[0, 3]))
     assert seen == {5, E - 1}  # both sides of the tie were met
+
+
+@pytest.mark.parametrize("lead", [0.0, 4.0, 12.0, 16.0, 20.0, 30.0, 60.0])
+@pytest.mark.parametrize("E,k", [(8, 1), (8, 3), (64, 6), (256, 8), (1000, 32)])
+def test_route_gradient_of_plain_softmax_where_one_expert_has_all_the_weight(E, k, lead):
+    """dl_j = scale p_j sum_e p_e (G_j - G_e), G_e = dw of a chosen expert and 0
+    of the others: the term of j itself is 0, and with a lead p_j (1 - p_j) is
+    far below the rounding of p_j."""
+    need_gpu()
+    T, scale = 19, 2.5
+    rng = np.random.default_rng(E + k)
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    ahead = rng.integers(0, E, T)
+    l[np.arange(T), ahead] = l.max(axis=1) + np.float32(lead)
+    if E > 2 * k:
+        l[1, :E // 2] = -np.inf
+    l = torch.from_numpy(l)
+    g = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32))
+    g[2] = 0.7
+    print(f"route plain softmax gradient E={E} k={k} lead={lead}", flush=True)
+    idx, w = bs.bs_moe_route(l.cuda(), k, renormalize=False, scale=scale)
+    d = bs.bs_moe_route_bwd(l.cuda(), idx, w, g.cuda(), renormalize=False, scale=scale).cpu().double().numpy()
+    L, at = _f64(l), idx.cpu().numpy()
+    p = np.exp(L - L.max(axis=1, keepdims=True))
+    p /= p.sum(axis=1, keepdims=True)
+    G = np.zeros((T, E))
+    np.put_along_axis(G, at, g.double().numpy(), 1)
+    diff = G[:, :, None] - G[:, None, :]
+    want = scale * p * (p[:, None, :] * diff).sum(axis=2)
+    # Terms that the kernel adds: (1 - p_j) G_j and p_e G_e of the others.  Relative errors in units of 2^-24: a share
+    # has lead + 5 from its exponent, 2 from the exponential, 25 from the sum and 5 from products and quotients; there
+    # are two in a term, and up to 40 additions: 2 (65 + 37) + 40 < 256.
+    others = np.ones((E, E)) - np.eye(E)
+    mag = scale * p * (np.abs(G) * (p @ others) + (p * np.abs(G)) @ others)
+    assert (np.abs(d - want) <= mag * 2.0 ** -16 + 1e-36).all()
