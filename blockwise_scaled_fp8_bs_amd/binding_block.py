@@ -273,9 +273,9 @@ def _norm_params(R, D, w_pre, w_post, gate):
     if gate is not None:
         B = _first(gate, "gate", dt)[0]
         p_gate, ld_gate = _matrix(gate, "gate", dt, B, D)
-        if B < 1 or R % B != 0:
+        if R % B != 0 if B else R != 0:
             raise ValueError(f"the {R} rows must be a multiple of the gate's {B}")
-        per = R // B
+        per = max(R // B, 1) if B else 1
     return (None if w_pre is None else _flat(w_pre, "w_pre", dt, (D,)),
             None if w_post is None else _flat(w_post, "w_post", dt, (D,)), p_gate, ld_gate, per, _DT[dt])
 

@@ -1,0 +1,25 @@
+"""GPU calls of the MoE block on no rows."""
+
+import pytest
+import torch
+
+import blockwise_scaled_fp8_bs_amd as bs
+from gpu_support import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("B", [0, 1, 2])
+def test_no_rows_with_a_gate(B):
+    need_gpu()
+    D = 256
+    x = torch.empty((B, 0, D) if B else (0, 3, D), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    u = torch.empty_like(x, requires_grad=True)
+    w_post, w_pre = (torch.ones(D, device="cuda", requires_grad=True) for _ in range(2))
+    gate = torch.ones((B, D), device="cuda", requires_grad=True)
+    print(f"norm of no rows, a gate of {B}", flush=True)
+    r, h = bs.resid_norm(x, w_pre, u=u, w_post=w_post, gate=gate)
+    assert r.shape == h.shape == x.shape
+    (r.float().sum() + h.float().sum()).backward()
+    for t in (x, u, w_post, w_pre, gate):
+        assert t.grad.shape == t.shape and not t.grad.any()
