@@ -31,8 +31,9 @@ bs_status check_bf16(const char* fn, const char* name, const void* p, int64_t co
 bs_status check_codes(const char* fn, int64_t R, int64_t C, const uint8_t* q_row, int64_t ld_qr, const float* s_row,
                       int64_t ld_sr, const uint8_t* q_col, int64_t ld_qc, const float* s_col, int64_t ld_sc) {
     const bool row = q_row || s_row, col = q_col || s_col;
-    REQUIRE(!row || (q_row && s_row), BS_ERR_NULL, "q_row and s_row must both be set or both NULL");
-    REQUIRE(!col || (q_col && s_col), BS_ERR_NULL, "q_col and s_col must both be set or both NULL");
+    const bool empty = R == 0 || C == 0;  // codes without elements may be NULL beside scales that are not
+    REQUIRE(!row || (q_row && s_row) || empty, BS_ERR_NULL, "q_row and s_row must both be set or both NULL");
+    REQUIRE(!col || (q_col && s_col) || empty, BS_ERR_NULL, "q_col and s_col must both be set or both NULL");
     if (row || col)
         REQUIRE(C % 128 == 0, BS_ERR_SHAPE, "%lld columns must be a multiple of 128 (1x128 blocks along rows)", (ll)C);
     if (row) {

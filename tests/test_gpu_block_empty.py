@@ -23,3 +23,16 @@ def test_no_rows_with_a_gate(B):
     (r.float().sum() + h.float().sum()).backward()
     for t in (x, u, w_post, w_pre, gate):
         assert t.grad.shape == t.shape and not t.grad.any()
+
+
+def test_no_rows_into_prepared_outputs():
+    """Codes of no rows, into views of buffers that were made for more."""
+    need_gpu()
+    D = 256
+    q, s = torch.empty((128, D), dtype=torch.uint8, device="cuda"), bs.empty_scales(D // 128, 128, "cuda").fill_(5.0)
+    x = torch.empty((0, D), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(D, device="cuda")
+    print("codes of no rows", flush=True)
+    bs.bs_resid_norm(x, w, q_row=q[:0], s_row=s)
+    bs.bs_moe_gather_quant_1x128(x, torch.empty(0, dtype=torch.int32, device="cuda"), 2, q_row=q[:0], s_row=s)
+    assert (s == 5.0).all()
