@@ -69,9 +69,9 @@ def _matrix(t, name, dtype, R, C):
     if t is None or t.dtype is not dtype or not t.is_cuda or t.shape != (R, C):
         _fail_matrix(t, name, dtype, R, C)
     ld, unit = t.stride()
-    if unit != 1 and C > 1:
+    if unit != 1 and C > 1 and R > 0:
         _mat(t, name, dtype)
-    # the stride of an only row says nothing: its length stands for it
+    # the strides of no row, and that of an only one, say nothing: its length stands for it
     return t.data_ptr() or None, ld if R > 1 else (C + 15) // 16 * 16
 
 

@@ -36,3 +36,17 @@ def test_no_rows_into_prepared_outputs():
     bs.bs_resid_norm(x, w, q_row=q[:0], s_row=s)
     bs.bs_moe_gather_quant_1x128(x, torch.empty(0, dtype=torch.int32, device="cuda"), 2, q_row=q[:0], s_row=s)
     assert (s == 5.0).all()
+
+
+def test_no_tokens_through_the_autograd_pieces():
+    """A sum's gradient of no elements comes with strides of 0."""
+    need_gpu()
+    D = 256
+    x = torch.empty((0, D), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    logits = torch.empty((0, 8), device="cuda", requires_grad=True)
+    print("autograd pieces of no tokens", flush=True)
+    idx, w = bs.moe_route(logits, 2)
+    plan = bs.bs_moe_plan(idx, 8)
+    y = bs.moe_combine(bs.moe_dispatch(x, plan), plan, w, x)
+    y.sum().backward()
+    assert y.shape == x.grad.shape == (0, D) and logits.grad.shape == (0, 8)
