@@ -106,14 +106,14 @@ __device__ __forceinline__ T block_sum(T v, T* lds) {
 }
 
 // 1 / sqrt(v) in float64: the hardware's estimate and two Newton steps, in
-// which infinities times 0 would be NaN: the estimate of 0 (infinity) and that
-// of infinity (0) stand as they are.
+// which infinity times 0 is NaN: the estimate of 0 (infinity) and that of
+// infinity (0) stand as they are.
 __device__ __forceinline__ double rsqrt64(double v) {
     const double y0 = __builtin_amdgcn_rsq(v);
     const double h = 0.5 * v;
     double y = y0 * __builtin_fma(-h * y0, y0, 1.5);
     y = y * __builtin_fma(-h * y, y, 1.5);
-    return v > 0.0 && v < __builtin_inf() ? y : y0;
+    return y == y ? y : y0;
 }
 
 // A workgroup has a thread for each NC chunks of 8 columns and walks down
