@@ -367,8 +367,10 @@ class Float8BlockwiseMoE(torch.nn.Module):
 
     router [experts, dim], w12 [experts, 2 hidden, dim], out_proj
     [experts, dim, hidden] (bf16 parameters) and balance [experts], the bias of
-    the choice (an fp32 buffer that a training loop moves by the loads in
-    ``last_counts``).  forward(x, residual) returns residual + experts(x).
+    the choice (a buffer that a training loop moves by the loads in
+    ``last_counts``, fp32 also where the module is cast).  forward(x, residual)
+    returns residual + experts(x).  The logits are a bf16 product: experts
+    whose logits round to the same value tie, and the lowest is taken.
 
     For serving, ``prepare_serving()`` lays the weights out once in FP8; while
     that layout is there and gradients are off, forward takes it: the rows are
@@ -435,7 +437,11 @@ class Float8BlockwiseMoE(torch.nn.Module):
 
     def _apply(self, fn, *args, **kw):
         self._serving = self._served = None
-        return super()._apply(fn, *args, **kw)
+        balance = self.balance
+        super()._apply(fn, *args, **kw)
+        if self.balance.dtype != torch.float32:  # the module was cast: the weights' type is not the bias's
+            self.balance = balance.to(self.balance.device)
+        return self
 
     def _load_from_state_dict(self, *args, **kw):
         self._serving = self._served = None
