@@ -18,6 +18,7 @@
 // wave of 4 tokens, 9 us) and 9 us back, of them about 2 for the last wave with
 // a token in doubt; without groups or bias the
 // choice is by the logits: 128000 tokens of 8 experts 3.8 us and 3.6 back.
+// Weights are computed in fp32, also where the choice went by float64.
 #include "bs_moe.h"
 #include "bs_device.h"
 
@@ -213,13 +214,19 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t row, int
         sum += key[v];
     }
     if (!a.sigmoid) {
-        const double r = 1.0 / seg_sum<L>(sum);
+        sum = seg_sum<L>(sum);
+        const double r = 1.0 / sum;
+        // a NaN or +inf logit makes every score NaN: it counts as the largest, and the others as 0
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] *= r;
+        for (int v = 0; v < V; ++v)
+            key[v] = sum == sum ? key[v] * r : lg[v] < __builtin_inff() ? 0.0 : __builtin_inf();
     }
     if (a.bias != nullptr) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] += e0 + v < E ? (double)a.bias[e0 + v] : 0.0;
+        for (int v = 0; v < V; ++v) {
+            const float b = e0 + v < E ? a.bias[e0 + v] : 0.f;
+            key[v] = b == kNegInf ? kNone : key[v] + (double)b;  // (masked, also where the score is not finite)
+        }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {

@@ -512,9 +512,11 @@ typedef enum bs_score_kind {
  *           0 where idx is -1.  A token with every logit -inf gets none.
  * Choices between values that differ are exact: they are made on the logits,
  * or on scores in fp32 where their error cannot change the choice and in
- * float64 where it could.  Weights are computed in fp32.  A NaN logit ranks above every number and its weights
- * (with softmax or renormalize: the token's) are NaN; +inf ranks first too,
- * and its softmax is NaN as the formula gives.
+ * float64 where it could.  Weights are computed in fp32.  A NaN logit that is
+ * not masked ranks above every number, and its weights (with softmax or
+ * renormalize: the token's) are NaN.  So does +inf with softmax, whose scores
+ * are NaN then as the formula gives (a choice by them takes them as 0 for the
+ * token's other experts); its sigmoid is 1.
  *   1 <= E <= 1024, 1 <= k <= min(E, 32), E % n_group == 0,
  *   1 <= topk_group <= n_group, scale finite and not 0.
  */
