@@ -194,7 +194,8 @@ __device__ __forceinline__ void quant_row(const float* f, int i, __amdgpu_buffer
 // checkpoint codes and its h, the backward's da and its db, of which each
 // recomputes what both need.  Forward and backward at 1152 x 640 (45 tiles):
 // 10.1 and 12.9 us, whole 11.4 and 17.1; at 256 tiles 13.0 and 18.3, 14.8 and
-// 19.1; at 512 19.6 and 29.5, 21.4 and 28.3.
+// 19.1; at 512 19.6 and 29.5, 21.4 and 28.3.  One limit for both, where the
+// backward's gain ends; the forward's reaches further.
 enum Part { kFirst = 0, kSecond = 1, kBoth = 2 };
 
 template <bool ROW, bool COL, int PART>

@@ -13,6 +13,15 @@
 // IEEE divide; bs_diag_division proves on the device that the sequences give
 // the IEEE quotient bit for bit over every (amax, x) pair that bf16 inputs
 // can produce, and the parity tests compare against the CPU oracle.
+//
+// Values in fp32 (norms, weighted rows) go the same way.  The scale is the
+// IEEE quotient for every amax: a 24-bit number over 448 = 7 * 2^6 lies at
+// least 1/14 of a unit in the last place from a middle between two floats, and
+// the corrected quotient errs by 2^-24 units before its rounding.  x / s errs
+// by as little, but may lie nearer to a middle than that, down to 2^-25
+// units: y can then be the float on its other side.  The code changes only if
+// one of the two is a tie between two codes, which 20 pairs of significands
+// come that near to; a test runs them, and random blocks.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -166,11 +166,12 @@ constexpr int kGatherSpan = 4;
 // Row r of the result is row row_slot[r] / k of x (times w[row_slot[r]]), zero
 // where the slot is negative.  As the quantizer's one-workgroup-per-tile form,
 // with the tile's rows taken from wherever their tokens lie.  Bound by HBM: at
-// 128000 slots of 64000 tokens of 5120 in rows and columns 455 us (1.28 GB read,
-// half of it out of the last-level cache, 1.36 GB written: 5.8 TB/s), 472
-// weighted, 306 in rows alone; with the blocks of rows outermost, so that every
-// slot's row comes from HBM, 522, 525 and 367.  With one slot a token nothing
-// is read twice: 526 that way, 542 the other.
+// 128000 slots of 64000 tokens of 5120 in rows and columns 437 us (1.28 GB read,
+// half of it out of the last-level cache, 1.36 GB written: 6.0 TB/s), 450
+// weighted, 297 in rows alone, 425 to bf16 (455, 472, 306 and 430 on another
+// card); with the blocks of rows outermost, so that every slot's row
+// comes from HBM, 522, 525 and 367.  With one slot a token nothing is read
+// twice: 526 that way, 542 the other.
 // NEAR: x within 2 GiB, its rows addressed by 32-bit offsets into one buffer
 // (absent rows past its end, where loads give zeros): registers for four waves
 // on a SIMD instead of three.

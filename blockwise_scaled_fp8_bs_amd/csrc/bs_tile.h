@@ -1,7 +1,7 @@
 // The 128x128 tile of the quantizer kernels: loads with bounds, row and column
 // blocks, transposed stores through LDS, and the gated activation's
 // arithmetic.  Shared by the kernels that quantize what they compute
-// (bs_quant.hip, bs_moe.hip, bs_norm.hip).  gfx950 only.
+// (bs_quant.hip, bs_moe.hip, bs_norm.hip, bs_ckpt.hip).  gfx950 only.
 //
 // A tile is owned by 256 threads (4 wave64s); thread t holds an 8x8
 // sub-block: rows 8*(t/16) .. +7 and columns 8*(t%16) .. +7.

@@ -371,6 +371,7 @@ class Float8BlockwiseMoE(torch.nn.Module):
     ``last_counts``, fp32 also where the module is cast).  forward(x, residual)
     returns residual + experts(x).  The logits are a bf16 product: experts
     whose logits round to the same value tie, and the lowest is taken.
+    checkpoint: how [a | b] is kept for the backward, in 8 bits by default.
 
     For serving, ``prepare_serving()`` lays the weights out once in FP8; while
     that layout is there and gradients are off, forward takes it: the rows are
@@ -381,7 +382,9 @@ class Float8BlockwiseMoE(torch.nn.Module):
     there for.  Where the weights laid out have been written in place or given
     other memory, forward raises.  It goes by autograd's version counter: what
     writes past that (through ``.data``, in a collective, in a kernel of one's
-    own) is not seen, and needs prepare_serving() again.
+    own) is not seen, and needs prepare_serving() again.  A pass captured into a
+    graph reads the memory of the layout that was there: capture it again after
+    prepare_serving(), and do not replay it once the layout was dropped.
     """
 
     def __init__(self, dim, hidden, experts, top_k, score="sigmoid", n_group=1, topk_group=1, group_best=1,
