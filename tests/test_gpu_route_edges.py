@@ -77,3 +77,29 @@ def test_route_gradient_of_plain_softmax_where_one_expert_has_all_the_weight(E, 
     others = np.ones((E, E)) - np.eye(E)
     mag = scale * p * (np.abs(G) * (p @ others) + (p * np.abs(G)) @ others)
     assert (np.abs(d - want) <= mag * 2.0 ** -16 + 1e-36).all()
+
+
+@pytest.mark.parametrize("kind", [block.SOFTMAX, block.SIGMOID], ids=["softmax", "sigmoid"])
+def test_route_gradient_of_plain_weights_equals_differences(kind):
+    """Of the float64 oracle's forward, one logit of a token ahead of the others."""
+    need_gpu()
+    T, E, k = 5, 16, 3
+    rng = np.random.default_rng(8)
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    l[np.arange(T), 3] += np.float32(2.0) * np.arange(T, dtype=np.float32)
+    g = rng.standard_normal((T, k)).astype(np.float32)
+    gl = torch.from_numpy(l).cuda()
+    print(f"route plain gradient against differences, kind {kind}", flush=True)
+    idx, w = bs.bs_moe_route(gl, k, score=kind, renormalize=False, scale=1.5)
+    d = bs.bs_moe_route_bwd(gl, idx, w, torch.from_numpy(g).cuda(), score=kind, renormalize=False, scale=1.5).cpu().numpy()
+    want, h = np.zeros((T, E)), 1e-6
+    for t in range(T):
+        for e in range(E):
+            ends = []
+            for step in (h, -h):
+                m = l.astype(np.float64)
+                m[t, e] += step
+                ends.append((block.route(m, k, kind=kind, renorm=False, scale=1.5)[1] * g).sum())
+            want[t, e] = (ends[0] - ends[1]) / (2 * h)
+    # differences: float64's 2^-52 of sums of about 10, over 2e-6, and the third derivative's h^2; the kernel's fp32
+    assert np.abs(d - want).max() < 1e-5
