@@ -52,6 +52,14 @@ from .binding_block import (  # noqa: F401,E402
     bs_swiglu_bwd_quant_1x128_ckpt,
     bs_swiglu_quant_1x128_ckpt,
 )
+from .binding_few import (  # noqa: F401,E402
+    BS_WEIGHT_E4M3_128X128,
+    BS_WEIGHT_MXFP4,
+    BS_WEIGHT_MXFP8,
+    bs_few_mm,
+    bs_moe_few,
+    bs_mx4_quant_1x32,
+)
 from .linear import Float8BlockwiseLinear, float8_blockwise_linear, swap_linear_layers  # noqa: F401,E402
 from .ffn import Float8BlockwiseGatedFFN, float8_blockwise_gated_ffn  # noqa: F401,E402
 from .mx import Float8MXLinear, float8_mx_linear, mx_grouped_mm  # noqa: F401,E402

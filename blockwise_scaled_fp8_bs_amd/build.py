@@ -33,7 +33,7 @@ CFLAGS = [
 ]
 
 SOURCES = ["bs_api.hip", "bs_quant.hip", "bs_gemm.hip", "bs_diag.hip", "bs_block_api.hip", "bs_route.hip", "bs_moe.hip",
-           "bs_norm.hip", "bs_ckpt.hip"]
+           "bs_norm.hip", "bs_ckpt.hip", "bs_few_api.hip", "bs_few.hip", "bs_mx4.hip"]
 
 
 def _run(cmd):

@@ -691,6 +691,96 @@ bs_status bs_swiglu_bwd_quant_1x128_ckpt(const uint8_t* ck, int64_t R, int64_t C
                                          int64_t ld_qr, float* s_row, int64_t ld_sr, uint8_t* q_col, int64_t ld_qc,
                                          float* s_col, int64_t ld_sc, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Serving few tokens from quantized weights: single tokens, drafted ones and
+ * decoding batches, for which the tiles of the GEMMs above are too large.
+ * Every weight is read once for up to 64 tokens; tokens are bf16 and are not
+ * quantized, sums are in fp32.
+ * ------------------------------------------------------------------------ */
+
+/* Formats of the weights [N, K], contiguous along the contraction. */
+typedef enum bs_weight_kind {
+    BS_WEIGHT_E4M3_128X128 = 0, /* bs_quant_128x128: float scales s[(k/128) * ld_s + n/128];
+                                   N and K multiples of 128                       */
+    BS_WEIGHT_MXFP8 = 1,        /* bs_mx_quant_1x32's row output: E8M0 bytes
+                                   s[(k/32) * ld_s + n]; K a multiple of 32, any N */
+    BS_WEIGHT_MXFP4 = 2         /* bs_mx4_quant_1x32: the same scales, two codes a byte */
+} bs_weight_kind;
+
+/*
+ * bs_mx4_quant_1x32 -- weights to MXFP4 (OCP Microscaling v1.0 with E2M1
+ * elements, the 4-bit sibling of bs_mx_quant_1x32): blocks of 32 consecutive
+ * values of a row, one E8M0 byte each, byte = floor(log2(amax)) - 2 + 127
+ * clamped to [0, 254] (a zero block gets byte 0), elements
+ * e2m1(clamp(x / 2^(byte - 127), -6, 6)), nearest even, sign of zero kept.
+ *   x  [R, C] bf16, finite, ld_x >= C; C % 32 == 0, any R
+ *   q  [R, C / 2] bytes, ld_q >= C / 2, a multiple of 16: column 2j in the low
+ *      four bits of byte j, column 2j + 1 in the high ones
+ *   s  [C / 32][ld_s >= R] bytes, K-major: s[(c / 32) * ld_s + r], ld_s a
+ *      multiple of 16; padding is never written
+ *   y  optional [R, C] bf16: the values that the codes stand for (exact),
+ *      ld_y >= C; may be x itself
+ */
+bs_status bs_mx4_quant_1x32(const uint16_t* x, int64_t R, int64_t C, int64_t ld_x, uint8_t* q, int64_t ld_q, uint8_t* s,
+                            int64_t ld_s, uint16_t* y, int64_t ld_y, hipStream_t stream);
+
+/*
+ * bs_few_mm -- out[T, N] = residual[T, N] + x[T, K] . W[N, K]^T for few rows x:
+ * the weights' values (code times scale) times bf16 x, summed in fp32 in an
+ * order that depends on the sizes alone, rounded once.  A row of the result
+ * depends on its row of x alone, but for the order of its sum, which can
+ * change with T.
+ *   x         [T, K] bf16, ld_x >= K, 0 <= T <= 2^21 (above 64 the weights are
+ *             read once for every 64 rows), K >= 1
+ *   w         [N, K] codes of the given kind, ld_w in bytes, a multiple of 16
+ *   s         its scales, K-major with row stride ld_s in elements; no
+ *             alignment but its type's.  Products of MX weights below 2^-126
+ *             in magnitude may be lost, and values above the largest bf16
+ *             (scale bytes that no quantizer makes) are infinite.
+ *   residual  [T, N] bf16 or NULL (zeros); may be out itself where that is bf16
+ *   out       [T, N] bf16 or fp32, ld_out >= N; rows need no alignment (columns
+ *             by fours, 8- or 16-byte aligned, are stored faster)
+ */
+bs_status bs_few_mm(bs_weight_kind kind, int64_t T, int64_t N, int64_t K, const uint16_t* x, int64_t ld_x, const uint8_t* w,
+                    int64_t ld_w, const void* s, int64_t ld_s, const uint16_t* residual, int64_t ld_res, void* out,
+                    int64_t ld_out, bs_dtype out_dtype, hipStream_t stream);
+
+/*
+ * bs_moe_few -- the gated experts of few routed tokens and their weighted sum,
+ * in two kernels:
+ *   out[t] = residual[t] + sum_j w[t, j] Wo_e (silu(a) b),  e = idx[t, j],
+ *   [a | b] = W12_e x[t] (a from W12's rows [0, H), b from [H, 2H))
+ * h = w silu(a) b is rounded once to bf16 (from fp32 a and b: what the matrix
+ * instructions take), everything else is in fp32 and rounded once at the end.
+ * Only experts that some token chose are read, once for every 64 tokens.
+ *   x         [T, D] bf16, ld_x >= D
+ *   idx       [T, k] int32, contiguous, as bs_moe_route gives them; values
+ *             outside [0, E) are not routed, and their w is not used.  NULL
+ *             with E = 1 and k = 1: every token takes expert 0 (a gated FFN)
+ *   w         [T, k] float, contiguous, or NULL (ones).  A token that names an
+ *             expert twice takes it once, with the sum of the two weights.
+ *   w12       [E][2H, D] codes, ld_w12 and stride_w12 (between experts) in
+ *             bytes, multiples of 16; s12 its scales, stride_s12 and ld_s12 in
+ *             elements
+ *   out_proj  [E][D, H], stride_wo, ld_wo; s_out, stride_so, ld_so
+ *   residual  [T, D] bf16 or NULL (zeros); may be out itself
+ *   out       [T, D] bf16, ld_out >= D
+ *   workspace bs_moe_few_workspace_bytes(T, k, H) bytes of DEVICE memory, 16-byte
+ *             aligned, without initial contents; calls that share one must not
+ *             overlap in time
+ *   D and H multiples of 128 (E4M3_128X128) or 32 (MX), at most 262144;
+ *   1 <= E <= 1024, 1 <= k <= min(E, 32), 0 <= T <= 2^21.
+ */
+bs_status bs_moe_few(bs_weight_kind kind, int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, const uint16_t* x,
+                     int64_t ld_x, const int32_t* idx, const float* w, const uint8_t* w12, int64_t stride_w12,
+                     int64_t ld_w12, const void* s12, int64_t stride_s12, int64_t ld_s12, const uint8_t* out_proj,
+                     int64_t stride_wo, int64_t ld_wo, const void* s_out, int64_t stride_so, int64_t ld_so,
+                     const uint16_t* residual, int64_t ld_res, uint16_t* out, int64_t ld_out, void* workspace,
+                     int64_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of bs_moe_few (h of every slot).  Invalid arguments give 0. */
+int64_t bs_moe_few_workspace_bytes(int64_t T, int64_t k, int64_t H);
+
 /* Human-readable name of a status code (static storage). */
 const char* bs_status_string(bs_status status);
 
