@@ -59,9 +59,9 @@ struct MoeFewArgs {
     uint16_t* out;
     int64_t ld_out;
     bool vec;
-    uint16_t* h;    // workspace [T, k, H] bf16
+    uint16_t* h;    // workspace [T * k, H] bf16
     int64_t tiles;  // set by the launcher
-    int32_t ranks;
+    int32_t items;  // set by the launcher: most (expert, 16 tokens) of a chunk
 };
 
 hipError_t launch_mx4_quant(const Mx4QuantArgs& a, hipStream_t stream);

@@ -15,7 +15,7 @@ typedef long long ll;
 
 constexpr int64_t kMaxI32 = 0x7fffffff;
 constexpr int64_t kMaxTokens = (int64_t)1 << 21;   // 32768 chunks: the launch grid's second axis
-constexpr int64_t kMaxScaleLd = (int64_t)1 << 28;  // four rows of scale bytes in 32-bit offsets
+constexpr int64_t kMaxScaleLd = (int64_t)1 << 28;  // eight rows of scale bytes in 32-bit offsets
 
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -53,9 +53,10 @@ bs_status check_weight(const char* fn, const char* name, bs_weight_kind kind, in
             "ld of the scales of %s = %lld must be >= %lld and < 2^28 (K-major)", name, (ll)w.ld_s, (ll)cols);
     if (kind == BS_WEIGHT_E4M3_128X128)
         REQUIRE(aligned_to(w.s, 4), BS_ERR_ALIGN, "the scales of %s must be aligned to their type", name);
-    if (E > 1) {
-        REQUIRE(w.stride_q >= 0 && w.stride_s >= 0, BS_ERR_LAYOUT, "the strides of %s must not be negative", name);
-    }
+    else
+        REQUIRE(aligned16(w.s) && w.ld_s % 16 == 0 && w.stride_s % 16 == 0, BS_ERR_ALIGN,
+                "the scales of %s must be 16-byte aligned, their ld and stride multiples of 16", name);
+    if (E > 1) REQUIRE(w.stride_q >= 0 && w.stride_s >= 0, BS_ERR_LAYOUT, "the strides of %s must not be negative", name);
     return BS_OK;
 }
 

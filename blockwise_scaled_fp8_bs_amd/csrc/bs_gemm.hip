@@ -40,6 +40,7 @@
 //    The scale bytes of a K block (4 chunks x 256 rows per operand, 1 KiB)
 //    ride along with its operand tiles.
 #include "bs_device.h"
+#include "bs_dma.h"
 #include "bs_kernels.h"
 
 namespace bs {
@@ -48,7 +49,6 @@ namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int BM = 256, BN = 256, BK = 128;
@@ -310,13 +310,6 @@ __device__ __forceinline__ void resolve_tile(const GemmArgs& p, int64_t idx, int
     if (t.kb1 < t.kb0) t.kb1 = t.kb0;
 }
 
-// Raw buffer resource (gfx9 layout): offsets at or beyond `bytes` read as zero.
-__device__ __forceinline__ i32x4 make_rsrc(const void* base, int64_t bytes) {
-    const uint64_t a = reinterpret_cast<uint64_t>(base);
-    const int32_t n = bytes > 0x7fffffff ? 0x7fffffff : (bytes < 0 ? 0 : (int32_t)bytes);
-    return i32x4{(int32_t)(uint32_t)a, (int32_t)((a >> 32) & 0xffffu), n, 0x00020000};
-}
-
 // The four descriptors of one tile's operands.
 struct Operands {
     i32x4 a, b, sa, sb;
@@ -357,30 +350,6 @@ __device__ __forceinline__ Operands make_operands(const GemmArgs& p, const Tile&
     }
     return o;
 }
-
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-    return (uint32_t)(size_t)(__attribute__((address_space(3))) const char*)p;
-}
-
-// Global -> LDS copies (buffer_load ... lds): lane i's bytes land at
-// lds_base + i * size.  Issued through inline asm so that the compiler does
-// not wait for them before every LDS read of the other stage (it cannot tell
-// the two stages apart); the kernel waits for them explicitly (vmcnt(0))
-// before the barrier that publishes the stage.
-// Byte address = buffer base + voffset (per lane) + soffset (uniform).
-__device__ __forceinline__ void dma16(i32x4 rs, uint32_t lds_base, int voffset, int soffset) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(__builtin_amdgcn_readfirstlane(lds_base)), "v"(voffset), "s"(rs),
-                    "s"(__builtin_amdgcn_readfirstlane(soffset)) : "memory");
-}
-
-__device__ __forceinline__ void dma4(i32x4 rs, uint32_t lds_base, int voffset, int soffset) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                 :: "s"(__builtin_amdgcn_readfirstlane(lds_base)), "v"(voffset), "s"(rs),
-                    "s"(__builtin_amdgcn_readfirstlane(soffset)) : "memory");
-}
-
-__device__ __forceinline__ void wait_dma() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // 16-byte-chunk swizzle of a 128-byte LDS row: physical chunk = logical ^ swz(row).
 // An MFMA operand read has 16 lanes on 16 consecutive rows at one logical

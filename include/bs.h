@@ -733,10 +733,12 @@ bs_status bs_mx4_quant_1x32(const uint16_t* x, int64_t R, int64_t C, int64_t ld_
  *   x         [T, K] bf16, ld_x >= K, 0 <= T <= 2^21 (above 64 the weights are
  *             read once for every 64 rows), K >= 1
  *   w         [N, K] codes of the given kind, ld_w in bytes, a multiple of 16
- *   s         its scales, K-major with row stride ld_s in elements; no
- *             alignment but its type's.  Products of MX weights below 2^-126
- *             in magnitude may be lost, and values above the largest bf16
- *             (scale bytes that no quantizer makes) are infinite.
+ *   s         its scales, K-major with row stride ld_s in elements: float
+ *             scales aligned to their type; scale bytes 16-byte aligned, ld_s a
+ *             multiple of 16, and read (never used) up to the next multiple of
+ *             16 past the last row of w.  MX weights below 2^-126 in magnitude
+ *             may count as 0, and values above the largest bf16 (scale bytes
+ *             that no quantizer makes) are infinite.
  *   residual  [T, N] bf16 or NULL (zeros); may be out itself where that is bf16
  *   out       [T, N] bf16 or fp32, ld_out >= N; rows need no alignment (columns
  *             by fours, 8- or 16-byte aligned, are stored faster)
@@ -760,8 +762,8 @@ bs_status bs_few_mm(bs_weight_kind kind, int64_t T, int64_t N, int64_t K, const 
  *   w         [T, k] float, contiguous, or NULL (ones).  A token that names an
  *             expert twice takes it once, with the sum of the two weights.
  *   w12       [E][2H, D] codes, ld_w12 and stride_w12 (between experts) in
- *             bytes, multiples of 16; s12 its scales, stride_s12 and ld_s12 in
- *             elements
+ *             bytes, multiples of 16; s12 its scales as in bs_few_mm, stride_s12
+ *             and ld_s12 in elements (scale bytes: multiples of 16)
  *   out_proj  [E][D, H], stride_wo, ld_wo; s_out, stride_so, ld_so
  *   residual  [T, D] bf16 or NULL (zeros); may be out itself
  *   out       [T, D] bf16, ld_out >= D

@@ -60,7 +60,7 @@ def test_quantizer_of_nothing(lib):
         call(lib, "bs_mx4_quant_1x32", QUANT, kw, OK)
 
 
-MM = dict(kind=2, T=3, N=50, K=96, x=P, ld_x=96, w=P, ld_w=48, s=P, ld_s=50, res=None, ld_res=0, out=P, ld_out=50, dtype=0,
+MM = dict(kind=2, T=3, N=50, K=96, x=P, ld_x=96, w=P, ld_w=48, s=P, ld_s=64, res=None, ld_res=0, out=P, ld_out=50, dtype=0,
           stream=None)
 
 
@@ -83,7 +83,9 @@ MM = dict(kind=2, T=3, N=50, K=96, x=P, ld_x=96, w=P, ld_w=48, s=P, ld_s=50, res
     (dict(ld_w=1 << 22), LAYOUT, "2^22"),
     (dict(ld_w=56), ALIGN, "multiples of 16"),
     (dict(w=PU), ALIGN, "16-byte"),
-    (dict(ld_s=49), LAYOUT, "scales of w"),
+    (dict(ld_s=48), LAYOUT, "scales of w"),
+    (dict(ld_s=56), ALIGN, "scales of w"),
+    (dict(s=P1), ALIGN, "scales of w"),
     (dict(ld_s=1 << 28), LAYOUT, "2^28"),
     (dict(kind=1), LAYOUT, "ld of w"),
     (dict(kind=0, N=64, K=128, ld_x=128, ld_w=128, ld_out=64), SHAPE, "128"),
@@ -133,12 +135,14 @@ MOE = dict(kind=1, T=3, D=96, H=64, E=4, k=2, x=P, ld_x=96, idx=P, w=P, w12=P, s
     (dict(s12=None), NULL, "w12"),
     (dict(ld_w12=80), LAYOUT, "w12"),
     (dict(stride_w12=8), ALIGN, "w12"),
-    (dict(stride_s12=-1), LAYOUT, "w12"),
-    (dict(ld_s12=127), LAYOUT, "w12"),
+    (dict(stride_s12=-16), LAYOUT, "w12"),
+    (dict(ld_s12=112), LAYOUT, "w12"),
+    (dict(ld_s12=136), ALIGN, "w12"),
+    (dict(stride_s12=24), ALIGN, "w12"),
     (dict(wo=None), NULL, "out_proj"),
     (dict(wo=PU), ALIGN, "out_proj"),
     (dict(ld_wo=48), LAYOUT, "out_proj"),
-    (dict(ld_so=95), LAYOUT, "out_proj"),
+    (dict(ld_so=80), LAYOUT, "out_proj"),
     (dict(res=P, ld_res=95), LAYOUT, "ld_res"),
     (dict(out=None), NULL, "out is NULL"),
     (dict(out=P1), ALIGN, "out"),
