@@ -352,248 +352,346 @@ __global__ __launch_bounds__(64 * W) void few_mm_kernel(FewMmArgs a) {
 // ---------------------------------------------------------------------------
 // gated experts: h of the routed slots, then their weighted sum
 // ---------------------------------------------------------------------------
+//
+// h has a row for every token of every expert that it chose (one that it names
+// twice counts once), in the order of the experts and, within one, of the
+// tokens.  A work item is 16 of an expert's tokens at most.
 
-// A chunk's choices in LDS: for every expert the tokens that chose it, as bits
-// (one that names it twice counts once).  h lies in the order of the experts
-// and, within one, of the tokens; both kernels derive it from these bits.
-struct Choices {
-    u64* tokens;  // [E]
-    float* w;     // [slots]
-    int16_t* e;   // [slots], -1: not routed
+// What a workgroup knows of its chunk of tokens.
+struct Routing {
+    const uint32_t* item;   // [items + 1]: expert << 16 | first row of h
+    const uint8_t* token;   // [row of h]
+    const float* weight;    // [row of h]
+    int items, most;        // the largest item's tokens
 };
 
-__host__ __device__ inline int choices_bytes(int E, int slots) { return (8 * E + 6 * slots + 15) / 16 * 16; }
-
-__device__ __forceinline__ Choices choices_at(uint8_t* lds, int E, int slots) {
-    Choices c;
-    c.tokens = reinterpret_cast<u64*>(lds);
-    c.w = reinterpret_cast<float*>(lds + 8 * E);
-    c.e = reinterpret_cast<int16_t*>(lds + 8 * E + 4 * slots);
-    return c;
-}
-
-template <int THREADS>
-__device__ __forceinline__ void load_choices(const MoeFewArgs& a, int64_t t0, int slots, const Choices& c) {
-    for (int i = threadIdx.x; i < a.E; i += THREADS) c.tokens[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < slots; i += THREADS) {
-        const int32_t e = a.idx ? a.idx[t0 * a.k + i] : 0;
-        const bool routed = (uint32_t)e < (uint32_t)a.E;
-        c.e[i] = (int16_t)(routed ? e : -1);
-        c.w[i] = a.w ? a.w[t0 * a.k + i] : 1.f;
-        if (routed) atomicOr(&c.tokens[e], 1ull << (i / a.k));
+// LDS of the table of E experts and `slots` choices, in the order below.
+struct RoutingLayout {
+    int weight, w, item, e, start, token, bytes;
+    __host__ __device__ RoutingLayout(int E, int slots, int items) {
+        weight = 8 * E;                   // after the experts' tokens, as bits
+        w = weight + 4 * slots;
+        item = w + 4 * slots;
+        e = item + 4 * (items + 3);       // and the numbers of items and of rows, and the largest item's tokens
+        start = e + 2 * slots;
+        token = start + 2 * E;
+        bytes = (token + slots + 15) / 16 * 16;
     }
-    __syncthreads();
-}
-
-__device__ __forceinline__ int wave_sum(int v) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    return v;
-}
+};
 
 __device__ __forceinline__ u64 below(int lane) { return (1ull << lane) - 1; }
 
-// Workgroup: 16 columns of h of the rank-th expert that a token of the chunk
-// chose, for all its tokens, 16 at a time.
-template <int KIND, int W, int RING>
+template <int THREADS>
+__device__ __forceinline__ Routing route_chunk(const MoeFewArgs& a, int64_t t0, int slots, uint8_t* lds) {
+    const RoutingLayout at(a.E, slots, a.items);
+    u64* const chose = reinterpret_cast<u64*>(lds);
+    float* const weight = reinterpret_cast<float*>(lds + at.weight);
+    float* const w = reinterpret_cast<float*>(lds + at.w);
+    uint32_t* const item = reinterpret_cast<uint32_t*>(lds + at.item);
+    uint32_t* const found = item + a.items + 1;
+    int16_t* const expert = reinterpret_cast<int16_t*>(lds + at.e);
+    uint16_t* const start = reinterpret_cast<uint16_t*>(lds + at.start);
+    uint8_t* const token = lds + at.token;
+    const int tid = threadIdx.x, lane = tid & 63;
+    for (int i = tid; i < a.E; i += THREADS) chose[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < slots; i += THREADS) {
+        const int32_t e = a.idx ? a.idx[t0 * a.k + i] : 0;
+        const bool routed = (uint32_t)e < (uint32_t)a.E;
+        expert[i] = (int16_t)(routed ? e : -1);
+        w[i] = a.w ? a.w[t0 * a.k + i] : 1.f;
+        if (routed) atomicOr(&chose[e], 1ull << (i / a.k));
+    }
+    __syncthreads();
+    if (tid < 64) {
+        int items = 0, rows = 0, most = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 64) {
+            const int n = e0 + lane < a.E ? __popcll(chose[e0 + lane]) : 0, its = (n + 15) >> 4;
+            int upto = n | its << 16;  // both sums in one: at most 2048 rows of a chunk
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int o = __shfl_up(upto, d);
+                if (lane >= d) upto += o;
+            }
+            const int r0 = rows + (upto & 0xffff) - n, i0 = items + (upto >> 16) - its;
+            if (e0 + lane < a.E) start[e0 + lane] = (uint16_t)r0;
+            for (int j = 0; j < its; ++j) item[i0 + j] = (uint32_t)(e0 + lane) << 16 | (uint32_t)(r0 + 16 * j);
+            most = max(most, min(n, 16));
+            const int all = __shfl(upto, 63);
+            rows += all & 0xffff;
+            items += all >> 16;
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
+        if (lane == 0) {
+            item[items] = (uint32_t)rows;
+            found[0] = (uint32_t)items;
+            found[1] = (uint32_t)most;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < slots; i += THREADS) {
+        const int e = expert[i], t = i / a.k;
+        if (e < 0) continue;
+        bool first = true;
+        float sum = 0.f;
+        for (int j = t * a.k; j < (t + 1) * a.k; ++j)
+            if (expert[j] == e) {
+                first &= j >= i;
+                sum += w[j];
+            }
+        if (!first) continue;
+        const int row = start[e] + __popcll(chose[e] & below(t));
+        token[row] = (uint8_t)t;
+        weight[row] = sum;
+    }
+    __syncthreads();
+    return {item, token, weight, __builtin_amdgcn_readfirstlane((int)found[0]),
+            __builtin_amdgcn_readfirstlane((int)found[1])};
+}
+
+// The same of a single token, a table for each wave, without a barrier.
+struct OneToken {
+    uint32_t item[34];
+    float weight[32];
+    uint8_t token[32];
+};
+
+__device__ __forceinline__ Routing route_one(const MoeFewArgs& a, OneToken& t) {
+    const int lane = threadIdx.x & 63;
+    int e = lane < a.k ? (a.idx ? a.idx[lane] : 0) : -1;
+    const float w = lane < a.k ? (a.w ? a.w[lane] : 1.f) : 0.f;
+    if ((uint32_t)e >= (uint32_t)a.E) e = -1;
+    float sum = 0.f;
+    bool first = e >= 0;
+    int before = 0;  // experts in ascending order, as with more tokens
+    for (int j = 0; j < a.k; ++j) {
+        const int ej = __builtin_amdgcn_readlane(e, j);
+        const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), j));
+        if (ej == e) sum += wj, first &= j >= lane;
+        before += (uint32_t)ej < (uint32_t)e;
+    }
+    // an earlier expert that is named twice stands before once
+    for (int j = 0; j < a.k; ++j) {
+        const int ej = __builtin_amdgcn_readlane(e, j);
+        const bool again = !__builtin_amdgcn_readlane((int)first, j);
+        if (again && (uint32_t)ej < (uint32_t)e) --before;
+    }
+    const int items = __popcll(__ballot(first));
+    if (first) {
+        t.item[before] = (uint32_t)e << 16 | (uint32_t)before;
+        t.weight[before] = sum;
+        t.token[before] = 0;
+    }
+    if (lane == 0) t.item[items] = (uint32_t)items;
+    wait_lds();
+    return {t.item, t.token, t.weight, items, 1};
+}
+
+// The it-th item: its expert, first row of h and number of tokens.
+__device__ __forceinline__ int item_rows(const Routing& rt, int it, int& first, int& n) {
+    const uint32_t v = __builtin_amdgcn_readfirstlane(rt.item[it]), w = __builtin_amdgcn_readfirstlane(rt.item[it + 1]);
+    first = (int)(v & 0xffff);
+    n = min(16, (int)(w & 0xffff) - first);
+    return (int)(v >> 16);
+}
+
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+// Calls run with the tokens' places and the unit's bytes for items of `most`
+// tokens, RXMAX at most.
+template <int KIND, int RXMAX, class Run>
+__device__ __forceinline__ void with_places(int most, Run run) {
+    constexpr int kMany = KIND == kFewMx4 ? 64 : 128;
+    if (RXMAX == 1 || most <= 1) return run(Int<1>{}, Int<128>{});
+    if constexpr (RXMAX > 1) {
+        if (RXMAX == 4 || most <= 4) return run(Int<4>{}, Int<128>{});
+    }
+    if constexpr (RXMAX > 4) {
+        if (RXMAX == 8 || most <= 8) return run(Int<8>{}, Int<kMany>{});
+    }
+    if constexpr (RXMAX > 8) run(Int<16>{}, Int<kMany>{});
+}
+
+// h of one lane's four columns: weight silu(a) b, rounded once.
+__device__ __forceinline__ void store_h(const MoeFewArgs& a, int64_t row, int64_t col, float weight, f32x4 ga, f32x4 up) {
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = bf16_bits(weight * (ga[j] / (1.f + __expf(-ga[j])) * up[j]));
+    *reinterpret_cast<uint2*>(a.h + row * a.H + col) = make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
+}
+
+// Workgroup: 16 columns of h of a work item; its waves take turns along the
+// contraction.
+template <int KIND, int RXMAX, int W, int RING>
 __global__ __launch_bounds__(64 * W) void moe_few_up_kernel(MoeFewArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];
     __shared__ __attribute__((aligned(16))) uint8_t s_ring[W * RING];
-    __shared__ uint8_t s_token[W][kFewChunk];
+    __shared__ OneToken s_one[RXMAX == 1 ? W : 1];
     const int padded = (int)((a.tiles + 7) & ~7);
-    const int rank = blockIdx.x / padded, tile = xcd_tile(blockIdx.x % padded, padded);
+    const int it = blockIdx.x / padded, tile = xcd_tile(blockIdx.x % padded, padded);
     if (tile >= a.tiles) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t0 = (int64_t)blockIdx.y * kFewChunk;
     const int T = (int)(a.T - t0 < kFewChunk ? a.T - t0 : kFewChunk);
-    const Choices ch = choices_at(s_dyn, a.E, T * a.k);
-    load_choices<64 * W>(a, t0, T * a.k, ch);
-
-    // the expert, and the rows of h before its own
-    int e = -1, start = 0;
-    u64 mine = 0;
-    for (int e0 = 0, seen = 0; e0 < a.E; e0 += 64) {
-        const u64 m = e0 + lane < a.E ? ch.tokens[e0 + lane] : 0;
-        const u64 some = __ballot(m != 0);
-        const u64 hit = __ballot(m != 0 && seen + __popcll(some & below(lane)) == rank);
-        const int at = hit ? __ffsll(hit) - 1 : 64;
-        start += wave_sum(lane < at ? __popcll(m) : 0);
-        seen += __popcll(some);
-        if (hit) {
-            e = e0 + at;
-            mine = (u64)(uint32_t)__shfl((int)(uint32_t)m, at) | (u64)(uint32_t)__shfl((int)(m >> 32), at) << 32;
-            break;
-        }
-    }
-    e = __builtin_amdgcn_readfirstlane(e);
-    if (e < 0) return;
-    start = __builtin_amdgcn_readfirstlane(start);
-    const int count = __builtin_amdgcn_readfirstlane(__popcll(mine));
-    if (mine >> lane & 1) s_token[wave][__popcll(mine & below(lane))] = (uint8_t)lane;
-    wait_lds();
+    const Routing rt = RXMAX == 1 ? route_one(a, s_one[wave]) : route_chunk<64 * W>(a, t0, T * a.k, s_dyn);
+    if (it >= rt.items) return;
+    int first, n;
+    const int e = item_rows(rt, it, first, n);
 
     const int r = lane & 15, g = lane >> 4, D = (int)a.D;
     const int64_t h0 = 16 * (int64_t)tile;
     const Tile16 rows[2] = {tile_rows<KIND>(a.w12, e, h0, a.H, D), tile_rows<KIND>(a.w12, e, a.H + h0, 2 * a.H, D)};
     const i32x4 x = make_rsrc(a.x + t0 * a.ld_x, ((T - 1) * a.ld_x + D) * 2);
+    f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    with_places<KIND, RXMAX>(n, [&](auto rx, auto hb) {
+        constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value;
+        Loader<KIND, HB, 2, RX> loader;
+        loader.rows(lane, a.w12.ld_q, a.w12.ld_s, D);
+        loader.tokens([&](int c) { return c < n ? rt.token[first + c] * (int)a.ld_x * 2 : kOut; });
+        const int units = (D + Unit<KIND, HB>::kCodes - 1) / Unit<KIND, HB>::kCodes;
+        stream_units<KIND, HB, 2, RX, RING>(
+            s_ring + wave * RING, (units - wave + W - 1) / W, r, g, acc,
+            [&](int i, uint32_t lds) { loader.load(rows, x, wave + i * W, lds); }, [](int) {});
+    });
+    __syncthreads();
     f32x4* const red = reinterpret_cast<f32x4*>(s_ring);
-    for (int c0 = 0; c0 < count; c0 += 16) {
-        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        auto run = [&](auto rx, auto hb) {
-            constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value;
-            Loader<KIND, HB, 2, RX> loader;
-            loader.rows(lane, a.w12.ld_q, a.w12.ld_s, D);
-            loader.tokens([&](int c) { return c0 + c < count ? s_token[wave][c0 + c] * (int)a.ld_x * 2 : kOut; });
-            const int units = (D + Unit<KIND, HB>::kCodes - 1) / Unit<KIND, HB>::kCodes;
-            stream_units<KIND, HB, 2, RX, RING>(
-                s_ring + wave * RING, (units - wave + W - 1) / W, r, g, acc,
-                [&](int i, uint32_t lds) { loader.load(rows, x, wave + i * W, lds); }, [](int) {});
-        };
-        const int left = count - c0;
-        if (left <= 1)
-            run(std::integral_constant<int, 1>{}, std::integral_constant<int, 128>{});
-        else if (left <= 4)
-            run(std::integral_constant<int, 4>{}, std::integral_constant<int, 128>{});
-        else if (left <= 8)
-            run(std::integral_constant<int, 8>{}, std::integral_constant<int, 128>{});
-        else
-            run(std::integral_constant<int, 16>{}, std::integral_constant<int, KIND == kFewMx4 ? 64 : 128>{});
-        __syncthreads();
-        put_sums(red, wave, lane, acc);
-        __syncthreads();
-        const int c = c0 + r;
-        if (wave == 0 && c < count) {
-            const f32x4 ga = sum_waves<W, 2>(red, 0, lane), up = sum_waves<W, 2>(red, 1, lane);
-            const int t = s_token[0][c];
-            float weight = 0.f;
-            for (int j = 0; j < a.k; ++j)
-                if (ch.e[t * a.k + j] == e) weight += ch.w[t * a.k + j];
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = bf16_bits(weight * (ga[j] / (1.f + __expf(-ga[j])) * up[j]));
-            *reinterpret_cast<uint2*>(a.h + (t0 * a.k + start + c) * a.H + h0 + 4 * g) =
-                make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
-        }
-        __syncthreads();
-    }
+    put_sums(red, wave, lane, acc);
+    __syncthreads();
+    if (wave == 0 && r < n)
+        store_h(a, t0 * a.k + first + r, h0 + 4 * g, rt.weight[first + r], sum_waves<W, 2>(red, 0, lane),
+                sum_waves<W, 2>(red, 1, lane));
 }
 
-// Workgroup: 16 columns of the output of every token of the chunk.  The work
-// items, 16 tokens of an expert at most, follow one another; each wave streams
-// an equal share of their units and adds what an item gave to sums of its own
-// for every token (the weights are in h already), added up at the end in the
-// order of the waves.
-template <int KIND, int W, int RING>
+// The same where there are many tiles: every wave streams whole tiles, one
+// after the other, without a barrier; an XCD's waves walk neighbouring tiles.
+template <int KIND, int RXMAX, int W, int RING>
+__global__ __launch_bounds__(64 * W) void moe_few_up_tiles_kernel(MoeFewArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];
+    __shared__ __attribute__((aligned(16))) uint8_t s_ring[W * RING];
+    __shared__ OneToken s_one[RXMAX == 1 ? W : 1];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t0 = (int64_t)blockIdx.y * kFewChunk;
+    const int T = (int)(a.T - t0 < kFewChunk ? a.T - t0 : kFewChunk);
+    const Routing rt = RXMAX == 1 ? route_one(a, s_one[wave]) : route_chunk<64 * W>(a, t0, T * a.k, s_dyn);
+
+    const int r = lane & 15, g = lane >> 4, D = (int)a.D;
+    const i32x4 x = make_rsrc(a.x + t0 * a.ld_x, ((T - 1) * a.ld_x + D) * 2);
+    const int share = (int)((a.tiles + 7) >> 3), tile0 = (blockIdx.x & 7) * share;        // of this XCD
+    const int width = max(0, min(share, (int)a.tiles - tile0));
+    const int q0 = (blockIdx.x >> 3) * W + wave, step = (gridDim.x >> 3) * W, all = rt.items * width;
+    if (q0 >= all) return;
+    const int mine = (all - q0 + step - 1) / step;
+    with_places<KIND, RXMAX>(rt.most, [&](auto rx, auto hb) {
+        constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value;
+        const int units = (D + Unit<KIND, HB>::kCodes - 1) / Unit<KIND, HB>::kCodes;
+        Loader<KIND, HB, 2, RX> loader;
+        loader.rows(lane, a.w12.ld_q, a.w12.ld_s, D);
+        Tile16 rows[2];
+        int l_q = q0, l_u = 0;  // of the next unit to load
+        auto select = [&] {
+            const bool there = l_q < all;
+            const int q = there ? l_q : q0;
+            int first, n;
+            const int e = item_rows(rt, q / width, first, n);
+            const int64_t h0 = 16 * (int64_t)(tile0 + q % width);
+            rows[0] = tile_rows<KIND>(a.w12, e, h0, a.H, D);
+            rows[1] = tile_rows<KIND>(a.w12, e, a.H + h0, 2 * a.H, D);
+            if (!there) rows[0].q[2] = rows[1].q[2] = n = 0;
+            loader.tokens([&](int c) { return c < n ? rt.token[first + c] * (int)a.ld_x * 2 : kOut; });
+        };
+        select();
+        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        int m_q = q0, m_u = 0;  // of the next one to multiply
+        auto put = [&] {
+            int first, n;
+            item_rows(rt, m_q / width, first, n);
+            if (r < n)
+                store_h(a, t0 * a.k + first + r, 16 * (int64_t)(tile0 + m_q % width) + 4 * g, rt.weight[first + r], acc[0],
+                        acc[1]);
+            acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        };
+        stream_units<KIND, HB, 2, RX, RING>(
+            s_ring + wave * RING, mine * units, r, g, acc,
+            [&](int, uint32_t lds) {
+                loader.load(rows, x, l_u, lds);
+                if (++l_u == units) l_u = 0, l_q += step, select();
+            },
+            [&](int) {
+                if (m_u == units) put(), m_u = 0, m_q += step;
+                ++m_u;
+            });
+        put();
+    });
+}
+
+// Workgroup: 16 columns of the output of every token of the chunk.  The items'
+// units follow one another; each wave streams an equal share of them and adds
+// what an item gave to sums of its own for every token (the weights are in h
+// already), added up at the end in the order of the waves.
+template <int KIND, int RXMAX, int W, int RING>
 __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];
     __shared__ __attribute__((aligned(16))) uint8_t s_ring[W * RING];
+    __shared__ OneToken s_one[RXMAX == 1 ? W : 1];
     const int tile = xcd_tile(blockIdx.x, gridDim.x);
     if (tile >= a.tiles) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t0 = (int64_t)blockIdx.y * kFewChunk;
-    const int T = (int)(a.T - t0 < kFewChunk ? a.T - t0 : kFewChunk), slots = T * a.k;
-    const Choices ch = choices_at(s_dyn, a.E, slots);
-    uint8_t* at_lds = s_dyn + choices_bytes(a.E, slots);
-    f32x4* const sums = reinterpret_cast<f32x4*>(at_lds);  // [wave][token][4]
-    at_lds += W * T * 64;
-    uint32_t* const item = reinterpret_cast<uint32_t*>(at_lds);  // expert << 16 | rows of h before it
-    uint8_t* const token = at_lds + 4 * (a.items + 1);           // [row of h]
-    load_choices<64 * W>(a, t0, slots, ch);
-    for (int i = lane; i < T * 4; i += 64) sums[wave * T * 4 + i] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    // every wave finds the items; the first one writes them down
-    int items = 0, start = 0, most = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64) {
-        const u64 m = e0 + lane < a.E ? ch.tokens[e0 + lane] : 0;
-        const int n = __popcll(m), its = (n + 15) >> 4;
-        int n_upto = n, i_upto = its;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int on = __shfl_up(n_upto, d), oi = __shfl_up(i_upto, d);
-            if (lane >= d) n_upto += on, i_upto += oi;
-        }
-        if (wave == 0) {
-            const int s0 = start + n_upto - n, i0 = items + i_upto - its;
-            for (int j = 0; j < its; ++j) item[i0 + j] = (uint32_t)(e0 + lane) << 16 | (uint32_t)(s0 + 16 * j);
-            u64 left = m;
-            for (int p = 0; p < n; ++p, left &= left - 1) token[s0 + p] = (uint8_t)(__ffsll(left) - 1);
-        }
-        most = max(most, n);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
-        items += __shfl(i_upto, 63);
-        start += __shfl(n_upto, 63);
-    }
-    items = __builtin_amdgcn_readfirstlane(items);
-    start = __builtin_amdgcn_readfirstlane(start);
-    most = __builtin_amdgcn_readfirstlane(most);
-    if (wave == 0 && lane == 0) item[items] = (uint32_t)start;
-    __syncthreads();
+    const int T = (int)(a.T - t0 < kFewChunk ? a.T - t0 : kFewChunk);
+    f32x4* const sums = reinterpret_cast<f32x4*>(s_dyn);  // [wave][token][4]
+    f32x4* const own = sums + wave * T * 4;
+    for (int i = lane; i < T * 4; i += 64) own[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const Routing rt = RXMAX == 1 ? route_one(a, s_one[wave]) : route_chunk<64 * W>(a, t0, T * a.k, s_dyn + W * T * 64);
 
     const int r = lane & 15, g = lane >> 4, H = (int)a.H;
     const int64_t d0 = 16 * (int64_t)tile;
-    f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
-    f32x4* const own = sums + wave * T * 4;
-    auto rows_of = [&](int it, int& first, int& n) {
-        const uint32_t v = __builtin_amdgcn_readfirstlane(item[it]), w = __builtin_amdgcn_readfirstlane(item[it + 1]);
-        first = (int)(v & 0xffff);
-        n = min(16, (int)(w & 0xffff) - first);
-        return (int)(v >> 16);
-    };
-    auto run = [&](auto rx, auto hb) {
+    with_places<KIND, RXMAX>(rt.most, [&](auto rx, auto hb) {
         constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value;
         const int units = (H + Unit<KIND, HB>::kCodes - 1) / Unit<KIND, HB>::kCodes;
-        const int all = items * units, share = (all + W - 1) / W, u0 = min(all, wave * share), mine = min(share, all - u0);
+        const int all = rt.items * units, share = (all + W - 1) / W, u0 = min(all, wave * share), mine = min(share, all - u0);
+        if (mine <= 0) return;
         Loader<KIND, HB, 1, RX> loader;
         loader.rows(lane, a.wo.ld_q, a.wo.ld_s, H);
         loader.tokens([&](int c) { return c * H * 2; });  // (those past the item's are outside the buffer)
-        int l_item = u0 / units, l_u = u0 % units, l_left = mine;      // of the next unit to load
-        int m_item = l_item, m_u = l_u;                                // of the next one to multiply
+        int l_item = u0 / units, l_u = u0 % units, l_left = mine;  // of the next unit to load
+        int m_item = l_item, m_u = l_u;                            // of the next one to multiply
         Tile16 rows[1];
         i32x4 h;
         auto select = [&] {
-            int first = 0, n = 0;
             const bool there = l_left > 0;
-            const int e = rows_of(there ? l_item : 0, first, n);
-            rows[0] = tile_rows<KIND>(a.wo, there ? e : 0, d0, a.D, H);
+            int first, n;
+            const int e = item_rows(rt, there ? l_item : 0, first, n);
+            rows[0] = tile_rows<KIND>(a.wo, e, d0, a.D, H);
             h = make_rsrc(a.h + (t0 * a.k + first) * a.H, (int64_t)n * H * 2);
             if (!there) rows[0].q[2] = h[2] = 0;
         };
-        if (mine > 0) {
-            select();
-            auto put = [&](int it) {
-                int first, n;
-                rows_of(it, first, n);
-                if (r < n) {
-                    f32x4* const s = own + token[first + r] * 4 + g;
-                    const f32x4 v = *s;
-                    *s = f32x4{v[0] + acc[0][0], v[1] + acc[0][1], v[2] + acc[0][2], v[3] + acc[0][3]};
-                }
-                acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
-            };
-            stream_units<KIND, HB, 1, RX, RING>(
-                s_ring + wave * RING, mine, r, g, acc,
-                [&](int, uint32_t lds) {
-                    loader.load(rows, h, l_u, lds);
-                    --l_left;
-                    if (++l_u == units || l_left == 0) l_u = 0, ++l_item, select();
-                },
-                [&](int) {
-                    if (m_u == units) put(m_item), m_u = 0, ++m_item;
-                    ++m_u;
-                });
-            put(m_item);
-        }
-    };
-    if (most <= 1)
-        run(std::integral_constant<int, 1>{}, std::integral_constant<int, 128>{});
-    else if (most <= 4)
-        run(std::integral_constant<int, 4>{}, std::integral_constant<int, 128>{});
-    else if (most <= 8)
-        run(std::integral_constant<int, 8>{}, std::integral_constant<int, 128>{});
-    else
-        run(std::integral_constant<int, 16>{}, std::integral_constant<int, KIND == kFewMx4 ? 64 : 128>{});
+        select();
+        f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+        auto put = [&] {
+            int first, n;
+            item_rows(rt, m_item, first, n);
+            if (r < n) {
+                f32x4* const s = own + rt.token[first + r] * 4 + g;
+                const f32x4 v = *s;
+                *s = f32x4{v[0] + acc[0][0], v[1] + acc[0][1], v[2] + acc[0][2], v[3] + acc[0][3]};
+            }
+            acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
+        };
+        stream_units<KIND, HB, 1, RX, RING>(
+            s_ring + wave * RING, mine, r, g, acc,
+            [&](int, uint32_t lds) {
+                loader.load(rows, h, l_u, lds);
+                --l_left;
+                if (++l_u == units || l_left == 0) l_u = 0, ++l_item, select();
+            },
+            [&](int) {
+                if (m_u == units) put(), m_u = 0, ++m_item;
+                ++m_u;
+            });
+        put();
+    });
     __syncthreads();
     for (int i = threadIdx.x; i < T * 4; i += 64 * W) {
         const int t = i >> 2;
@@ -622,26 +720,40 @@ template <int KIND>
 hipError_t mm_kind(const FewMmArgs& a, hipStream_t stream) {
     if (a.T <= 1) return mm<KIND, 128, 1, 8, 9728>(a, stream);
     if (a.T <= 4) return mm<KIND, 128, 4, 8, 9728>(a, stream);
-    if (a.T <= 8) return mm<KIND, 128, 8, 8, 14336>(a, stream);
-    return mm<KIND, KIND == kFewMx4 ? 64 : 128, 16, 8, 14336>(a, stream);
+    if (a.T <= 8) return mm<KIND, KIND == kFewMx4 ? 64 : 128, 8, 8, 9728>(a, stream);
+    return mm<KIND, KIND == kFewMx4 ? 64 : 128, 16, 4, 19200>(a, stream);
 }
 
-template <int KIND>
-hipError_t moe_kind(MoeFewArgs a, hipStream_t stream) {
-    constexpr int WU = 4, WD = 8;
+// Workgroups of at most 80 KiB: two on a CU.
+template <int KIND, int RXMAX, int WD, int RING_D>
+hipError_t moe(MoeFewArgs a, hipStream_t stream) {
+    constexpr int WU = 4, RING_U = 19200;
     const int64_t chunks = (a.T + kFewChunk - 1) / kFewChunk, tokens = a.T < kFewChunk ? a.T : kFewChunk;
-    const int64_t slots = tokens * a.k, ranks = slots < a.E ? slots : a.E;
+    const int slots = (int)(tokens * a.k);
+    a.items = (slots < a.E ? slots : a.E) + slots / 16;
+    const int table = RXMAX == 1 ? 0 : RoutingLayout(a.E, slots, a.items).bytes;
     a.tiles = (a.H + 15) / 16;
     const int64_t padded = (a.tiles + 7) & ~7;
-    hipLaunchKernelGGL((moe_few_up_kernel<KIND, WU, 19200>), dim3((unsigned)(ranks * padded), (unsigned)chunks), dim3(64 * WU),
-                       choices_bytes(a.E, (int)slots), stream, a);
+    if (a.items * a.tiles >= 4096)
+        hipLaunchKernelGGL((moe_few_up_tiles_kernel<KIND, RXMAX, WU, RING_U>), dim3(512, (unsigned)chunks), dim3(64 * WU), table,
+                           stream, a);
+    else
+        hipLaunchKernelGGL((moe_few_up_kernel<KIND, RXMAX, WU, RING_U>), dim3((unsigned)(a.items * padded), (unsigned)chunks),
+                           dim3(64 * WU), table, stream, a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     a.tiles = (a.D + 15) / 16;
-    a.items = (int32_t)(ranks + slots / 16);
-    hipLaunchKernelGGL((moe_few_down_kernel<KIND, WD, 12800>), dim3((unsigned)((a.tiles + 7) & ~7), (unsigned)chunks),
-                       dim3(64 * WD), choices_bytes(a.E, (int)slots) + WD * tokens * 64 + 4 * (a.items + 1) + slots, stream, a);
+    hipLaunchKernelGGL((moe_few_down_kernel<KIND, RXMAX, WD, RING_D>), dim3((unsigned)((a.tiles + 7) & ~7), (unsigned)chunks),
+                       dim3(64 * WD), table + WD * tokens * 64, stream, a);
     return hipGetLastError();
+}
+
+template <int KIND>
+hipError_t moe_kind(const MoeFewArgs& a, hipStream_t stream) {
+    if (a.T <= 1) return moe<KIND, 1, 8, 9728>(a, stream);
+    if (a.T <= 4) return moe<KIND, 4, 8, 9728>(a, stream);
+    if (a.T <= 8) return moe<KIND, 8, 8, 9728>(a, stream);
+    return moe<KIND, 16, 4, 19200>(a, stream);
 }
 
 }  // namespace
