@@ -33,8 +33,8 @@ typedef unsigned long long u64;
 
 constexpr int kOut = 0x70000000;  // an offset past every buffer: reads zero
 
-// A unit: HB bytes along each of 16 rows of codes (128; 64 for e2m1 beside many
-// tokens, whose values would fill the ring).
+// A unit: HB bytes along each of 16 rows of codes, 128, or 64 beside many
+// tokens, whose values would fill the ring.
 template <int KIND, int HB>
 struct Unit {
     static constexpr int kCodes = KIND == kFewMx4 ? 2 * HB : HB;   // along the contraction
@@ -118,7 +118,7 @@ struct Loader {
                 dma16(tile[n].q, lds + n * S::kTile + i * 1024, in ? row[i] : kOut, at);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const uint8_t* const s = tile[n].s + (int64_t)u * U::kBlocks * ld_s;
+            const uint8_t* const s = tile[n].s + (KIND == kFewE4m3 ? at / 128 : u * U::kBlocks) * ld_s;
             if (KIND == kFewE4m3) {
                 const i32x4 rs = make_rsrc(s, u * HB < row_bytes && tile[n].q[2] > 0 ? 4 : 0);
                 if (lane == 0) dma4(rs, lds + S::kScaleAt + n * S::kScales, 0, 0);
@@ -169,7 +169,8 @@ template <int KIND, int HB, int NT, int RX>
 struct Operands {
     using U = Unit<KIND, HB>;
     using S = Stage<KIND, HB, NT, RX>;
-    u32x4 a[NT][U::kHalves], x[U::kSteps];
+    static constexpr int TT = RX > 16 ? RX / 16 : 1;  // tiles of tokens
+    u32x4 a[NT][U::kHalves], x[TT][U::kSteps];
     uint32_t s[NT][U::kHalves];
     float sc[NT];
 
@@ -179,12 +180,15 @@ struct Operands {
 #pragma unroll
             for (int h = 0; h < U::kHalves; ++h)
                 a[n][h] = *reinterpret_cast<const u32x4*>(stage + n * S::kTile + r * HB + 16 * ((4 * h + g) ^ U::key(r)));
-        const int t = r & (RX - 1);  // the columns past the tokens are not used
 #pragma unroll
-        for (int f = 0; f < U::kSteps; ++f) {
-            constexpr int per = U::kSteps / U::kHalves;  // steps, and 16-byte pieces of tokens, of a piece of codes
-            const int p = (4 * (f / per) + g) * per + f % per;
-            x[f] = *reinterpret_cast<const u32x4*>(stage + S::kTokenAt + t * U::kTokenRow + 16 * (p ^ (t & 7)));
+        for (int t = 0; t < TT; ++t) {
+            const int row = 16 * t + (RX < 16 ? r & (RX - 1) : r);  // the columns past the tokens are not used
+#pragma unroll
+            for (int f = 0; f < U::kSteps; ++f) {
+                constexpr int per = U::kSteps / U::kHalves;  // steps, and 16-byte pieces of tokens, of a piece of codes
+                const int p = (4 * (f / per) + g) * per + f % per;
+                x[t][f] = *reinterpret_cast<const u32x4*>(stage + S::kTokenAt + row * U::kTokenRow + 16 * (p ^ (row & 7)));
+            }
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -199,16 +203,24 @@ struct Operands {
         }
     }
 
-    __device__ __forceinline__ void multiply(f32x4 (&acc)[NT]) const {
+    __device__ __forceinline__ void multiply(f32x4 (&acc)[NT][TT]) const {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            f32x4 p = KIND == kFewE4m3 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[n];
+            f32x4 p[TT];
 #pragma unroll
-            for (int f = 0; f < U::kSteps; ++f)
-                p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(weights<KIND>(a[n], s[n], f), __builtin_bit_cast(bf16x8, x[f]), p, 0,
-                                                            0, 0);
+            for (int t = 0; t < TT; ++t) p[t] = KIND == kFewE4m3 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[n][t];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] = KIND == kFewE4m3 ? __builtin_fmaf(p[i], sc[n], acc[n][i]) : p[i];
+            for (int f = 0; f < U::kSteps; ++f) {
+                const bf16x8 w = weights<KIND>(a[n], s[n], f);
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+                    p[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, x[t][f]), p[t], 0, 0, 0);
+            }
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[n][t][i] = KIND == kFewE4m3 ? __builtin_fmaf(p[t][i], sc[n], acc[n][t][i]) : p[t][i];
         }
     }
 };
@@ -223,8 +235,8 @@ __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 // Streams `units` units through the wave's ring: load(i, lds) starts the loads
 // of the wave's i-th unit (also of those past the end, which read zeros and
 // keep the count), before(i) runs ahead of its products.
-template <int KIND, int HB, int NT, int RX, int RING, class Load, class Before>
-__device__ __forceinline__ void stream_units(const uint8_t* ring, int units, int r, int g, f32x4 (&acc)[NT], Load load,
+template <int KIND, int HB, int NT, int RX, int RING, int TT, class Load, class Before>
+__device__ __forceinline__ void stream_units(const uint8_t* ring, int units, int r, int g, f32x4 (&acc)[NT][TT], Load load,
                                              Before before) {
     using S = Stage<KIND, HB, NT, RX>;
     constexpr int DEPTH = ring_stages(RING, S::kBytes);
@@ -260,20 +272,30 @@ __device__ __forceinline__ Tile16 tile_rows(const FewWeight& w, int64_t e, int64
     return t;
 }
 
-// Each wave's sums into LDS: red[wave][n][lane].
-template <int NT>
-__device__ __forceinline__ void put_sums(f32x4* red, int wave, int lane, const f32x4 (&acc)[NT]) {
+template <int NT, int TT>
+__device__ __forceinline__ void zero(f32x4 (&acc)[NT][TT]) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) red[(wave * NT + n) * 64 + lane] = acc[n];
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[n][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
+// Each wave's sums into LDS: red[wave][n][t][lane].
+template <int NT, int TT>
+__device__ __forceinline__ void put_sums(f32x4* red, int wave, int lane, const f32x4 (&acc)[NT][TT]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) red[((wave * NT + n) * TT + t) * 64 + lane] = acc[n][t];
 }
 
 // The waves' sums of one lane's place in a tile, in the order of the waves.
-template <int W, int NT>
-__device__ __forceinline__ f32x4 sum_waves(const f32x4* red, int n, int lane) {
-    f32x4 v = red[n * 64 + lane];
+template <int W, int TILES>
+__device__ __forceinline__ f32x4 sum_waves(const f32x4* red, int tile, int lane) {
+    f32x4 v = red[tile * 64 + lane];
 #pragma unroll
     for (int w = 1; w < W; ++w) {
-        const f32x4 o = red[(w * NT + n) * 64 + lane];
+        const f32x4 o = red[(w * TILES + tile) * 64 + lane];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] += o[i];
     }
@@ -316,37 +338,45 @@ __device__ __forceinline__ int xcd_tile(int b, int padded) { return (b & 7) * (p
 // out = residual + x W^T
 // ---------------------------------------------------------------------------
 
-// Workgroup: 16 columns of up to RX rows; its waves take turns along the
+// Workgroup: 16 NT columns of up to RX rows; its waves take turns along the
 // contraction.
-template <int KIND, int HB, int RX, int W, int RING>
+template <int KIND, int HB, int NT, int RX, int W, int RING>
 __global__ __launch_bounds__(64 * W) void few_mm_kernel(FewMmArgs a) {
+    constexpr int TT = RX > 16 ? RX / 16 : 1;
+    static_assert(RING >= NT * TT * 1024, "the sums take the ring's place");
     __shared__ __attribute__((aligned(16))) uint8_t s_ring[W * RING];
     const int tile = xcd_tile(blockIdx.x, gridDim.x);
     if (tile >= a.tiles) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int64_t t0 = (int64_t)blockIdx.y * RX, row0 = (int64_t)tile * 16;
+    const int64_t t0 = (int64_t)blockIdx.y * RX, row0 = (int64_t)tile * (16 * NT);
     const int T = (int)(a.T - t0 < RX ? a.T - t0 : RX), K = (int)a.K;
     const i32x4 x = make_rsrc(a.x + t0 * a.ld_x, ((T - 1) * a.ld_x + K) * 2);
-    const Tile16 rows[1] = {tile_rows<KIND>(a.w, 0, row0, a.N, K)};
-    Loader<KIND, HB, 1, RX> loader;
+    Tile16 rows[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) rows[n] = tile_rows<KIND>(a.w, 0, row0 + 16 * n, a.N, K);
+    Loader<KIND, HB, NT, RX> loader;
     loader.rows(lane, a.w.ld_q, a.w.ld_s, K);
     loader.tokens([&](int c) { return c < T ? c * (int)a.ld_x * 2 : kOut; });
     const int units = (K + Unit<KIND, HB>::kCodes - 1) / Unit<KIND, HB>::kCodes;
-    f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
-    stream_units<KIND, HB, 1, RX, RING>(
+    f32x4 acc[NT][TT];
+    zero(acc);
+    stream_units<KIND, HB, NT, RX, RING>(
         s_ring + wave * RING, (units - wave + W - 1) / W, r, g, acc,
         [&](int i, uint32_t lds) { loader.load(rows, x, wave + i * W, lds); }, [](int) {});
     __syncthreads();
     f32x4* const red = reinterpret_cast<f32x4*>(s_ring);
     put_sums(red, wave, lane, acc);
     __syncthreads();
-    const int64_t n = row0 + 4 * g;
-    if (wave != 0 || r >= T || n >= a.N) return;
-    const int64_t at = (t0 + r) * a.ld_out + n;
-    store4(sum_waves<W, 1>(red, 0, lane), a.residual ? a.residual + (t0 + r) * a.ld_res + n : nullptr,
-           a.f32 ? (void*)(static_cast<float*>(a.out) + at) : (void*)(static_cast<uint16_t*>(a.out) + at), a.f32, a.vec,
-           (int)(a.N - n < 4 ? a.N - n : 4));
+    for (int i = wave; i < NT * TT; i += W) {
+        const int64_t n = row0 + 16 * (i / TT) + 4 * g;
+        const int t = 16 * (i % TT) + r;
+        if (t >= T || n >= a.N) continue;
+        const int64_t at = (t0 + t) * a.ld_out + n;
+        store4(sum_waves<W, NT * TT>(red, i, lane), a.residual ? a.residual + (t0 + t) * a.ld_res + n : nullptr,
+               a.f32 ? (void*)(static_cast<float*>(a.out) + at) : (void*)(static_cast<uint16_t*>(a.out) + at), a.f32, a.vec,
+               (int)(a.N - n < 4 ? a.N - n : 4));
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -544,7 +574,8 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_kernel(MoeFewArgs a) {
     const int64_t h0 = 16 * (int64_t)tile;
     const Tile16 rows[2] = {tile_rows<KIND>(a.w12, e, h0, a.H, D), tile_rows<KIND>(a.w12, e, a.H + h0, 2 * a.H, D)};
     const i32x4 x = make_rsrc(a.x + t0 * a.ld_x, ((T - 1) * a.ld_x + D) * 2);
-    f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    f32x4 acc[2][1];
+    zero(acc);
     with_places<KIND, RXMAX>(n, [&](auto rx, auto hb) {
         constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value;
         Loader<KIND, HB, 2, RX> loader;
@@ -602,15 +633,16 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_tiles_kernel(MoeFewArgs a) 
             loader.tokens([&](int c) { return c < n ? rt.token[first + c] * (int)a.ld_x * 2 : kOut; });
         };
         select();
-        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        f32x4 acc[2][1];
+        zero(acc);
         int m_q = q0, m_u = 0;  // of the next one to multiply
         auto put = [&] {
             int first, n;
             item_rows(rt, m_q / width, first, n);
             if (r < n)
-                store_h(a, t0 * a.k + first + r, 16 * (int64_t)(tile0 + m_q % width) + 4 * g, rt.weight[first + r], acc[0],
-                        acc[1]);
-            acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+                store_h(a, t0 * a.k + first + r, 16 * (int64_t)(tile0 + m_q % width) + 4 * g, rt.weight[first + r],
+                        acc[0][0], acc[1][0]);
+            zero(acc);
         };
         stream_units<KIND, HB, 2, RX, RING>(
             s_ring + wave * RING, mine * units, r, g, acc,
@@ -668,16 +700,18 @@ __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
             if (!there) rows[0].q[2] = h[2] = 0;
         };
         select();
-        f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+        f32x4 acc[1][1];
+        zero(acc);
         auto put = [&] {
             int first, n;
             item_rows(rt, m_item, first, n);
             if (r < n) {
                 f32x4* const s = own + rt.token[first + r] * 4 + g;
                 const f32x4 v = *s;
-                *s = f32x4{v[0] + acc[0][0], v[1] + acc[0][1], v[2] + acc[0][2], v[3] + acc[0][3]};
+                const f32x4 p = acc[0][0];
+                *s = f32x4{v[0] + p[0], v[1] + p[1], v[2] + p[2], v[3] + p[3]};
             }
-            acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
+            zero(acc);
         };
         stream_units<KIND, HB, 1, RX, RING>(
             s_ring + wave * RING, mine, r, g, acc,
@@ -708,20 +742,23 @@ __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
     }
 }
 
-template <int KIND, int HB, int RX, int W, int RING>
+template <int KIND, int HB, int NT, int RX, int W, int RING>
 hipError_t mm(FewMmArgs a, hipStream_t stream) {
-    a.tiles = (a.N + 15) / 16;
+    a.tiles = (a.N + 16 * NT - 1) / (16 * NT);
     const dim3 grid((unsigned)((a.tiles + 7) & ~7), (unsigned)((a.T + RX - 1) / RX));
-    hipLaunchKernelGGL((few_mm_kernel<KIND, HB, RX, W, RING>), grid, dim3(64 * W), 0, stream, a);
+    hipLaunchKernelGGL((few_mm_kernel<KIND, HB, NT, RX, W, RING>), grid, dim3(64 * W), 0, stream, a);
     return hipGetLastError();
 }
 
 template <int KIND>
 hipError_t mm_kind(const FewMmArgs& a, hipStream_t stream) {
-    if (a.T <= 1) return mm<KIND, 128, 1, 8, 9728>(a, stream);
-    if (a.T <= 4) return mm<KIND, 128, 4, 8, 9728>(a, stream);
-    if (a.T <= 8) return mm<KIND, KIND == kFewMx4 ? 64 : 128, 8, 8, 9728>(a, stream);
-    return mm<KIND, KIND == kFewMx4 ? 64 : 128, 16, 4, 19200>(a, stream);
+    constexpr int kMany = KIND == kFewMx4 ? 64 : 128;
+    if (a.T <= 1) return mm<KIND, 128, 1, 1, 8, 9728>(a, stream);
+    if (a.T <= 4) return mm<KIND, 128, 1, 4, 8, 9728>(a, stream);
+    if (a.T <= 8) return mm<KIND, kMany, 1, 8, 8, 9728>(a, stream);
+    if (a.T <= 16) return mm<KIND, kMany, 1, 16, 4, 19200>(a, stream);
+    if (a.T <= 32) return mm<KIND, 64, 2, 32, 4, 40960>(a, stream);
+    return mm<KIND, 64, 2, 64, 4, 40960>(a, stream);
 }
 
 // Workgroups of at most 80 KiB: two on a CU.
