@@ -65,8 +65,7 @@ constexpr int ring_stages(int ring, int stage) { return ring / stage < 6 ? ring 
 
 // 16 rows of weights.
 struct Tile16 {
-    i32x4 q;           // their codes
-    const uint8_t* s;  // their scales' first byte
+    i32x4 q, s;  // their codes and scales
 };
 
 // The units of a wave: weights' row pieces and tokens' pieces of its lanes.
@@ -77,14 +76,13 @@ struct Loader {
     int lane, piece;               // 16-byte piece of the row that the lane fetches, in bytes
     int row[S::kTileLoads];        // offset of its row and piece
     int token[S::kCopies];         // offset of its token and piece (kOut: none)
-    int K, row_bytes;
-    int64_t ld_s;                  // bytes
+    int K, row_bytes, ld_s;        // (ld_s in bytes: the scales of a matrix are below 2^31)
 
     __device__ __forceinline__ void rows(int lane_, int64_t ld_q, int64_t ld_s_, int K_) {
         lane = lane_;
         K = K_;
         row_bytes = KIND == kFewMx4 ? K / 2 : K;
-        ld_s = KIND == kFewE4m3 ? 4 * ld_s_ : ld_s_;
+        ld_s = (int)(KIND == kFewE4m3 ? 4 * ld_s_ : ld_s_);
         constexpr int per = 64 / U::kPieces;  // rows of a load
 #pragma unroll
         for (int i = 0; i < S::kTileLoads; ++i) {
@@ -118,14 +116,11 @@ struct Loader {
                 dma16(tile[n].q, lds + n * S::kTile + i * 1024, in ? row[i] : kOut, at);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const uint8_t* const s = tile[n].s + (KIND == kFewE4m3 ? at / 128 : u * U::kBlocks) * ld_s;
             if (KIND == kFewE4m3) {
-                const i32x4 rs = make_rsrc(s, u * HB < row_bytes && tile[n].q[2] > 0 ? 4 : 0);
-                if (lane == 0) dma4(rs, lds + S::kScaleAt + n * S::kScales, 0, 0);
+                if (lane == 0) dma4(tile[n].s, lds + S::kScaleAt + n * S::kScales, 0, at / 128 * ld_s);
             } else {
-                const int64_t left = K / 32 - (int64_t)u * U::kBlocks;
-                const i32x4 rs = make_rsrc(s, tile[n].q[2] > 0 && left > 0 ? (left - 1) * ld_s + 16 : 0);
-                if (lane < U::kBlocks) dma16(rs, lds + S::kScaleAt + n * S::kScales, lane * (int)ld_s, 0);
+                if (lane < U::kBlocks)
+                    dma16(tile[n].s, lds + S::kScaleAt + n * S::kScales, lane * ld_s, u * U::kBlocks * ld_s);
             }
         }
         const int xat = u * U::kTokenRow;
@@ -262,13 +257,18 @@ __device__ __forceinline__ void stream_units(const uint8_t* ring, int units, int
     wait_loads<0>();
 }
 
+// Rows row0 .. of the N of expert e; `there` false: nothing, all of it reads zeros.
 template <int KIND>
-__device__ __forceinline__ Tile16 tile_rows(const FewWeight& w, int64_t e, int64_t row0, int64_t N, int K) {
+__device__ __forceinline__ Tile16 tile_rows(const FewWeight& w, int64_t e, int64_t row0, int64_t N, int K, bool there = true) {
     const int row_bytes = KIND == kFewMx4 ? K / 2 : K;
     const int64_t rows = N - row0 < 16 ? N - row0 : 16;
+    there &= rows > 0;
     Tile16 t;
-    t.q = make_rsrc(w.q + e * w.stride_q + row0 * w.ld_q, rows > 0 ? (rows - 1) * w.ld_q + row_bytes : 0);
-    t.s = static_cast<const uint8_t*>(w.s) + (KIND == kFewE4m3 ? 4 * (e * w.stride_s + row0 / 128) : e * w.stride_s + row0);
+    t.q = make_rsrc(w.q + e * w.stride_q + row0 * w.ld_q, there ? (rows - 1) * w.ld_q + row_bytes : 0);
+    if (KIND == kFewE4m3)
+        t.s = make_rsrc(static_cast<const float*>(w.s) + e * w.stride_s + row0 / 128, there ? ((K / 128 - 1) * w.ld_s + 1) * 4 : 0);
+    else
+        t.s = make_rsrc(static_cast<const uint8_t*>(w.s) + e * w.stride_s + row0, there ? (K / 32 - 1) * w.ld_s + 16 : 0);
     return t;
 }
 
@@ -385,7 +385,8 @@ __global__ __launch_bounds__(64 * W) void few_mm_kernel(FewMmArgs a) {
 //
 // h has a row for every token of every expert that it chose (one that it names
 // twice counts once), in the order of the experts and, within one, of the
-// tokens.  A work item is 16 of an expert's tokens at most.
+// tokens.  A work item is 16 of an expert's tokens at most, 32 where most
+// experts have more than that.
 
 // What a workgroup knows of its chunk of tokens.
 struct Routing {
@@ -395,33 +396,37 @@ struct Routing {
     int items, most;        // the largest item's tokens
 };
 
-// LDS of the table of E experts and `slots` choices, in the order below.
+// LDS of the table for `slots` choices and `items` items, and what making it
+// takes besides: the ring's place.
 struct RoutingLayout {
-    int weight, w, item, e, start, token, bytes;
+    int weight, item, token, bytes;        // the table
+    int chose, w, e, start, scratch;       // the experts' tokens as bits, and the choices
     __host__ __device__ RoutingLayout(int E, int slots, int items) {
-        weight = 8 * E;                   // after the experts' tokens, as bits
-        w = weight + 4 * slots;
-        item = w + 4 * slots;
-        e = item + 4 * (items + 3);       // and the numbers of items and of rows, and the largest item's tokens
-        start = e + 2 * slots;
-        token = start + 2 * E;
+        weight = 0;
+        item = 4 * slots;
+        token = item + 4 * (items + 3);    // and the numbers of items and the largest one's tokens
         bytes = (token + slots + 15) / 16 * 16;
+        chose = 0;
+        w = 8 * E;
+        e = w + 4 * slots;
+        start = e + 2 * slots;
+        scratch = start + 2 * E;
     }
 };
 
 __device__ __forceinline__ u64 below(int lane) { return (1ull << lane) - 1; }
 
-template <int THREADS>
-__device__ __forceinline__ Routing route_chunk(const MoeFewArgs& a, int64_t t0, int slots, uint8_t* lds) {
+template <int PER, int THREADS>
+__device__ __forceinline__ Routing route_chunk(const MoeFewArgs& a, int64_t t0, int slots, uint8_t* lds, uint8_t* scratch) {
     const RoutingLayout at(a.E, slots, a.items);
-    u64* const chose = reinterpret_cast<u64*>(lds);
     float* const weight = reinterpret_cast<float*>(lds + at.weight);
-    float* const w = reinterpret_cast<float*>(lds + at.w);
     uint32_t* const item = reinterpret_cast<uint32_t*>(lds + at.item);
     uint32_t* const found = item + a.items + 1;
-    int16_t* const expert = reinterpret_cast<int16_t*>(lds + at.e);
-    uint16_t* const start = reinterpret_cast<uint16_t*>(lds + at.start);
     uint8_t* const token = lds + at.token;
+    u64* const chose = reinterpret_cast<u64*>(scratch + at.chose);
+    float* const w = reinterpret_cast<float*>(scratch + at.w);
+    int16_t* const expert = reinterpret_cast<int16_t*>(scratch + at.e);
+    uint16_t* const start = reinterpret_cast<uint16_t*>(scratch + at.start);
     const int tid = threadIdx.x, lane = tid & 63;
     for (int i = tid; i < a.E; i += THREADS) chose[i] = 0;
     __syncthreads();
@@ -436,7 +441,7 @@ __device__ __forceinline__ Routing route_chunk(const MoeFewArgs& a, int64_t t0, 
     if (tid < 64) {
         int items = 0, rows = 0, most = 0;
         for (int e0 = 0; e0 < a.E; e0 += 64) {
-            const int n = e0 + lane < a.E ? __popcll(chose[e0 + lane]) : 0, its = (n + 15) >> 4;
+            const int n = e0 + lane < a.E ? __popcll(chose[e0 + lane]) : 0, its = (n + PER - 1) / PER;
             int upto = n | its << 16;  // both sums in one: at most 2048 rows of a chunk
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
@@ -445,8 +450,8 @@ __device__ __forceinline__ Routing route_chunk(const MoeFewArgs& a, int64_t t0, 
             }
             const int r0 = rows + (upto & 0xffff) - n, i0 = items + (upto >> 16) - its;
             if (e0 + lane < a.E) start[e0 + lane] = (uint16_t)r0;
-            for (int j = 0; j < its; ++j) item[i0 + j] = (uint32_t)(e0 + lane) << 16 | (uint32_t)(r0 + 16 * j);
-            most = max(most, min(n, 16));
+            for (int j = 0; j < its; ++j) item[i0 + j] = (uint32_t)(e0 + lane) << 16 | (uint32_t)(r0 + PER * j);
+            most = max(most, min(n, PER));
             const int all = __shfl(upto, 63);
             rows += all & 0xffff;
             items += all >> 16;
@@ -519,15 +524,19 @@ __device__ __forceinline__ Routing route_one(const MoeFewArgs& a, OneToken& t) {
 }
 
 // The it-th item: its expert, first row of h and number of tokens.
+template <int PER>
 __device__ __forceinline__ int item_rows(const Routing& rt, int it, int& first, int& n) {
     const uint32_t v = __builtin_amdgcn_readfirstlane(rt.item[it]), w = __builtin_amdgcn_readfirstlane(rt.item[it + 1]);
     first = (int)(v & 0xffff);
-    n = min(16, (int)(w & 0xffff) - first);
+    n = min(PER, (int)(w & 0xffff) - first);
     return (int)(v >> 16);
 }
 
 template <int V>
 using Int = std::integral_constant<int, V>;
+
+// Tokens of an item, at most, in kernels for RXMAX tokens.
+constexpr int item_tokens(int rxmax) { return rxmax > 16 ? rxmax : 16; }
 
 // Calls run with the tokens' places and the unit's bytes for items of `most`
 // tokens, RXMAX at most.
@@ -541,7 +550,10 @@ __device__ __forceinline__ void with_places(int most, Run run) {
     if constexpr (RXMAX > 4) {
         if (RXMAX == 8 || most <= 8) return run(Int<8>{}, Int<kMany>{});
     }
-    if constexpr (RXMAX > 8) run(Int<16>{}, Int<kMany>{});
+    if constexpr (RXMAX > 8) {
+        if (RXMAX == 16 || most <= 16) return run(Int<16>{}, Int<kMany>{});
+    }
+    if constexpr (RXMAX > 16) run(Int<32>{}, Int<64>{});
 }
 
 // h of one lane's four columns: weight silu(a) b, rounded once.
@@ -556,6 +568,7 @@ __device__ __forceinline__ void store_h(const MoeFewArgs& a, int64_t row, int64_
 // contraction.
 template <int KIND, int RXMAX, int W, int RING>
 __global__ __launch_bounds__(64 * W) void moe_few_up_kernel(MoeFewArgs a) {
+    constexpr int PER = item_tokens(RXMAX);
     extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];
     __shared__ __attribute__((aligned(16))) uint8_t s_ring[W * RING];
     __shared__ OneToken s_one[RXMAX == 1 ? W : 1];
@@ -565,57 +578,60 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_kernel(MoeFewArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t0 = (int64_t)blockIdx.y * kFewChunk;
     const int T = (int)(a.T - t0 < kFewChunk ? a.T - t0 : kFewChunk);
-    const Routing rt = RXMAX == 1 ? route_one(a, s_one[wave]) : route_chunk<64 * W>(a, t0, T * a.k, s_dyn);
+    const Routing rt = RXMAX == 1 ? route_one(a, s_one[wave]) : route_chunk<PER, 64 * W>(a, t0, T * a.k, s_dyn, s_ring);
     if (it >= rt.items) return;
     int first, n;
-    const int e = item_rows(rt, it, first, n);
+    const int e = item_rows<PER>(rt, it, first, n);
 
     const int r = lane & 15, g = lane >> 4, D = (int)a.D;
     const int64_t h0 = 16 * (int64_t)tile;
     const Tile16 rows[2] = {tile_rows<KIND>(a.w12, e, h0, a.H, D), tile_rows<KIND>(a.w12, e, a.H + h0, 2 * a.H, D)};
     const i32x4 x = make_rsrc(a.x + t0 * a.ld_x, ((T - 1) * a.ld_x + D) * 2);
-    f32x4 acc[2][1];
-    zero(acc);
     with_places<KIND, RXMAX>(n, [&](auto rx, auto hb) {
-        constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value;
+        constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value, TT = RX > 16 ? RX / 16 : 1;
+        static_assert(RING >= 2 * TT * 1024, "the sums take the ring's place");
         Loader<KIND, HB, 2, RX> loader;
         loader.rows(lane, a.w12.ld_q, a.w12.ld_s, D);
         loader.tokens([&](int c) { return c < n ? rt.token[first + c] * (int)a.ld_x * 2 : kOut; });
         const int units = (D + Unit<KIND, HB>::kCodes - 1) / Unit<KIND, HB>::kCodes;
+        f32x4 acc[2][TT];
+        zero(acc);
         stream_units<KIND, HB, 2, RX, RING>(
             s_ring + wave * RING, (units - wave + W - 1) / W, r, g, acc,
             [&](int i, uint32_t lds) { loader.load(rows, x, wave + i * W, lds); }, [](int) {});
+        __syncthreads();
+        f32x4* const red = reinterpret_cast<f32x4*>(s_ring);
+        put_sums(red, wave, lane, acc);
+        __syncthreads();
+        const int c = 16 * wave + r;
+        if (wave < TT && c < n)
+            store_h(a, t0 * a.k + first + c, h0 + 4 * g, rt.weight[first + c], sum_waves<W, 2 * TT>(red, wave, lane),
+                    sum_waves<W, 2 * TT>(red, TT + wave, lane));
     });
-    __syncthreads();
-    f32x4* const red = reinterpret_cast<f32x4*>(s_ring);
-    put_sums(red, wave, lane, acc);
-    __syncthreads();
-    if (wave == 0 && r < n)
-        store_h(a, t0 * a.k + first + r, h0 + 4 * g, rt.weight[first + r], sum_waves<W, 2>(red, 0, lane),
-                sum_waves<W, 2>(red, 1, lane));
 }
 
 // The same where there are many tiles: every wave streams whole tiles, one
 // after the other, without a barrier; an XCD's waves walk neighbouring tiles.
 template <int KIND, int RXMAX, int W, int RING>
 __global__ __launch_bounds__(64 * W) void moe_few_up_tiles_kernel(MoeFewArgs a) {
+    constexpr int PER = item_tokens(RXMAX);
     extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];
     __shared__ __attribute__((aligned(16))) uint8_t s_ring[W * RING];
     __shared__ OneToken s_one[RXMAX == 1 ? W : 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t0 = (int64_t)blockIdx.y * kFewChunk;
     const int T = (int)(a.T - t0 < kFewChunk ? a.T - t0 : kFewChunk);
-    const Routing rt = RXMAX == 1 ? route_one(a, s_one[wave]) : route_chunk<64 * W>(a, t0, T * a.k, s_dyn);
+    const Routing rt = RXMAX == 1 ? route_one(a, s_one[wave]) : route_chunk<PER, 64 * W>(a, t0, T * a.k, s_dyn, s_ring);
 
     const int r = lane & 15, g = lane >> 4, D = (int)a.D;
     const i32x4 x = make_rsrc(a.x + t0 * a.ld_x, ((T - 1) * a.ld_x + D) * 2);
-    const int share = (int)((a.tiles + 7) >> 3), tile0 = (blockIdx.x & 7) * share;        // of this XCD
+    const int share = (int)((a.tiles + 7) >> 3), tile0 = (blockIdx.x & 7) * share;  // of this XCD
     const int width = max(0, min(share, (int)a.tiles - tile0));
     const int q0 = (blockIdx.x >> 3) * W + wave, step = (gridDim.x >> 3) * W, all = rt.items * width;
     if (q0 >= all) return;
     const int mine = (all - q0 + step - 1) / step;
     with_places<KIND, RXMAX>(rt.most, [&](auto rx, auto hb) {
-        constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value;
+        constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value, TT = RX > 16 ? RX / 16 : 1;
         const int units = (D + Unit<KIND, HB>::kCodes - 1) / Unit<KIND, HB>::kCodes;
         Loader<KIND, HB, 2, RX> loader;
         loader.rows(lane, a.w12.ld_q, a.w12.ld_s, D);
@@ -625,23 +641,24 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_tiles_kernel(MoeFewArgs a) 
             const bool there = l_q < all;
             const int q = there ? l_q : q0;
             int first, n;
-            const int e = item_rows(rt, q / width, first, n);
+            const int e = item_rows<PER>(rt, q / width, first, n);
             const int64_t h0 = 16 * (int64_t)(tile0 + q % width);
-            rows[0] = tile_rows<KIND>(a.w12, e, h0, a.H, D);
-            rows[1] = tile_rows<KIND>(a.w12, e, a.H + h0, 2 * a.H, D);
-            if (!there) rows[0].q[2] = rows[1].q[2] = n = 0;
-            loader.tokens([&](int c) { return c < n ? rt.token[first + c] * (int)a.ld_x * 2 : kOut; });
+            rows[0] = tile_rows<KIND>(a.w12, e, h0, a.H, D, there);
+            rows[1] = tile_rows<KIND>(a.w12, e, a.H + h0, 2 * a.H, D, there);
+            loader.tokens([&](int c) { return c < n && there ? rt.token[first + c] * (int)a.ld_x * 2 : kOut; });
         };
         select();
-        f32x4 acc[2][1];
+        f32x4 acc[2][TT];
         zero(acc);
         int m_q = q0, m_u = 0;  // of the next one to multiply
         auto put = [&] {
             int first, n;
-            item_rows(rt, m_q / width, first, n);
-            if (r < n)
-                store_h(a, t0 * a.k + first + r, 16 * (int64_t)(tile0 + m_q % width) + 4 * g, rt.weight[first + r],
-                        acc[0][0], acc[1][0]);
+            item_rows<PER>(rt, m_q / width, first, n);
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+                if (16 * t + r < n)
+                    store_h(a, t0 * a.k + first + 16 * t + r, 16 * (int64_t)(tile0 + m_q % width) + 4 * g,
+                            rt.weight[first + 16 * t + r], acc[0][t], acc[1][t]);
             zero(acc);
         };
         stream_units<KIND, HB, 2, RX, RING>(
@@ -664,6 +681,7 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_tiles_kernel(MoeFewArgs a) 
 // already), added up at the end in the order of the waves.
 template <int KIND, int RXMAX, int W, int RING>
 __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
+    constexpr int PER = item_tokens(RXMAX);
     extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];
     __shared__ __attribute__((aligned(16))) uint8_t s_ring[W * RING];
     __shared__ OneToken s_one[RXMAX == 1 ? W : 1];
@@ -675,12 +693,13 @@ __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
     f32x4* const sums = reinterpret_cast<f32x4*>(s_dyn);  // [wave][token][4]
     f32x4* const own = sums + wave * T * 4;
     for (int i = lane; i < T * 4; i += 64) own[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const Routing rt = RXMAX == 1 ? route_one(a, s_one[wave]) : route_chunk<64 * W>(a, t0, T * a.k, s_dyn + W * T * 64);
+    const Routing rt = RXMAX == 1 ? route_one(a, s_one[wave])
+                                  : route_chunk<PER, 64 * W>(a, t0, T * a.k, s_dyn + W * T * 64, s_ring);
 
     const int r = lane & 15, g = lane >> 4, H = (int)a.H;
     const int64_t d0 = 16 * (int64_t)tile;
     with_places<KIND, RXMAX>(rt.most, [&](auto rx, auto hb) {
-        constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value;
+        constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value, TT = RX > 16 ? RX / 16 : 1;
         const int units = (H + Unit<KIND, HB>::kCodes - 1) / Unit<KIND, HB>::kCodes;
         const int all = rt.items * units, share = (all + W - 1) / W, u0 = min(all, wave * share), mine = min(share, all - u0);
         if (mine <= 0) return;
@@ -694,23 +713,23 @@ __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
         auto select = [&] {
             const bool there = l_left > 0;
             int first, n;
-            const int e = item_rows(rt, there ? l_item : 0, first, n);
-            rows[0] = tile_rows<KIND>(a.wo, e, d0, a.D, H);
-            h = make_rsrc(a.h + (t0 * a.k + first) * a.H, (int64_t)n * H * 2);
-            if (!there) rows[0].q[2] = h[2] = 0;
+            const int e = item_rows<PER>(rt, there ? l_item : 0, first, n);
+            rows[0] = tile_rows<KIND>(a.wo, e, d0, a.D, H, there);
+            h = make_rsrc(a.h + (t0 * a.k + first) * a.H, there ? (int64_t)n * H * 2 : 0);
         };
         select();
-        f32x4 acc[1][1];
+        f32x4 acc[1][TT];
         zero(acc);
         auto put = [&] {
             int first, n;
-            item_rows(rt, m_item, first, n);
-            if (r < n) {
-                f32x4* const s = own + rt.token[first + r] * 4 + g;
-                const f32x4 v = *s;
-                const f32x4 p = acc[0][0];
-                *s = f32x4{v[0] + p[0], v[1] + p[1], v[2] + p[2], v[3] + p[3]};
-            }
+            item_rows<PER>(rt, m_item, first, n);
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+                if (16 * t + r < n) {
+                    f32x4* const s = own + rt.token[first + 16 * t + r] * 4 + g;
+                    const f32x4 v = *s, p = acc[0][t];
+                    *s = f32x4{v[0] + p[0], v[1] + p[1], v[2] + p[2], v[3] + p[3]};
+                }
             zero(acc);
         };
         stream_units<KIND, HB, 1, RX, RING>(
@@ -761,13 +780,14 @@ hipError_t mm_kind(const FewMmArgs& a, hipStream_t stream) {
     return mm<KIND, 64, 2, 64, 4, 40960>(a, stream);
 }
 
-// Workgroups of at most 80 KiB: two on a CU.
-template <int KIND, int RXMAX, int WD, int RING_D>
+constexpr int kLds = 160 * 1024;  // of a CU
+
+template <int KIND, int RXMAX, int WU, int RING_U, int WD, int RING_D>
 hipError_t moe(MoeFewArgs a, hipStream_t stream) {
-    constexpr int WU = 4, RING_U = 19200;
+    constexpr int PER = item_tokens(RXMAX);
     const int64_t chunks = (a.T + kFewChunk - 1) / kFewChunk, tokens = a.T < kFewChunk ? a.T : kFewChunk;
     const int slots = (int)(tokens * a.k);
-    a.items = (slots < a.E ? slots : a.E) + slots / 16;
+    a.items = (slots < a.E ? slots : a.E) + slots / PER;
     const int table = RXMAX == 1 ? 0 : RoutingLayout(a.E, slots, a.items).bytes;
     a.tiles = (a.H + 15) / 16;
     const int64_t padded = (a.tiles + 7) & ~7;
@@ -787,10 +807,16 @@ hipError_t moe(MoeFewArgs a, hipStream_t stream) {
 
 template <int KIND>
 hipError_t moe_kind(const MoeFewArgs& a, hipStream_t stream) {
-    if (a.T <= 1) return moe<KIND, 1, 8, 9728>(a, stream);
-    if (a.T <= 4) return moe<KIND, 4, 8, 9728>(a, stream);
-    if (a.T <= 8) return moe<KIND, 8, 8, 9728>(a, stream);
-    return moe<KIND, 16, 4, 19200>(a, stream);
+    // workgroups of 80 KiB, two on a CU
+    if (a.T <= 1) return moe<KIND, 1, 4, 19200, 8, 9728>(a, stream);
+    if (a.T <= 4) return moe<KIND, 4, 4, 19200, 8, 9728>(a, stream);
+    if (a.T <= 8) return moe<KIND, 8, 4, 19200, 8, 9728>(a, stream);
+    const int64_t tokens = a.T < kFewChunk ? a.T : kFewChunk;
+    if (tokens * a.k > 12 * a.E && tokens > 16) return moe<KIND, 32, 4, 31104, 4, 27904>(a, stream);
+    const int slots = (int)(tokens * a.k), items = (slots < a.E ? slots : a.E) + slots / 16;
+    if (RoutingLayout(a.E, slots, items).bytes + 8 * tokens * 64 + 8 * 15552 <= kLds)
+        return moe<KIND, 16, 4, 19200, 8, 15552>(a, stream);
+    return moe<KIND, 16, 4, 19200, 8, 12800>(a, stream);
 }
 
 }  // namespace

@@ -15,7 +15,7 @@ typedef long long ll;
 
 constexpr int64_t kMaxI32 = 0x7fffffff;
 constexpr int64_t kMaxTokens = (int64_t)1 << 21;   // 32768 chunks: the launch grid's second axis
-constexpr int64_t kMaxScaleLd = (int64_t)1 << 28;  // eight rows of scale bytes in 32-bit offsets
+constexpr int64_t kMaxScales = (int64_t)1 << 30;   // bytes of a matrix's scales: 32-bit offsets, past its end too
 
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -49,8 +49,11 @@ bs_status check_weight(const char* fn, const char* name, bs_weight_kind kind, in
     REQUIRE(aligned16(w.q) && w.ld_q % 16 == 0 && w.stride_q % 16 == 0, BS_ERR_ALIGN,
             "%s must be 16-byte aligned, its ld and stride multiples of 16", name);
     const int64_t cols = kind == BS_WEIGHT_E4M3_128X128 ? N / 128 : N;
-    REQUIRE(w.ld_s >= cols && w.ld_s < kMaxScaleLd, BS_ERR_LAYOUT,
-            "ld of the scales of %s = %lld must be >= %lld and < 2^28 (K-major)", name, (ll)w.ld_s, (ll)cols);
+    REQUIRE(w.ld_s >= cols, BS_ERR_LAYOUT, "ld of the scales of %s = %lld must be >= %lld (K-major)", name, (ll)w.ld_s,
+            (ll)cols);
+    const int64_t blocks = kind == BS_WEIGHT_E4M3_128X128 ? K / 128 : K / 32;
+    REQUIRE(w.ld_s <= kMaxScales / (blocks > 8 ? blocks : 8) / (kind == BS_WEIGHT_E4M3_128X128 ? 4 : 1), BS_ERR_LAYOUT,
+            "the scales of %s, %lld rows of %lld, must be below 2^30 bytes", name, (ll)blocks, (ll)w.ld_s);
     if (kind == BS_WEIGHT_E4M3_128X128)
         REQUIRE(aligned_to(w.s, 4), BS_ERR_ALIGN, "the scales of %s must be aligned to their type", name);
     else

@@ -736,7 +736,7 @@ bs_status bs_mx4_quant_1x32(const uint16_t* x, int64_t R, int64_t C, int64_t ld_
  *   s         its scales, K-major with row stride ld_s in elements: float
  *             scales aligned to their type; scale bytes 16-byte aligned, ld_s a
  *             multiple of 16, and read (never used) up to the next multiple of
- *             16 past the last row of w.  MX weights below 2^-126 in magnitude
+ *             16 past the last row of w; below 2^30 bytes of them.  MX weights below 2^-126 in magnitude
  *             may count as 0, and values above the largest bf16 (scale bytes
  *             that no quantizer makes) are infinite.
  *   residual  [T, N] bf16 or NULL (zeros); may be out itself where that is bf16

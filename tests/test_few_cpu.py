@@ -86,7 +86,7 @@ MM = dict(kind=2, T=3, N=50, K=96, x=P, ld_x=96, w=P, ld_w=48, s=P, ld_s=64, res
     (dict(ld_s=48), LAYOUT, "scales of w"),
     (dict(ld_s=56), ALIGN, "scales of w"),
     (dict(s=P1), ALIGN, "scales of w"),
-    (dict(ld_s=1 << 28), LAYOUT, "2^28"),
+    (dict(ld_s=1 << 28), LAYOUT, "2^30"),
     (dict(kind=1), LAYOUT, "ld of w"),
     (dict(kind=0, N=64, K=128, ld_x=128, ld_w=128, ld_out=64), SHAPE, "128"),
     (dict(kind=0, N=128, ld_w=96, ld_out=128), SHAPE, "128"),
