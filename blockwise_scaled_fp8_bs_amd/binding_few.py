@@ -17,59 +17,74 @@ Weights [N, K] by kind, codes as uint8 with contiguous rows:
 import torch
 
 from . import _lib
-from .binding import BS_OUT_BF16, _check, _mat, _require
-from .binding_block import _DT, _first, _flat, _matrix, _new, _optional, _scales, _stream_of
+from .binding import _check, _mat
+from .binding_block import _DT, _first, _flat, _matrix, _new, _optional, _stream_of
 
 BS_WEIGHT_E4M3_128X128 = 0
 BS_WEIGHT_MXFP8 = 1
 BS_WEIGHT_MXFP4 = 2
 
-_KINDS = (BS_WEIGHT_E4M3_128X128, BS_WEIGHT_MXFP8, BS_WEIGHT_MXFP4)
+#: by kind: codes a byte, contraction and rows of a scale, type of the scales
+_KINDS = {
+    BS_WEIGHT_E4M3_128X128: (1, 128, 128, torch.float32),
+    BS_WEIGHT_MXFP8: (1, 32, 1, torch.uint8),
+    BS_WEIGHT_MXFP4: (2, 32, 1, torch.uint8),
+}
 
 
-def _call(fn, device, *args):
-    """Calls the library with the tensors' device as the current one."""
+def _call(fn, index, *args):
+    """Calls the library with the GPU of the tensors as the current one."""
     call = getattr(_lib.load(), fn)
-    if torch._C._cuda_getDevice() == device.index:
-        _check(call(*args), fn)
+    if torch._C._cuda_getDevice() == index:
+        status = call(*args)
     else:
-        with torch.cuda.device(device):
-            _check(call(*args), fn)
+        with torch.cuda.device(index):
+            status = call(*args)
+    if status:
+        _check(status, fn)
 
 
-def _one_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, x on {device}: all tensors must be on one GPU")
+def _other_gpu(t, name, index):
+    raise ValueError(f"{name} is on {t.device}, x on cuda:{index}: all tensors must be on one GPU")
 
 
-def _out_matrix(t, name, dtype, R, C):
-    """(address, row stride) of a row-major matrix whose rows need no alignment."""
+def _rows_of(t, name, dtype, R, C, index):
+    """(address, row stride) of a row-major [R, C] matrix on GPU `index` whose
+    rows need no alignment; (None, 0) for None."""
+    if t is None:
+        return None, 0
     p, ld = _matrix(t, name, dtype, R, C)
+    if t.get_device() != index:
+        _other_gpu(t, name, index)
     return p, ld if R > 1 else C
 
 
-def _weight(q, s, name, s_name, kind, N, K, experts=None):
-    """C arguments of weights [N, K] (or [experts, N, K]): codes, their
-    strides, scales and theirs."""
+def _weight(q, s, names, kind, N, K, index, experts=None):
+    """C arguments of weights [N, K], or [experts, N, K]: codes, their strides,
+    scales and theirs.  Strides of dimensions with one entry say nothing."""
     if kind not in _KINDS:
-        raise ValueError(f"kind must be one of BS_WEIGHT_E4M3_128X128, BS_WEIGHT_MXFP8 and BS_WEIGHT_MXFP4, got {kind!r}")
-    row = K // 2 if kind == BS_WEIGHT_MXFP4 else K
-    blocks, cols, dtype = (K // 128, N // 128, torch.float32) if kind == BS_WEIGHT_E4M3_128X128 else (K // 32, N, torch.uint8)
+        raise ValueError(f"kind must be BS_WEIGHT_E4M3_128X128, BS_WEIGHT_MXFP8 or BS_WEIGHT_MXFP4, got {kind!r}")
+    per, block, rows, dtype = _KINDS[kind]
+    row, blocks, cols = K // per, K // block, N // rows
     lead = () if experts is None else (experts,)
-    _mat(q, name, torch.uint8, len(lead) + 2)
-    _require(tuple(q.shape) == lead + (N, row), f"{name} must be {list(lead + (N, row))}, got {list(q.shape)}")
-    _mat(s, s_name, dtype, len(lead) + 2)
-    _require(tuple(s.shape[:-1]) == lead + (blocks,) and s.shape[-1] >= cols,
-             f"{s_name} must be {list(lead + (blocks,))} x >= {cols} (K-major), got {list(s.shape)}")
-    # strides of dimensions with one entry say nothing
+    if q is None or q.dtype is not torch.uint8 or q.shape != lead + (N, row) or q.stride(-1) != 1:
+        _mat(q, names[0], torch.uint8, len(lead) + 2)
+        raise ValueError(f"{names[0]} must be {list(lead + (N, row))}, got {list(q.shape)}")
+    if s is None or s.dtype is not dtype or s.dim() != len(lead) + 2 or s.shape[:-1] != lead + (blocks,) \
+            or s.shape[-1] < cols or (s.stride(-1) != 1 and s.shape[-1] > 1):
+        _mat(s, names[1], dtype, len(lead) + 2)
+        raise ValueError(f"{names[1]} must be {list(lead + (blocks,))} x >= {cols} (K-major), got {list(s.shape)}")
+    for t, name in zip((q, s), names):
+        if t.get_device() != index:
+            _mat(t, name, t.dtype, len(lead) + 2)
+            _other_gpu(t, name, index)
     ld = q.stride(-2) if N > 1 else (row + 15) // 16 * 16
-    ld_s = s.stride(-2) if blocks > 1 else s.shape[-1]
-    p, p_s = q.data_ptr() or None, s.data_ptr() or None
+    ld_s = s.stride(-2) if blocks > 1 else s.shape[-1] if rows > 1 else (cols + 15) // 16 * 16
     if experts is None:
-        return p, ld, p_s, ld_s
-    many = experts > 1
-    return p, (q.stride(0) if many else 0), ld, p_s, (s.stride(0) if many else 0), ld_s
+        return q.data_ptr(), ld, s.data_ptr(), ld_s
+    if experts == 1:
+        return q.data_ptr(), 0, ld, s.data_ptr(), 0, ld_s
+    return q.data_ptr(), q.stride(0), ld, s.data_ptr(), s.stride(0), ld_s
 
 
 def bs_mx4_quant_1x32(x, q, s, y=None, stream=None):
@@ -78,17 +93,20 @@ def bs_mx4_quant_1x32(x, q, s, y=None, stream=None):
     and, if given, y [R, C] bf16, the values that the codes stand for."""
     bf16 = torch.bfloat16
     R, C = _first(x, "x", bf16)
-    _one_device(x.device, q=q, s=s, y=y)
-    _mat(s, "s", torch.uint8)
-    _require(s.shape[0] == C // 32 and s.shape[1] >= R, f"s must be [{C // 32}, >= {R}], got {list(s.shape)}")
-    ld_s = s.stride(0) if s.shape[0] > 1 else s.shape[1] // 16 * 16 if s.shape[1] // 16 * 16 >= R else s.stride(0)
-    _call("bs_mx4_quant_1x32", x.device, *_first_args(x, R, C), *_matrix(q, "q", torch.uint8, R, C // 2),
-          s.data_ptr() or None, ld_s, *_optional(y, "y", bf16, R, C), _stream_of(x, stream))
-
-
-def _first_args(x, R, C):
-    p, ld = _matrix(x, "x", torch.bfloat16, R, C)
-    return p, R, C, ld
+    p, ld = _matrix(x, "x", bf16, R, C)
+    index = x.get_device()
+    if s is None or s.dtype is not torch.uint8 or s.dim() != 2 or s.shape[0] != C // 32 or s.shape[1] < R \
+            or s.stride(1) != 1:
+        _mat(s, "s", torch.uint8)
+        raise ValueError(f"s must be [{C // 32}, >= {R}], got {list(s.shape)}")
+    p_q, ld_q = _matrix(q, "q", torch.uint8, R, C // 2)
+    p_y, ld_y = _optional(y, "y", bf16, R, C)
+    for t, name in ((q, "q"), (s, "s"), (y, "y")):
+        if t is not None and t.get_device() != index:
+            _mat(t, name, t.dtype)
+            _other_gpu(t, name, index)
+    _call("bs_mx4_quant_1x32", index, p, R, C, ld, p_q, ld_q, s.data_ptr() or None,
+          s.stride(0) if C > 32 else max(s.shape[1], (R + 15) // 16 * 16) // 16 * 16, p_y, ld_y, _stream_of(x, stream))
 
 
 def bs_few_mm(x, w, s, kind, residual=None, out=None, out_dtype=torch.bfloat16, stream=None):
@@ -96,20 +114,24 @@ def bs_few_mm(x, w, s, kind, residual=None, out=None, out_dtype=torch.bfloat16, 
     weights [N, K] of the given kind; residual [T, N] bf16; out bf16 or fp32."""
     bf16 = torch.bfloat16
     T, K = _first(x, "x", bf16)
+    p_x, ld_x = _matrix(x, "x", bf16, T, K)
+    index = x.get_device()
     if w is None or w.dim() != 2:
         _mat(w, "w", torch.uint8)
     N = w.shape[0]
+    weight = _weight(w, s, ("w", "s"), kind, N, K, index)
     if out is None:
         if out_dtype not in _DT:
             raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
         out = _new(stream, (T, N), out_dtype, x.device)
-    elif out.dtype not in _DT:
-        raise ValueError(f"out must be bfloat16 or float32, got {out.dtype}")
-    _one_device(x.device, w=w, s=s, residual=residual, out=out)
-    p_x, ld_x = _matrix(x, "x", bf16, T, K)
-    _call("bs_few_mm", x.device, kind, T, N, K, p_x, ld_x, *_weight(w, s, "w", "s", kind, N, K),
-          *((None, 0) if residual is None else _out_matrix(residual, "residual", bf16, T, N)),
-          *_out_matrix(out, "out", out.dtype, T, N), _DT[out.dtype], _stream_of(x, stream))
+        p_out, ld_out = out.data_ptr() or None, N
+    else:
+        if out.dtype not in _DT:
+            raise ValueError(f"out must be bfloat16 or float32, got {out.dtype}")
+        p_out, ld_out = _rows_of(out, "out", out.dtype, T, N, index)
+    p_res, ld_res = _rows_of(residual, "residual", bf16, T, N, index)
+    _call("bs_few_mm", index, kind, T, N, K, p_x, ld_x, *weight, p_res, ld_res, p_out, ld_out, _DT[out.dtype],
+          _stream_of(x, stream))
     return out
 
 
@@ -124,24 +146,34 @@ def bs_moe_few(x, idx, w, w12, s12, out_proj, s_out, kind, residual=None, out=No
     """
     bf16 = torch.bfloat16
     T, D = _first(x, "x", bf16)
+    p_x, ld_x = _matrix(x, "x", bf16, T, D)
+    index = x.get_device()
     if w12 is None or w12.dim() != 3 or w12.shape[1] % 2 != 0:
         raise ValueError(f"w12 must be [E, 2H, D], got {None if w12 is None else list(w12.shape)}")
     E, H = w12.shape[0], w12.shape[1] // 2
-    if idx is None:
-        k, p_idx = 1, None
-        _require(E == 1, f"idx is required with {E} experts")
-    else:
-        _require(idx.dim() == 2 and idx.shape[0] == T, f"idx must be [{T}, k], got {list(idx.shape)}")
+    k, p_idx, p_w = 1, None, None
+    if idx is not None:
+        if idx.dim() != 2 or idx.shape[0] != T:
+            raise ValueError(f"idx must be [{T}, k], got {list(idx.shape)}")
         k, p_idx = idx.shape[1], _flat(idx, "idx", torch.int32, idx.shape)
+        if idx.get_device() != index:
+            _other_gpu(idx, "idx", index)
+    elif E != 1:
+        raise ValueError(f"idx is required with {E} experts")
+    if w is not None:
+        p_w = _flat(w, "w", torch.float32, (T, k))
+        if w.get_device() != index:
+            _other_gpu(w, "w", index)
+    up = _weight(w12, s12, ("w12", "s12"), kind, 2 * H, D, index, E)
+    down = _weight(out_proj, s_out, ("out_proj", "s_out"), kind, D, H, index, E)
+    p_res, ld_res = _rows_of(residual, "residual", bf16, T, D, index)
     if out is None:
         out = _new(stream, (T, D), bf16, x.device)
-    _one_device(x.device, idx=idx, w=w, w12=w12, s12=s12, out_proj=out_proj, s_out=s_out, residual=residual, out=out)
-    p_x, ld_x = _matrix(x, "x", bf16, T, D)
-    nbytes = _lib.load().bs_moe_few_workspace_bytes(T, k, H)
+        p_out, ld_out = out.data_ptr() or None, D
+    else:
+        p_out, ld_out = _rows_of(out, "out", bf16, T, D, index)
+    nbytes = 2 * T * k * H      # bs_moe_few_workspace_bytes
     h = _new(stream, nbytes, torch.uint8, x.device)
-    _call("bs_moe_few", x.device, kind, T, D, H, E, k, p_x, ld_x, p_idx,
-          None if w is None else _flat(w, "w", torch.float32, (T, k)), *_weight(w12, s12, "w12", "s12", kind, 2 * H, D, E),
-          *_weight(out_proj, s_out, "out_proj", "s_out", kind, D, H, E),
-          *((None, 0) if residual is None else _out_matrix(residual, "residual", bf16, T, D)),
-          *_out_matrix(out, "out", bf16, T, D), h.data_ptr() or None, nbytes, _stream_of(x, stream))
+    _call("bs_moe_few", index, kind, T, D, H, E, k, p_x, ld_x, p_idx, p_w, *up, *down, p_res, ld_res, p_out, ld_out,
+          h.data_ptr() or None, nbytes, _stream_of(x, stream))
     return out
