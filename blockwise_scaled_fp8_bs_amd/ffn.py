@@ -27,6 +27,8 @@ inside the stacked scale tensor), dim and the token count multiples of 128.
 import torch
 
 from . import binding as _b
+from . import binding_few as _f
+from . import serving as _s
 from .linear import _check_dims, _quant_rows_cols
 
 
@@ -120,10 +122,17 @@ def float8_blockwise_gated_ffn(x, w1, w2, out_proj):
     return y.view(*lead, D)
 
 
-class Float8BlockwiseGatedFFN(torch.nn.Module):
+class Float8BlockwiseGatedFFN(_s.ServedWeights, torch.nn.Module):
     """Bias-free gated FFN  out_proj(silu(w1 x) * w2 x)  in blockwise FP8,
     with parameters named like the ToyModel FFN (w1, w2, out_proj; each an
-    [out, in] weight)."""
+    [out, in] weight).
+
+    For serving, ``prepare_serving()`` lays the weights out once; while that
+    layout is there (see ``ServedWeights``) and gradients are off, forward
+    takes any number of tokens.
+    """
+
+    _served_names = ("w1", "w2", "out_proj")
 
     def __init__(self, dim, hidden, device=None, dtype=torch.bfloat16):
         super().__init__()
@@ -152,8 +161,40 @@ class Float8BlockwiseGatedFFN(torch.nn.Module):
             m.out_proj.copy_(out_proj.weight.to(torch.bfloat16))
         return m
 
+    def prepare_serving(self, weights="fp8", few_tokens=_s.FEW_TOKENS):
+        """Quantizes the weights for the forward, w1 and w2 stacked; call again
+        after they change.  weights and few_tokens as for Float8BlockwiseLinear;
+        few tokens take both products in two kernels (bs_moe_few)."""
+        _s.check_formats(weights, few_tokens, ("fp8", "mxfp4"))
+
+        def layout(w1, w2, out_proj):
+            w12 = torch.cat([w1, w2])
+            if weights == "fp8":
+                gemm = few = _s.rows_128(w12) + _s.rows_128(out_proj)
+                kind = _f.BS_WEIGHT_E4M3_128X128
+            else:
+                q12, s12, w12 = _s.rows_mx4(w12, values=True)
+                qo, so, out_proj = _s.rows_mx4(out_proj, values=True)
+                gemm, few = _s.rows_128(w12) + _s.rows_128(out_proj), (q12, s12, qo, so)
+                kind = _f.BS_WEIGHT_MXFP4
+            return gemm + tuple(t[None] for t in few) + (kind, few_tokens)
+
+        return self._lay_out(layout)
+
     def forward(self, x):
-        return float8_blockwise_gated_ffn(x, self.w1, self.w2, self.out_proj)
+        layout = None if torch.is_grad_enabled() else self._layout()
+        if layout is None:
+            return float8_blockwise_gated_ffn(x, self.w1, self.w2, self.out_proj)
+        *gemm, q12, s12, qo, so, kind, few_tokens = layout
+        x2 = _s.token_rows(x, self.dim)
+        if x2.shape[0] <= few_tokens:
+            return _f.bs_moe_few(x2, None, None, q12, s12, qo, so, kind).view(x.shape)
+        q12, s12, qo, so = gemm
+        ab = _b.bs_scaled_mm(*_s.quantized_rows(x2), q12, s12, _b.BS_SCALE_128X128, out_dtype=torch.bfloat16)
+        qh = torch.empty((x2.shape[0], self.hidden), dtype=torch.uint8, device=x.device)
+        sh = _b.empty_scales(self.hidden // 128, x2.shape[0], x.device)
+        _b.bs_swiglu_quant_1x128(ab[:, :self.hidden], ab[:, self.hidden:], None, qh, sh)
+        return _b.bs_scaled_mm(qh, sh, qo, so, _b.BS_SCALE_128X128, out_dtype=torch.bfloat16).view(x.shape)
 
     def extra_repr(self):
         return f"dim={self.dim}, hidden={self.hidden}, blockwise fp8, fused gated activation"

@@ -26,6 +26,8 @@ behind the caller's back.
 import torch
 
 from . import binding as _b
+from . import binding_few as _f
+from . import serving as _s
 
 
 def _check_dims(M, K, N):
@@ -105,9 +107,16 @@ def float8_blockwise_linear(x, weight):
     return y.view(*lead, N)
 
 
-class Float8BlockwiseLinear(torch.nn.Module):
+class Float8BlockwiseLinear(_s.ServedWeights, torch.nn.Module):
     """Bias-free linear layer whose forward and backward GEMMs run in
-    blockwise-scaled FP8 (activations and gradients 1x128, weights 128x128)."""
+    blockwise-scaled FP8 (activations and gradients 1x128, weights 128x128).
+
+    For serving, ``prepare_serving()`` lays the weight out once; while that
+    layout is there (see ``ServedWeights``) and gradients are off, forward
+    takes any number of tokens.
+    """
+
+    _served_names = ("weight",)
 
     def __init__(self, in_features, out_features, device=None, dtype=torch.bfloat16):
         super().__init__()
@@ -127,8 +136,35 @@ class Float8BlockwiseLinear(torch.nn.Module):
             m.weight.copy_(lin.weight.to(torch.bfloat16))
         return m
 
+    def prepare_serving(self, weights="fp8", few_tokens=_s.FEW_TOKENS):
+        """Quantizes the weight for the forward; call again after it changes.
+
+        weights: "fp8" (the 128x128 blocks of the training forward) or "mxfp4"
+        (4 bits, for half the traffic of few tokens; more tokens take the 4-bit
+        values in FP8).  Up to few_tokens tokens meet it in bf16 (bs_few_mm);
+        more are quantized, as in training.
+        """
+        _s.check_formats(weights, few_tokens, ("fp8", "mxfp4"))
+
+        def layout(w):
+            if weights == "fp8":
+                return _s.rows_128(w) * 2 + (_f.BS_WEIGHT_E4M3_128X128, few_tokens)
+            q, s, y = _s.rows_mx4(w, values=True)
+            return _s.rows_128(y) + (q, s, _f.BS_WEIGHT_MXFP4, few_tokens)
+
+        return self._lay_out(layout)
+
     def forward(self, x):
-        return float8_blockwise_linear(x, self.weight)
+        layout = None if torch.is_grad_enabled() else self._layout()
+        if layout is None:
+            return float8_blockwise_linear(x, self.weight)
+        q, s, few_q, few_s, kind, few_tokens = layout
+        x2 = _s.token_rows(x, self.in_features)
+        if x2.shape[0] <= few_tokens:
+            y = _f.bs_few_mm(x2, few_q, few_s, kind)
+        else:
+            y = _b.bs_scaled_mm(*_s.quantized_rows(x2), q, s, _b.BS_SCALE_128X128, out_dtype=torch.bfloat16)
+        return y.view(*x.shape[:-1], self.out_features)
 
     def extra_repr(self):
         return f"in_features={self.in_features}, out_features={self.out_features}, blockwise fp8"

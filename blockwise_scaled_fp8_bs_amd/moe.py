@@ -43,6 +43,8 @@ from torch.autograd.function import once_differentiable
 
 from . import binding as _b
 from . import binding_block as _k
+from . import binding_few as _f
+from . import serving as _s
 
 
 def _rows(t, name):
@@ -362,7 +364,7 @@ def float8_blockwise_moe_ffn(x, idx, w, w12, out_proj, residual=None, checkpoint
     return y.view(x.shape)
 
 
-class Float8BlockwiseMoE(torch.nn.Module):
+class Float8BlockwiseMoE(_s.ServedWeights, torch.nn.Module):
     """Bias-free gated experts in blockwise FP8 behind a top-k router.
 
     router [experts, dim], w12 [experts, 2 hidden, dim], out_proj
@@ -374,18 +376,17 @@ class Float8BlockwiseMoE(torch.nn.Module):
     checkpoint: how [a | b] is kept for the backward, in 8 bits by default.
 
     For serving, ``prepare_serving()`` lays the weights out once in FP8; while
-    that layout is there and gradients are off, forward takes it: the rows are
-    sorted without padding and quantized along rows only.  train(), moving the
-    module and loading a state drop the layout, and a copy has none.  Other
-    weights than those laid out (assigned since, or passed for one call by
-    ``torch.func.functional_call``) are quantized by the forward that they are
-    there for.  Where the weights laid out have been written in place or given
-    other memory, forward raises.  It goes by autograd's version counter: what
-    writes past that (through ``.data``, in a collective, in a kernel of one's
-    own) is not seen, and needs prepare_serving() again.  A pass captured into a
+    that layout is there (see ``ServedWeights``) and gradients are off, forward
+    takes it: the rows are sorted without padding and quantized along rows
+    only.  With ``prepare_serving(few_tokens=...)`` passes of up to that many
+    tokens take the experts in two kernels instead, tokens in bf16, and
+    ``last_counts`` is None after them.  Other weights than those laid out are
+    quantized by the forward that they are there for.  A pass captured into a
     graph reads the memory of the layout that was there: capture it again after
     prepare_serving(), and do not replay it once the layout was dropped.
     """
+
+    _served_names = ("w12", "out_proj")
 
     def __init__(self, dim, hidden, experts, top_k, score="sigmoid", n_group=1, topk_group=1, group_best=1,
                  renormalize=True, scale=1.0, checkpoint="fp8", device=None):
@@ -406,52 +407,37 @@ class Float8BlockwiseMoE(torch.nn.Module):
             for p in (self.router, self.w12, self.out_proj):
                 p.uniform_(-p.shape[-1] ** -0.5, p.shape[-1] ** -0.5)
         self.last_counts = None
-        self._serving = self._served = None
 
-    def prepare_serving(self):
+    def prepare_serving(self, weights="fp8", few_tokens=0):
         """Quantizes the expert weights for the forward; call again after they
-        change.  Not for inference tensors, whose changes nothing counts."""
-        weights = self.w12, self.out_proj
-        if any(p.is_inference() for p in weights):
-            raise RuntimeError("the expert weights are inference tensors, whose changes nothing counts: make or load the "
-                               "module outside torch.inference_mode()")
-        with torch.no_grad():
-            self._serving = _expert_weights(weights[0])[:2] + _expert_weights(weights[1])[:2]
-        # what the layout is of: the tensors, their memory (an alias, so that its address is not handed out again) and
-        # their versions
-        self._served = [(p, p.detach(), p._version) for p in weights]
-        return self
+        change.  Not for inference tensors, whose changes nothing counts.
 
-    def _layout(self):
-        """The layout if it is that of the present weights, None if there is none of them."""
-        if self._serving is None or self.w12 is not self._served[0][0] or self.out_proj is not self._served[1][0]:
-            return None
-        if any(p._version != version or not p.is_set_to(memory) for p, memory, version in self._served):
-            raise RuntimeError("the expert weights changed after prepare_serving(): call it again")
-        return self._serving
+        weights: "fp8" (the 128x128 blocks of the training forward) or "mxfp4"
+        (4 bits, for half the traffic of few tokens; passes of more tokens take
+        the 4-bit values in FP8).  few_tokens: tokens up to which a pass takes
+        bs_moe_few; 0: none.
+        """
+        _s.check_formats(weights, few_tokens, ("fp8", "mxfp4"))
 
-    def __getstate__(self):
-        return dict(self.__dict__, _serving=None, _served=None)
+        def layout(w12, out_proj):
+            if weights == "fp8":
+                gemm = _expert_weights(w12)[:2] + _expert_weights(out_proj)[:2]
+                return gemm + gemm + (_f.BS_WEIGHT_E4M3_128X128, few_tokens)
+            q12, s12, w12 = _s.experts_mx4(w12)
+            qo, so, out_proj = _s.experts_mx4(out_proj)
+            return _expert_weights(w12)[:2] + _expert_weights(out_proj)[:2] + (q12, s12, qo, so, _f.BS_WEIGHT_MXFP4, few_tokens)
 
-    def train(self, mode=True):
-        if mode:
-            self._serving = self._served = None
-        return super().train(mode)
+        return self._lay_out(layout)
 
     def _apply(self, fn, *args, **kw):
-        self._serving = self._served = None
         balance = self.balance
         super()._apply(fn, *args, **kw)
         if self.balance.dtype != torch.float32:  # the module was cast: the weights' type is not the bias's
             self.balance = balance.to(self.balance.device)
         return self
 
-    def _load_from_state_dict(self, *args, **kw):
-        self._serving = self._served = None
-        return super()._load_from_state_dict(*args, **kw)
-
     def _serve(self, layout, x2, idx, w, residual):
-        q12, s12, qo, so = layout
+        q12, s12, qo, so = layout[:4]
         plan = _k.bs_moe_plan(idx, self.experts, align=1)
         M, H, dev = plan.row_slot.shape[0], self.hidden, x2.device
         qx = _codes(M, self.dim, False, dev)
@@ -469,7 +455,11 @@ class Float8BlockwiseMoE(torch.nn.Module):
         idx, w = moe_route(logits, self.top_k, bias=self.balance, **self.how)
         layout = None if torch.is_grad_enabled() or x2.shape[0] == 0 else self._layout()
         if layout is not None:
-            plan, y = self._serve(layout, x2, idx, w, None if residual is None else _rows(residual, "residual"))
+            r2 = None if residual is None else _rows(residual, "residual")
+            if x2.shape[0] <= layout[-1]:
+                self.last_counts = None
+                return _f.bs_moe_few(x2, idx, w, *layout[4:9], residual=r2).view(x.shape)
+            plan, y = self._serve(layout, x2, idx, w, r2)
             y = y.view(x.shape)
         else:
             plan = _k.bs_moe_plan(idx, self.experts)

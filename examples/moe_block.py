@@ -8,7 +8,9 @@ The block takes the residual stream x and the output u of the block before it:
     r, h = resid_norm(x, w_pre, u, w_post, gate)   r = x + gate N(u) w_post, h = N(r) w_pre
     y    = r + experts(h)                          router, dispatch, FP8 experts, combine
 
-and is trained to move r towards a fixed random target.  Data and weights are random.
+and is trained to move r towards a fixed random target; served, it takes the grouped
+GEMMs or, with prepare_serving(few_tokens=...), two kernels for all experts.  Data and
+weights are random.
 """
 
 import argparse
@@ -77,25 +79,32 @@ def main():
     print(f"training: {a.tokens} tokens, {ms:.2f} ms a step, "
           f"{torch.cuda.max_memory_allocated() / 2 ** 20:.0f} MiB at the peak, loss " + " ".join(f"{v:.4f}" for v in losses))
     block.eval()
-    block.moe.prepare_serving()
-    with torch.no_grad():
-        for n in (1, 32):
-            xs, us = new(n, 1.0), new(n, 1.0)
-            graph = torch.cuda.CUDAGraph()
-            block(xs, us)
-            with torch.cuda.graph(graph):
-                y = block(xs, us)
-            took = []
-            for step in (lambda: block(xs, us), graph.replay):
+    for how, kw in (("grouped GEMMs", {}), ("few tokens", dict(few_tokens=32)),
+                    ("few tokens, 4-bit weights", dict(weights="mxfp4", few_tokens=32))):
+        block.moe.prepare_serving(**kw)
+        serve(block, a.dim, how)
+
+
+@torch.no_grad()
+def serve(block, dim, how):
+    """Passes of one token and of 32, eagerly and replayed from a graph."""
+    for n in (1, 32):
+        xs, us = ((torch.randn(n, dim, device="cuda")).to(torch.bfloat16) for _ in range(2))
+        graph = torch.cuda.CUDAGraph()
+        block(xs, us)
+        with torch.cuda.graph(graph):
+            y = block(xs, us)
+        took = []
+        for step in (lambda: block(xs, us), graph.replay):
+            step()
+            torch.cuda.synchronize()
+            t = time.perf_counter()
+            for _ in range(100):
                 step()
-                torch.cuda.synchronize()
-                t = time.perf_counter()
-                for _ in range(100):
-                    step()
-                torch.cuda.synchronize()
-                took.append((time.perf_counter() - t) * 1e4)
-            print(f"serving: {n} token(s), {took[0]:.0f} us a pass, {took[1]:.0f} us replayed from a graph, "
-                  f"|y| {float(y.float().norm()):.3f}")
+            torch.cuda.synchronize()
+            took.append((time.perf_counter() - t) * 1e4)
+        print(f"serving ({how}): {n} token(s), {took[0]:.0f} us a pass, {took[1]:.0f} us replayed from a graph, "
+              f"|y| {float(y.float().norm()):.3f}")
 
 
 if __name__ == "__main__":
