@@ -172,8 +172,8 @@ def bs_moe_few(x, idx, w, w12, s12, out_proj, s_out, kind, residual=None, out=No
         p_out, ld_out = out.data_ptr() or None, D
     else:
         p_out, ld_out = _rows_of(out, "out", bf16, T, D, index)
-    nbytes = 2 * T * k * H      # bs_moe_few_workspace_bytes
-    h = _new(stream, nbytes, torch.uint8, x.device)
+    nbytes = _lib.load().bs_moe_few_workspace_bytes(T, D, H, E, k)
+    workspace = _new(stream, nbytes, torch.uint8, x.device)
     _call("bs_moe_few", index, kind, T, D, H, E, k, p_x, ld_x, p_idx, p_w, *up, *down, p_res, ld_res, p_out, ld_out,
-          h.data_ptr() or None, nbytes, _stream_of(x, stream))
+          workspace.data_ptr() or None, nbytes, _stream_of(x, stream))
     return out

@@ -9,7 +9,11 @@
 namespace bs {
 
 constexpr int64_t kFewChunk = 64;               // tokens that a workgroup takes at a time
+constexpr int kCus = 256;
+constexpr int kMaxSplits = 16;                  // workgroups that share columns of bs_moe_few's output
 constexpr int64_t kMaxFewDim = (int64_t)1 << 18;  // widths of bs_moe_few: a chunk's slots times them in 32-bit offsets
+
+typedef float few_f32x4 __attribute__((ext_vector_type(4)));
 
 enum FewKind { kFewE4m3 = 0, kFewMx8 = 1, kFewMx4 = 2 };
 
@@ -60,12 +64,18 @@ struct MoeFewArgs {
     int64_t ld_out;
     bool vec;
     uint16_t* h;    // workspace [T * k, H] bf16
-    int64_t tiles;  // set by the launcher
-    int32_t items;  // set by the launcher: most (expert, 16 tokens) of a chunk
+    // set by the launcher
+    int64_t tiles;
+    int32_t items;      // work items of a chunk at most
+    int32_t splits;     // workgroups that share columns of the output
+    few_f32x4* part;    // workspace: their sums [splits][T, D]
 };
 
 hipError_t launch_mx4_quant(const Mx4QuantArgs& a, hipStream_t stream);
 hipError_t launch_few_mm(const FewMmArgs& a, FewKind kind, hipStream_t stream);
 hipError_t launch_moe_few(const MoeFewArgs& a, FewKind kind, hipStream_t stream);
+
+// Workspace of the workgroups that share columns of the output (0: none can).
+int64_t moe_few_shares_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k);
 
 }  // namespace bs

@@ -393,7 +393,7 @@ struct Routing {
     const uint32_t* item;   // [items + 1]: expert << 16 | first row of h
     const uint8_t* token;   // [row of h]
     const float* weight;    // [row of h]
-    int items, most;        // the largest item's tokens
+    int items, most;        // places (a power of two) that the largest item's tokens take
 };
 
 // LDS of the table for `slots` choices and `items` items, and what making it
@@ -404,7 +404,7 @@ struct RoutingLayout {
     __host__ __device__ RoutingLayout(int E, int slots, int items) {
         weight = 0;
         item = 4 * slots;
-        token = item + 4 * (items + 3);    // and the numbers of items and the largest one's tokens
+        token = item + 4 * (items + 4);    // and what was found: items, the places of the largest one, an expert named twice
         bytes = (token + slots + 15) / 16 * 16;
         chose = 0;
         w = 8 * E;
@@ -415,6 +415,18 @@ struct RoutingLayout {
 };
 
 __device__ __forceinline__ u64 below(int lane) { return (1ull << lane) - 1; }
+
+// Sum over the lanes up to this one: within rows of 16 by shifts, then the
+// rows' last lanes passed on.
+__device__ __forceinline__ int prefix_sum(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);  // row_shr 2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);  // row_shr 4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);  // row_shr 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2 and 3
+    return v;
+}
 
 template <int PER, int THREADS>
 __device__ __forceinline__ Routing route_chunk(const MoeFewArgs& a, int64_t t0, int slots, uint8_t* lds, uint8_t* scratch) {
@@ -428,53 +440,63 @@ __device__ __forceinline__ Routing route_chunk(const MoeFewArgs& a, int64_t t0, 
     int16_t* const expert = reinterpret_cast<int16_t*>(scratch + at.e);
     uint16_t* const start = reinterpret_cast<uint16_t*>(scratch + at.start);
     const int tid = threadIdx.x, lane = tid & 63;
+    // (the first choices are on their way while the table is cleared)
+    int32_t e0 = -1;
+    float w0 = 1.f;
+    if (tid < slots) {
+        e0 = a.idx ? a.idx[t0 * a.k + tid] : 0;
+        if (a.w) w0 = a.w[t0 * a.k + tid];
+    }
     for (int i = tid; i < a.E; i += THREADS) chose[i] = 0;
+    if (tid == 0) found[2] = 0;
     __syncthreads();
     for (int i = tid; i < slots; i += THREADS) {
-        const int32_t e = a.idx ? a.idx[t0 * a.k + i] : 0;
+        const int32_t e = i == tid ? e0 : a.idx ? a.idx[t0 * a.k + i] : 0;
         const bool routed = (uint32_t)e < (uint32_t)a.E;
         expert[i] = (int16_t)(routed ? e : -1);
-        w[i] = a.w ? a.w[t0 * a.k + i] : 1.f;
-        if (routed) atomicOr(&chose[e], 1ull << (i / a.k));
+        w[i] = i == tid ? w0 : a.w ? a.w[t0 * a.k + i] : 1.f;
+        const u64 bit = 1ull << (i / a.k);
+        if (routed && (atomicOr(&chose[e], bit) & bit)) found[2] = 1;  // named twice
     }
     __syncthreads();
     if (tid < 64) {
         int items = 0, rows = 0, most = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 64) {
-            const int n = e0 + lane < a.E ? __popcll(chose[e0 + lane]) : 0, its = (n + PER - 1) / PER;
-            int upto = n | its << 16;  // both sums in one: at most 2048 rows of a chunk
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int o = __shfl_up(upto, d);
-                if (lane >= d) upto += o;
-            }
+        for (int e = lane; e - lane < a.E; e += 64) {
+            const int n = e < a.E ? __popcll(chose[e]) : 0, its = (n + PER - 1) / PER;
+            const int upto = prefix_sum(n | its << 16);  // both sums in one: at most 2048 rows of a chunk
             const int r0 = rows + (upto & 0xffff) - n, i0 = items + (upto >> 16) - its;
-            if (e0 + lane < a.E) start[e0 + lane] = (uint16_t)r0;
-            for (int j = 0; j < its; ++j) item[i0 + j] = (uint32_t)(e0 + lane) << 16 | (uint32_t)(r0 + PER * j);
+            if (e < a.E) start[e] = (uint16_t)r0;
+            for (int j = 0; j < its; ++j) item[i0 + j] = (uint32_t)e << 16 | (uint32_t)(r0 + PER * j);
             most = max(most, min(n, PER));
-            const int all = __shfl(upto, 63);
+            const int all = __builtin_amdgcn_readlane(upto, 63);
             rows += all & 0xffff;
             items += all >> 16;
         }
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
+        // (PER is a power of two: the largest count's power is the bit that counts)
+        int places = 1;
+        for (; places < PER && __ballot(most > places); places *= 2) {
+        }
         if (lane == 0) {
             item[items] = (uint32_t)rows;
             found[0] = (uint32_t)items;
-            found[1] = (uint32_t)most;
+            found[1] = (uint32_t)places;
         }
     }
     __syncthreads();
+    const bool twice = found[2] != 0;
     for (int i = tid; i < slots; i += THREADS) {
         const int e = expert[i], t = i / a.k;
         if (e < 0) continue;
         bool first = true;
-        float sum = 0.f;
-        for (int j = t * a.k; j < (t + 1) * a.k; ++j)
-            if (expert[j] == e) {
-                first &= j >= i;
-                sum += w[j];
-            }
+        float sum = w[i];
+        if (twice) {
+            sum = 0.f;
+            for (int j = t * a.k; j < (t + 1) * a.k; ++j)
+                if (expert[j] == e) {
+                    first &= j >= i;
+                    sum += w[j];
+                }
+        }
         if (!first) continue;
         const int row = start[e] + __popcll(chose[e] & below(t));
         token[row] = (uint8_t)t;
@@ -539,13 +561,13 @@ using Int = std::integral_constant<int, V>;
 constexpr int item_tokens(int rxmax) { return rxmax > 16 ? rxmax : 16; }
 
 // Calls run with the tokens' places and the unit's bytes for items of `most`
-// tokens, RXMAX at most.
-template <int KIND, int RXMAX, class Run>
+// tokens, RXMAX at most; short units throughout with SHORT.
+template <int KIND, int RXMAX, bool SHORT, class Run>
 __device__ __forceinline__ void with_places(int most, Run run) {
-    constexpr int kMany = KIND == kFewMx4 ? 64 : 128;
-    if (RXMAX == 1 || most <= 1) return run(Int<1>{}, Int<128>{});
+    constexpr int kFew = SHORT ? 64 : 128, kMany = SHORT || KIND == kFewMx4 ? 64 : 128;
+    if (RXMAX == 1 || most <= 1) return run(Int<1>{}, Int<kFew>{});
     if constexpr (RXMAX > 1) {
-        if (RXMAX == 4 || most <= 4) return run(Int<4>{}, Int<128>{});
+        if (RXMAX == 4 || most <= 4) return run(Int<4>{}, Int<kFew>{});
     }
     if constexpr (RXMAX > 4) {
         if (RXMAX == 8 || most <= 8) return run(Int<8>{}, Int<kMany>{});
@@ -587,7 +609,7 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_kernel(MoeFewArgs a) {
     const int64_t h0 = 16 * (int64_t)tile;
     const Tile16 rows[2] = {tile_rows<KIND>(a.w12, e, h0, a.H, D), tile_rows<KIND>(a.w12, e, a.H + h0, 2 * a.H, D)};
     const i32x4 x = make_rsrc(a.x + t0 * a.ld_x, ((T - 1) * a.ld_x + D) * 2);
-    with_places<KIND, RXMAX>(n, [&](auto rx, auto hb) {
+    with_places<KIND, RXMAX, false>(n, [&](auto rx, auto hb) {
         constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value, TT = RX > 16 ? RX / 16 : 1;
         static_assert(RING >= 2 * TT * 1024, "the sums take the ring's place");
         Loader<KIND, HB, 2, RX> loader;
@@ -610,11 +632,12 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_kernel(MoeFewArgs a) {
     });
 }
 
-// The same where there are many tiles: every wave streams whole tiles, one
-// after the other, without a barrier; an XCD's waves walk neighbouring tiles.
-template <int KIND, int RXMAX, int W, int RING>
+// The same where there are many tiles: every wave streams whole tiles (16 NH
+// columns), one after the other, without a barrier; an XCD's waves walk
+// neighbouring tiles.
+template <int KIND, int RXMAX, int NH, int W, int RING>
 __global__ __launch_bounds__(64 * W) void moe_few_up_tiles_kernel(MoeFewArgs a) {
-    constexpr int PER = item_tokens(RXMAX);
+    constexpr int PER = item_tokens(RXMAX), NT = 2 * NH;
     extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];
     __shared__ __attribute__((aligned(16))) uint8_t s_ring[W * RING];
     __shared__ OneToken s_one[RXMAX == 1 ? W : 1];
@@ -630,38 +653,44 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_tiles_kernel(MoeFewArgs a) 
     const int q0 = (blockIdx.x >> 3) * W + wave, step = (gridDim.x >> 3) * W, all = rt.items * width;
     if (q0 >= all) return;
     const int mine = (all - q0 + step - 1) / step;
-    with_places<KIND, RXMAX>(rt.most, [&](auto rx, auto hb) {
+    with_places<KIND, RXMAX, (NH > 1)>(rt.most, [&](auto rx, auto hb) {
         constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value, TT = RX > 16 ? RX / 16 : 1;
         const int units = (D + Unit<KIND, HB>::kCodes - 1) / Unit<KIND, HB>::kCodes;
-        Loader<KIND, HB, 2, RX> loader;
+        Loader<KIND, HB, NT, RX> loader;
         loader.rows(lane, a.w12.ld_q, a.w12.ld_s, D);
-        Tile16 rows[2];
+        Tile16 rows[NT];
         int l_q = q0, l_u = 0;  // of the next unit to load
         auto select = [&] {
             const bool there = l_q < all;
             const int q = there ? l_q : q0;
             int first, n;
             const int e = item_rows<PER>(rt, q / width, first, n);
-            const int64_t h0 = 16 * (int64_t)(tile0 + q % width);
-            rows[0] = tile_rows<KIND>(a.w12, e, h0, a.H, D, there);
-            rows[1] = tile_rows<KIND>(a.w12, e, a.H + h0, 2 * a.H, D, there);
+            const int64_t h0 = 16 * NH * (int64_t)(tile0 + q % width);
+#pragma unroll
+            for (int i = 0; i < NH; ++i) {
+                rows[2 * i] = tile_rows<KIND>(a.w12, e, h0 + 16 * i, a.H, D, there);
+                rows[2 * i + 1] = tile_rows<KIND>(a.w12, e, a.H + h0 + 16 * i, 2 * a.H, D, there);
+            }
             loader.tokens([&](int c) { return c < n && there ? rt.token[first + c] * (int)a.ld_x * 2 : kOut; });
         };
         select();
-        f32x4 acc[2][TT];
+        f32x4 acc[NT][TT];
         zero(acc);
         int m_q = q0, m_u = 0;  // of the next one to multiply
         auto put = [&] {
             int first, n;
             item_rows<PER>(rt, m_q / width, first, n);
+            const int64_t h0 = 16 * NH * (int64_t)(tile0 + m_q % width) + 4 * g;
 #pragma unroll
             for (int t = 0; t < TT; ++t)
-                if (16 * t + r < n)
-                    store_h(a, t0 * a.k + first + 16 * t + r, 16 * (int64_t)(tile0 + m_q % width) + 4 * g,
-                            rt.weight[first + 16 * t + r], acc[0][t], acc[1][t]);
+#pragma unroll
+                for (int i = 0; i < NH; ++i)
+                    if (16 * t + r < n && (NH == 1 || h0 + 16 * i < a.H))
+                        store_h(a, t0 * a.k + first + 16 * t + r, h0 + 16 * i, rt.weight[first + 16 * t + r], acc[2 * i][t],
+                                acc[2 * i + 1][t]);
             zero(acc);
         };
-        stream_units<KIND, HB, 2, RX, RING>(
+        stream_units<KIND, HB, NT, RX, RING>(
             s_ring + wave * RING, mine * units, r, g, acc,
             [&](int, uint32_t lds) {
                 loader.load(rows, x, l_u, lds);
@@ -675,50 +704,54 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_tiles_kernel(MoeFewArgs a) 
     });
 }
 
-// Workgroup: 16 columns of the output of every token of the chunk.  The items'
-// units follow one another; each wave streams an equal share of them and adds
-// what an item gave to sums of its own for every token (the weights are in h
-// already), added up at the end in the order of the waves.
-template <int KIND, int RXMAX, int W, int RING>
+// Workgroup: 16 NT columns of the output of every token of the chunk, or with
+// a.splits > 1 its share of them.  The items' units follow one another; each
+// wave streams an equal share of them and adds what an item gave to sums of its
+// own for every token (the weights are in h already), added up at the end in
+// the order of the waves.  Where few columns leave CUs idle, several
+// workgroups share the units, and each leaves its sums in the workspace.
+template <int KIND, int RXMAX, int NT, int W, int RING>
 __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
-    constexpr int PER = item_tokens(RXMAX);
+    constexpr int PER = item_tokens(RXMAX), Q = 4 * NT;  // f32x4 of a token
     extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];
     __shared__ __attribute__((aligned(16))) uint8_t s_ring[W * RING];
     __shared__ OneToken s_one[RXMAX == 1 ? W : 1];
-    const int tile = xcd_tile(blockIdx.x, gridDim.x);
+    const int split = (int)(blockIdx.x % a.splits), tile = xcd_tile(blockIdx.x / a.splits, gridDim.x / a.splits);
     if (tile >= a.tiles) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t0 = (int64_t)blockIdx.y * kFewChunk;
     const int T = (int)(a.T - t0 < kFewChunk ? a.T - t0 : kFewChunk);
-    f32x4* const sums = reinterpret_cast<f32x4*>(s_dyn);  // [wave][token][4]
-    f32x4* const own = sums + wave * T * 4;
-    for (int i = lane; i < T * 4; i += 64) own[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4* const sums = reinterpret_cast<f32x4*>(s_dyn);  // [wave][token][Q]
+    f32x4* const own = sums + wave * T * Q;
+    for (int i = lane; i < T * Q; i += 64) own[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     const Routing rt = RXMAX == 1 ? route_one(a, s_one[wave])
-                                  : route_chunk<PER, 64 * W>(a, t0, T * a.k, s_dyn + W * T * 64, s_ring);
+                                  : route_chunk<PER, 64 * W>(a, t0, T * a.k, s_dyn + W * T * 16 * Q, s_ring);
 
     const int r = lane & 15, g = lane >> 4, H = (int)a.H;
-    const int64_t d0 = 16 * (int64_t)tile;
-    with_places<KIND, RXMAX>(rt.most, [&](auto rx, auto hb) {
+    const int64_t d0 = 16 * NT * (int64_t)tile;
+    with_places<KIND, RXMAX, (NT > 1)>(rt.most, [&](auto rx, auto hb) {
         constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value, TT = RX > 16 ? RX / 16 : 1;
         const int units = (H + Unit<KIND, HB>::kCodes - 1) / Unit<KIND, HB>::kCodes;
-        const int all = rt.items * units, share = (all + W - 1) / W, u0 = min(all, wave * share), mine = min(share, all - u0);
+        const int all = rt.items * units, shares = W * a.splits, share = (all + shares - 1) / shares;
+        const int u0 = min(all, (split * W + wave) * share), mine = min(share, all - u0);
         if (mine <= 0) return;
-        Loader<KIND, HB, 1, RX> loader;
+        Loader<KIND, HB, NT, RX> loader;
         loader.rows(lane, a.wo.ld_q, a.wo.ld_s, H);
         loader.tokens([&](int c) { return c * H * 2; });  // (those past the item's are outside the buffer)
         int l_item = u0 / units, l_u = u0 % units, l_left = mine;  // of the next unit to load
         int m_item = l_item, m_u = l_u;                            // of the next one to multiply
-        Tile16 rows[1];
+        Tile16 rows[NT];
         i32x4 h;
         auto select = [&] {
             const bool there = l_left > 0;
             int first, n;
             const int e = item_rows<PER>(rt, there ? l_item : 0, first, n);
-            rows[0] = tile_rows<KIND>(a.wo, e, d0, a.D, H, there);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) rows[i] = tile_rows<KIND>(a.wo, e, d0 + 16 * i, a.D, H, there);
             h = make_rsrc(a.h + (t0 * a.k + first) * a.H, there ? (int64_t)n * H * 2 : 0);
         };
         select();
-        f32x4 acc[1][TT];
+        f32x4 acc[NT][TT];
         zero(acc);
         auto put = [&] {
             int first, n;
@@ -726,13 +759,16 @@ __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
 #pragma unroll
             for (int t = 0; t < TT; ++t)
                 if (16 * t + r < n) {
-                    f32x4* const s = own + rt.token[first + 16 * t + r] * 4 + g;
-                    const f32x4 v = *s, p = acc[0][t];
-                    *s = f32x4{v[0] + p[0], v[1] + p[1], v[2] + p[2], v[3] + p[3]};
+                    f32x4* const s = own + rt.token[first + 16 * t + r] * Q + g;
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const f32x4 v = s[4 * i], p = acc[i][t];
+                        s[4 * i] = f32x4{v[0] + p[0], v[1] + p[1], v[2] + p[2], v[3] + p[3]};
+                    }
                 }
             zero(acc);
         };
-        stream_units<KIND, HB, 1, RX, RING>(
+        stream_units<KIND, HB, NT, RX, RING>(
             s_ring + wave * RING, mine, r, g, acc,
             [&](int, uint32_t lds) {
                 loader.load(rows, h, l_u, lds);
@@ -746,19 +782,35 @@ __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
         put();
     });
     __syncthreads();
-    for (int i = threadIdx.x; i < T * 4; i += 64 * W) {
-        const int t = i >> 2;
-        const int64_t d = d0 + 4 * (i & 3);
-        if (d >= a.D) continue;
+    for (int i = threadIdx.x; i < T * Q; i += 64 * W) {
         f32x4 v = sums[i];
 #pragma unroll
         for (int w = 1; w < W; ++w) {
-            const f32x4 o = sums[w * T * 4 + i];
+            const f32x4 o = sums[w * T * Q + i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] += o[j];
         }
-        store4(v, a.residual ? a.residual + (t0 + t) * a.ld_res + d : nullptr, a.out + (t0 + t) * a.ld_out + d, false, a.vec, 4);
+        const int64_t t = t0 + i / Q, d = d0 + 4 * (i % Q);
+        if (d >= a.D) continue;
+        if (a.splits > 1)
+            a.part[(split * a.T + t) * (a.D / 4) + d / 4] = v;
+        else
+            store4(v, a.residual ? a.residual + t * a.ld_res + d : nullptr, a.out + t * a.ld_out + d, false, a.vec, 4);
     }
+}
+
+// The sums of the workgroups that shared columns, in their order.
+__global__ __launch_bounds__(256) void moe_few_join_kernel(MoeFewArgs a) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = a.T * (a.D / 4);
+    if (i >= n) return;
+    f32x4 v = a.part[i];
+    for (int p = 1; p < a.splits; ++p) {
+        const f32x4 o = a.part[p * n + i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += o[j];
+    }
+    const int64_t t = i / (a.D / 4), d = 4 * (i % (a.D / 4));
+    store4(v, a.residual ? a.residual + t * a.ld_res + d : nullptr, a.out + t * a.ld_out + d, false, a.vec, 4);
 }
 
 template <int KIND, int HB, int NT, int RX, int W, int RING>
@@ -782,41 +834,66 @@ hipError_t mm_kind(const FewMmArgs& a, hipStream_t stream) {
 
 constexpr int kLds = 160 * 1024;  // of a CU
 
-template <int KIND, int RXMAX, int WU, int RING_U, int WD, int RING_D>
+// Workgroups that share the units of 16 nt columns of the output: enough to
+// give every CU one where a wave without sharing has 32 units and more (half a
+// microsecond each; joining the shares costs five).
+int down_splits(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, int nt, int waves) {
+    const int64_t chunks = (T + kFewChunk - 1) / kFewChunk, tokens = T < kFewChunk ? T : kFewChunk;
+    const int64_t groups = (D + 16 * nt - 1) / (16 * nt) * chunks, slots = tokens * k;
+    const int64_t units = (slots < E ? slots : E) * ((H + 127) / 128);  // of a workgroup, about
+    const int64_t wanted = kCus / groups, room = units / (16 * waves);
+    const int64_t n = wanted < room ? wanted : room;
+    return n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : (int)n;
+}
+
+template <int KIND, int RXMAX, int NH, int WU, int RING_U, int NT, int WD, int RING_D>
 hipError_t moe(MoeFewArgs a, hipStream_t stream) {
     constexpr int PER = item_tokens(RXMAX);
     const int64_t chunks = (a.T + kFewChunk - 1) / kFewChunk, tokens = a.T < kFewChunk ? a.T : kFewChunk;
     const int slots = (int)(tokens * a.k);
-    a.items = (slots < a.E ? slots : a.E) + slots / PER;
+    a.items = (slots < a.E ? slots : a.E) + (tokens > PER ? slots / PER : 0);
     const int table = RXMAX == 1 ? 0 : RoutingLayout(a.E, slots, a.items).bytes;
-    a.tiles = (a.H + 15) / 16;
-    const int64_t padded = (a.tiles + 7) & ~7;
-    if (a.items * a.tiles >= 4096)
-        hipLaunchKernelGGL((moe_few_up_tiles_kernel<KIND, RXMAX, WU, RING_U>), dim3(512, (unsigned)chunks), dim3(64 * WU), table,
-                           stream, a);
-    else
+    const int64_t out_tiles = (a.D + 16 * NT - 1) / (16 * NT);
+    a.splits = down_splits(a.T, a.D, a.H, a.E, a.k, NT, WD);
+    a.part = reinterpret_cast<f32x4*>(a.h + a.T * a.k * a.H);
+    const int64_t wide = (a.H + 16 * NH - 1) / (16 * NH);
+    if (a.items * wide >= 4096 / NH) {
+        a.tiles = wide;
+        hipLaunchKernelGGL((moe_few_up_tiles_kernel<KIND, RXMAX, NH, WU, RING_U>), dim3(512, (unsigned)chunks), dim3(64 * WU),
+                           table, stream, a);
+    } else {
+        a.tiles = (a.H + 15) / 16;
+        const int64_t padded = (a.tiles + 7) & ~7;
         hipLaunchKernelGGL((moe_few_up_kernel<KIND, RXMAX, WU, RING_U>), dim3((unsigned)(a.items * padded), (unsigned)chunks),
                            dim3(64 * WU), table, stream, a);
+    }
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    a.tiles = (a.D + 15) / 16;
-    hipLaunchKernelGGL((moe_few_down_kernel<KIND, RXMAX, WD, RING_D>), dim3((unsigned)((a.tiles + 7) & ~7), (unsigned)chunks),
-                       dim3(64 * WD), table + WD * tokens * 64, stream, a);
+    a.tiles = out_tiles;
+    hipLaunchKernelGGL((moe_few_down_kernel<KIND, RXMAX, NT, WD, RING_D>),
+                       dim3((unsigned)(((a.tiles + 7) & ~7) * a.splits), (unsigned)chunks), dim3(64 * WD),
+                       table + WD * tokens * 64 * NT, stream, a);
+    if (a.splits > 1) {
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(moe_few_join_kernel, dim3((unsigned)((a.T * (a.D / 4) + 255) / 256)), dim3(256), 0, stream, a);
+    }
     return hipGetLastError();
 }
 
 template <int KIND>
 hipError_t moe_kind(const MoeFewArgs& a, hipStream_t stream) {
     // workgroups of 80 KiB, two on a CU
-    if (a.T <= 1) return moe<KIND, 1, 4, 19200, 8, 9728>(a, stream);
-    if (a.T <= 4) return moe<KIND, 4, 4, 19200, 8, 9728>(a, stream);
-    if (a.T <= 8) return moe<KIND, 8, 4, 19200, 8, 9728>(a, stream);
+    if (a.T <= 1) return moe<KIND, 1, 1, 4, 19200, 1, 8, 9728>(a, stream);
+    if (a.T <= 4) return moe<KIND, 4, 1, 4, 19200, 1, 8, 9728>(a, stream);
+    if (a.T <= 8) return moe<KIND, 8, 1, 4, 19200, 1, 8, 9472>(a, stream);
     const int64_t tokens = a.T < kFewChunk ? a.T : kFewChunk;
-    if (tokens * a.k > 12 * a.E && tokens > 16) return moe<KIND, 32, 4, 31104, 4, 27904>(a, stream);
+    if (tokens * a.k > 12 * a.E && tokens > 16) return moe<KIND, 32, 2, 4, 31104, 2, 4, 25600>(a, stream);
+    if (tokens * a.k >= 5 * a.E) return moe<KIND, 16, 2, 4, 19200, 2, 4, 25600>(a, stream);
     const int slots = (int)(tokens * a.k), items = (slots < a.E ? slots : a.E) + slots / 16;
-    if (RoutingLayout(a.E, slots, items).bytes + 8 * tokens * 64 + 8 * 15552 <= kLds)
-        return moe<KIND, 16, 4, 19200, 8, 15552>(a, stream);
-    return moe<KIND, 16, 4, 19200, 8, 12800>(a, stream);
+    if (RoutingLayout(a.E, slots, items).bytes + 8 * tokens * 64 + 8 * 15552 <= kLds - 64)
+        return moe<KIND, 16, 1, 4, 19200, 1, 8, 15552>(a, stream);
+    return moe<KIND, 16, 1, 4, 19200, 1, 8, 12800>(a, stream);
 }
 
 }  // namespace
@@ -824,6 +901,15 @@ hipError_t moe_kind(const MoeFewArgs& a, hipStream_t stream) {
 hipError_t launch_few_mm(const FewMmArgs& a, FewKind kind, hipStream_t stream) {
     return kind == kFewE4m3 ? mm_kind<kFewE4m3>(a, stream)
            : kind == kFewMx8 ? mm_kind<kFewMx8>(a, stream) : mm_kind<kFewMx4>(a, stream);
+}
+
+int64_t moe_few_shares_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k) {
+    int most = 1;
+    for (int nt = 1; nt <= 2; ++nt) {
+        const int n = down_splits(T, D, H, E, k, nt, nt == 1 ? 8 : 4);
+        most = n > most ? n : most;
+    }
+    return most > 1 ? most * T * D * 4 : 0;
 }
 
 hipError_t launch_moe_few(const MoeFewArgs& a, FewKind kind, hipStream_t stream) {

@@ -129,9 +129,11 @@ bs_status bs_few_mm(bs_weight_kind kind, int64_t T, int64_t N, int64_t K, const 
     return hip_status(bs::launch_few_mm(a, few_kind(kind), stream), fn);
 }
 
-int64_t bs_moe_few_workspace_bytes(int64_t T, int64_t k, int64_t H) {
-    if (T < 0 || T > kMaxTokens || k < 1 || k > bs::kMaxTopK || H < 0 || H > bs::kMaxFewDim) return 0;
-    return T * k * H * 2;
+int64_t bs_moe_few_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k) {
+    if (T < 0 || T > kMaxTokens || D < 0 || D > bs::kMaxFewDim || H < 0 || H > bs::kMaxFewDim || E < 1 || E > bs::kMaxExperts ||
+        k < 1 || k > bs::kMaxTopK)
+        return 0;
+    return T == 0 || D == 0 ? 0 : T * k * H * 2 + bs::moe_few_shares_bytes(T, D, H, E, k);
 }
 
 bs_status bs_moe_few(bs_weight_kind kind, int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, const uint16_t* x,
@@ -164,9 +166,9 @@ bs_status bs_moe_few(bs_weight_kind kind, int64_t T, int64_t D, int64_t H, int64
         REQUIRE(ld_res >= D, BS_ERR_LAYOUT, "ld_res=%lld < D=%lld: the residual is row-major [T, D]", (ll)ld_res, (ll)D);
         REQUIRE(aligned_to(residual, 2), BS_ERR_ALIGN, "residual must be aligned to its type");
     }
-    REQUIRE(workspace && workspace_bytes >= bs_moe_few_workspace_bytes(T, k, H), BS_ERR_SHAPE,
+    REQUIRE(workspace && workspace_bytes >= bs_moe_few_workspace_bytes(T, D, H, E, k), BS_ERR_SHAPE,
             "the workspace has %lld bytes: this needs %lld", (ll)(workspace ? workspace_bytes : 0),
-            (ll)bs_moe_few_workspace_bytes(T, k, H));
+            (ll)bs_moe_few_workspace_bytes(T, D, H, E, k));
     REQUIRE(aligned16(workspace), BS_ERR_ALIGN, "workspace must be 16-byte aligned");
     a.T = T; a.D = D; a.H = H; a.E = (int32_t)E; a.k = (int32_t)k;
     a.x = x; a.ld_x = ld_x; a.idx = idx; a.w = w;

@@ -767,8 +767,8 @@ bs_status bs_few_mm(bs_weight_kind kind, int64_t T, int64_t N, int64_t K, const 
  *   out_proj  [E][D, H], stride_wo, ld_wo; s_out, stride_so, ld_so
  *   residual  [T, D] bf16 or NULL (zeros); may be out itself
  *   out       [T, D] bf16, ld_out >= D
- *   workspace bs_moe_few_workspace_bytes(T, k, H) bytes of DEVICE memory, 16-byte
- *             aligned, without initial contents; calls that share one must not
+ *   workspace bs_moe_few_workspace_bytes(T, D, H, E, k) bytes of DEVICE memory,
+ *             16-byte aligned, without initial contents; calls that share one must not
  *             overlap in time
  *   D and H multiples of 128 (E4M3_128X128) or 32 (MX), at most 262144;
  *   1 <= E <= 1024, 1 <= k <= min(E, 32), 0 <= T <= 2^21.
@@ -780,8 +780,10 @@ bs_status bs_moe_few(bs_weight_kind kind, int64_t T, int64_t D, int64_t H, int64
                      const uint16_t* residual, int64_t ld_res, uint16_t* out, int64_t ld_out, void* workspace,
                      int64_t workspace_bytes, hipStream_t stream);
 
-/* Workspace bytes of bs_moe_few (h of every slot).  Invalid arguments give 0. */
-int64_t bs_moe_few_workspace_bytes(int64_t T, int64_t k, int64_t H);
+/* Workspace bytes of bs_moe_few: h of every slot and, where D is small beside
+ * the experts' H, sums of workgroups that share columns (joined by a third
+ * kernel).  Invalid arguments give 0. */
+int64_t bs_moe_few_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k);
 
 /* Human-readable name of a status code (static storage). */
 const char* bs_status_string(bs_status status);

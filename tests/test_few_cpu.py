@@ -110,7 +110,7 @@ def test_product_of_nothing(lib):
 
 MOE = dict(kind=1, T=3, D=96, H=64, E=4, k=2, x=P, ld_x=96, idx=P, w=P, w12=P, stride_w12=128 * 96, ld_w12=96, s12=P,
            stride_s12=3 * 128, ld_s12=128, wo=P, stride_wo=96 * 64, ld_wo=64, so=P, stride_so=2 * 96, ld_so=96, res=None,
-           ld_res=0, out=P, ld_out=96, ws=P, nbytes=3 * 2 * 64 * 2, stream=None)
+           ld_res=0, out=P, ld_out=96, ws=P, nbytes=1 << 24, stream=None)
 
 
 @pytest.mark.parametrize("kw,code,frag", [
@@ -148,7 +148,7 @@ MOE = dict(kind=1, T=3, D=96, H=64, E=4, k=2, x=P, ld_x=96, idx=P, w=P, w12=P, s
     (dict(out=P1), ALIGN, "out"),
     (dict(ld_out=95), LAYOUT, "ld_out"),
     (dict(ws=None), SHAPE, "workspace"),
-    (dict(nbytes=767), SHAPE, "needs 768"),
+    (dict(nbytes=767), SHAPE, "the workspace has 767 bytes: this needs 768"),
     (dict(ws=PU), ALIGN, "workspace"),
 ])
 def test_experts_refusals(lib, kw, code, frag):
@@ -158,8 +158,11 @@ def test_experts_refusals(lib, kw, code, frag):
 def test_experts_of_nothing_and_workspace(lib):
     call(lib, "bs_moe_few", MOE, dict(T=0, x=None, out=None, ws=None, nbytes=0), OK)
     size = lib.bs_moe_few_workspace_bytes
-    assert size(3, 2, 64) == 768 and size(0, 1, 64) == 0
-    for bad in ((-1, 2, 64), (3, 0, 64), (3, 33, 64), (3, 2, -1), (3, 2, 1 << 19)):
+    assert size(3, 96, 64, 4, 2) == 768 and size(0, 96, 64, 4, 1) == 0
+    # few columns beside a long contraction: workgroups share them, and leave their sums
+    assert size(8, 128, 8192, 16, 8) >= 8 * 8 * 8192 * 2 + 2 * 8 * 128 * 4
+    for bad in ((-1, 96, 64, 4, 2), (3, 96, 64, 4, 0), (3, 96, 64, 4, 33), (3, 96, -1, 4, 2), (3, 96, 1 << 19, 4, 2),
+                (3, 1 << 19, 64, 4, 2), (3, 96, 64, 0, 2), (3, 96, 64, 1025, 2)):
         assert size(*bad) == 0
 
 

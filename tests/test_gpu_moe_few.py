@@ -41,7 +41,9 @@ def _run(kind, x, idx, w, weights, residual=None, **kw):
 
 CASES = [(1, 128, 128, 4, 2), (1, 640, 384, 8, 8), (3, 256, 128, 1, 1), (6, 128, 512, 5, 3), (16, 256, 256, 16, 4),
          (17, 384, 128, 8, 2), (32, 128, 256, 2, 1), (40, 256, 128, 3, 2), (64, 128, 128, 64, 8), (67, 128, 128, 6, 2),
-         (130, 128, 256, 4, 1)]
+         (130, 128, 256, 4, 1),
+         # few columns and long contractions: workgroups share them
+         (1, 128, 2048, 8, 8), (10, 128, 1024, 16, 6), (24, 384, 1152, 12, 4), (40, 128, 1536, 4, 2), (66, 128, 1024, 2, 2)]
 
 
 @pytest.mark.parametrize("kind", KINDS)
