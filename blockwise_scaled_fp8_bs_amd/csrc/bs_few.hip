@@ -561,13 +561,16 @@ using Int = std::integral_constant<int, V>;
 constexpr int item_tokens(int rxmax) { return rxmax > 16 ? rxmax : 16; }
 
 // Calls run with the tokens' places and the unit's bytes for items of `most`
-// tokens, RXMAX at most; short units throughout with SHORT.
-template <int KIND, int RXMAX, bool SHORT, class Run>
+// tokens, RXMAX at most.  Units of 128 bytes (whole cache lines: 64 tokens over
+// 64 experts in 4 bits take 119 us in the first kernel, 148 with units of 64),
+// but where the tokens would leave the ring without a second stage: e2m1 beside
+// more than 4 tokens in a ring that is not WIDE, and beside more than 16.
+template <int KIND, int RXMAX, bool WIDE, class Run>
 __device__ __forceinline__ void with_places(int most, Run run) {
-    constexpr int kFew = SHORT ? 64 : 128, kMany = SHORT || KIND == kFewMx4 ? 64 : 128;
-    if (RXMAX == 1 || most <= 1) return run(Int<1>{}, Int<kFew>{});
+    constexpr int kMany = KIND != kFewMx4 || WIDE ? 128 : 64, kMost = KIND != kFewMx4 ? 128 : 64;
+    if (RXMAX == 1 || most <= 1) return run(Int<1>{}, Int<128>{});
     if constexpr (RXMAX > 1) {
-        if (RXMAX == 4 || most <= 4) return run(Int<4>{}, Int<kFew>{});
+        if (RXMAX == 4 || most <= 4) return run(Int<4>{}, Int<128>{});
     }
     if constexpr (RXMAX > 4) {
         if (RXMAX == 8 || most <= 8) return run(Int<8>{}, Int<kMany>{});
@@ -575,7 +578,7 @@ __device__ __forceinline__ void with_places(int most, Run run) {
     if constexpr (RXMAX > 8) {
         if (RXMAX == 16 || most <= 16) return run(Int<16>{}, Int<kMany>{});
     }
-    if constexpr (RXMAX > 16) run(Int<32>{}, Int<64>{});
+    if constexpr (RXMAX > 16) run(Int<32>{}, Int<kMost>{});
 }
 
 // h of one lane's four columns: weight silu(a) b, rounded once.
@@ -846,54 +849,58 @@ int down_splits(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, int nt, i
     return n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : (int)n;
 }
 
-template <int KIND, int RXMAX, int NH, int WU, int RING_U, int NT, int WD, int RING_D>
+// NH, NT: tiles of h and of the output a wave takes at a time; W, RING of the
+// three kernels.
+template <int KIND, int RXMAX, int RING_U, int NH, int RING_T, int NT, int WD, int RING_D>
 hipError_t moe(MoeFewArgs a, hipStream_t stream) {
-    constexpr int PER = item_tokens(RXMAX);
+    constexpr int PER = item_tokens(RXMAX), W = 4;
     const int64_t chunks = (a.T + kFewChunk - 1) / kFewChunk, tokens = a.T < kFewChunk ? a.T : kFewChunk;
     const int slots = (int)(tokens * a.k);
     a.items = (slots < a.E ? slots : a.E) + (tokens > PER ? slots / PER : 0);
     const int table = RXMAX == 1 ? 0 : RoutingLayout(a.E, slots, a.items).bytes;
-    const int64_t out_tiles = (a.D + 16 * NT - 1) / (16 * NT);
     a.splits = down_splits(a.T, a.D, a.H, a.E, a.k, NT, WD);
     a.part = reinterpret_cast<f32x4*>(a.h + a.T * a.k * a.H);
+    // Whole tiles for every wave that is resident, or the waves of a workgroup share one: two items of 32 tokens and
+    // 512 tiles of 5120 e4m3 rows take 20 us by tiles and 52 shared, 24 items and 64 tiles of 2048 28 and 19.
+    constexpr int kGroups = kCus * (2 * W * RING_T <= kLds ? 2 : 1);
     const int64_t wide = (a.H + 16 * NH - 1) / (16 * NH);
-    if (a.items * wide >= 4096 / NH) {
+    if (a.items * wide >= kGroups * W) {
         a.tiles = wide;
-        hipLaunchKernelGGL((moe_few_up_tiles_kernel<KIND, RXMAX, NH, WU, RING_U>), dim3(512, (unsigned)chunks), dim3(64 * WU),
+        hipLaunchKernelGGL((moe_few_up_tiles_kernel<KIND, RXMAX, NH, W, RING_T>), dim3(kGroups, (unsigned)chunks), dim3(64 * W),
                            table, stream, a);
     } else {
         a.tiles = (a.H + 15) / 16;
         const int64_t padded = (a.tiles + 7) & ~7;
-        hipLaunchKernelGGL((moe_few_up_kernel<KIND, RXMAX, WU, RING_U>), dim3((unsigned)(a.items * padded), (unsigned)chunks),
-                           dim3(64 * WU), table, stream, a);
+        hipLaunchKernelGGL((moe_few_up_kernel<KIND, RXMAX, W, RING_U>), dim3((unsigned)(a.items * padded), (unsigned)chunks),
+                           dim3(64 * W), table, stream, a);
     }
-    const hipError_t err = hipGetLastError();
+    hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    a.tiles = out_tiles;
+    a.tiles = (a.D + 16 * NT - 1) / (16 * NT);
     hipLaunchKernelGGL((moe_few_down_kernel<KIND, RXMAX, NT, WD, RING_D>),
                        dim3((unsigned)(((a.tiles + 7) & ~7) * a.splits), (unsigned)chunks), dim3(64 * WD),
                        table + WD * tokens * 64 * NT, stream, a);
-    if (a.splits > 1) {
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(moe_few_join_kernel, dim3((unsigned)((a.T * (a.D / 4) + 255) / 256)), dim3(256), 0, stream, a);
-    }
+    err = hipGetLastError();
+    if (a.splits == 1 || err != hipSuccess) return err;
+    hipLaunchKernelGGL(moe_few_join_kernel, dim3((unsigned)((a.T * (a.D / 4) + 255) / 256)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
 template <int KIND>
 hipError_t moe_kind(const MoeFewArgs& a, hipStream_t stream) {
-    // workgroups of 80 KiB, two on a CU
-    if (a.T <= 1) return moe<KIND, 1, 1, 4, 19200, 1, 8, 9728>(a, stream);
-    if (a.T <= 4) return moe<KIND, 4, 1, 4, 19200, 1, 8, 9728>(a, stream);
-    if (a.T <= 8) return moe<KIND, 8, 1, 4, 19200, 1, 8, 9472>(a, stream);
+    // Up to 8 tokens, workgroups of 80 KiB, two on a CU.
+    if (a.T <= 1) return moe<KIND, 1, 19200, 1, 19200, 1, 8, 9728>(a, stream);
+    if (a.T <= 4) return moe<KIND, 4, 19200, 1, 19200, 1, 8, 9728>(a, stream);
+    if (a.T <= 8) return moe<KIND, 8, 19200, 1, 19200, 1, 8, 9472>(a, stream);
+    // Beside more tokens of an expert a wave takes two tiles at a time, which
+    // halves what it fetches of tokens, in rings of a whole CU.
     const int64_t tokens = a.T < kFewChunk ? a.T : kFewChunk;
-    if (tokens * a.k > 12 * a.E && tokens > 16) return moe<KIND, 32, 2, 4, 31104, 2, 4, 25600>(a, stream);
-    if (tokens * a.k >= 5 * a.E) return moe<KIND, 16, 2, 4, 19200, 2, 4, 25600>(a, stream);
+    if (tokens * a.k > 12 * a.E && tokens > 16) return moe<KIND, 32, 31104, 1, 33792, 2, 4, 25600>(a, stream);
+    if (tokens * a.k >= 5 * a.E) return moe<KIND, 16, 19200, 2, 38400, 2, 4, 25600>(a, stream);
     const int slots = (int)(tokens * a.k), items = (slots < a.E ? slots : a.E) + slots / 16;
-    if (RoutingLayout(a.E, slots, items).bytes + 8 * tokens * 64 + 8 * 15552 <= kLds - 64)
-        return moe<KIND, 16, 1, 4, 19200, 1, 8, 15552>(a, stream);
-    return moe<KIND, 16, 1, 4, 19200, 1, 8, 12800>(a, stream);
+    if (RoutingLayout(a.E, slots, items).bytes + 8 * tokens * 64 + 8 * 15552 <= kLds)
+        return moe<KIND, 16, 19200, 1, 19200, 1, 8, 15552>(a, stream);
+    return moe<KIND, 16, 19200, 1, 19200, 1, 8, 12800>(a, stream);
 }
 
 }  // namespace
