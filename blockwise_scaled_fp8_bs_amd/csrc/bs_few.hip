@@ -560,25 +560,27 @@ using Int = std::integral_constant<int, V>;
 // Tokens of an item, at most, in kernels for RXMAX tokens.
 constexpr int item_tokens(int rxmax) { return rxmax > 16 ? rxmax : 16; }
 
+// Bytes of a unit: whole cache lines (64 tokens over 64 experts in 4 bits take
+// 119 us in the first kernel, 148 with half ones), but where the tokens would
+// leave the ring without a second stage.
+template <int KIND, int NT, int RX, int RING>
+using UnitBytes = Int<RING >= 2 * Stage<KIND, 128, NT, RX>::kBytes ? 128 : 64>;
+
 // Calls run with the tokens' places and the unit's bytes for items of `most`
-// tokens, RXMAX at most.  Units of 128 bytes (whole cache lines: 64 tokens over
-// 64 experts in 4 bits take 119 us in the first kernel, 148 with units of 64),
-// but where the tokens would leave the ring without a second stage: e2m1 beside
-// more than 4 tokens in a ring that is not WIDE, and beside more than 16.
-template <int KIND, int RXMAX, bool WIDE, class Run>
+// tokens, RXMAX at most.
+template <int KIND, int RXMAX, int NT, int RING, class Run>
 __device__ __forceinline__ void with_places(int most, Run run) {
-    constexpr int kMany = KIND != kFewMx4 || WIDE ? 128 : 64, kMost = KIND != kFewMx4 ? 128 : 64;
-    if (RXMAX == 1 || most <= 1) return run(Int<1>{}, Int<128>{});
+    if (RXMAX == 1 || most <= 1) return run(Int<1>{}, UnitBytes<KIND, NT, 1, RING>{});
     if constexpr (RXMAX > 1) {
-        if (RXMAX == 4 || most <= 4) return run(Int<4>{}, Int<128>{});
+        if (RXMAX == 4 || most <= 4) return run(Int<4>{}, UnitBytes<KIND, NT, 4, RING>{});
     }
     if constexpr (RXMAX > 4) {
-        if (RXMAX == 8 || most <= 8) return run(Int<8>{}, Int<kMany>{});
+        if (RXMAX == 8 || most <= 8) return run(Int<8>{}, UnitBytes<KIND, NT, 8, RING>{});
     }
     if constexpr (RXMAX > 8) {
-        if (RXMAX == 16 || most <= 16) return run(Int<16>{}, Int<kMany>{});
+        if (RXMAX == 16 || most <= 16) return run(Int<16>{}, UnitBytes<KIND, NT, 16, RING>{});
     }
-    if constexpr (RXMAX > 16) run(Int<32>{}, Int<kMost>{});
+    if constexpr (RXMAX > 16) run(Int<32>{}, UnitBytes<KIND, NT, 32, RING>{});
 }
 
 // h of one lane's four columns: weight silu(a) b, rounded once.
@@ -612,7 +614,7 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_kernel(MoeFewArgs a) {
     const int64_t h0 = 16 * (int64_t)tile;
     const Tile16 rows[2] = {tile_rows<KIND>(a.w12, e, h0, a.H, D), tile_rows<KIND>(a.w12, e, a.H + h0, 2 * a.H, D)};
     const i32x4 x = make_rsrc(a.x + t0 * a.ld_x, ((T - 1) * a.ld_x + D) * 2);
-    with_places<KIND, RXMAX, false>(n, [&](auto rx, auto hb) {
+    with_places<KIND, RXMAX, 2, RING>(n, [&](auto rx, auto hb) {
         constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value, TT = RX > 16 ? RX / 16 : 1;
         static_assert(RING >= 2 * TT * 1024, "the sums take the ring's place");
         Loader<KIND, HB, 2, RX> loader;
@@ -656,7 +658,7 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_tiles_kernel(MoeFewArgs a) 
     const int q0 = (blockIdx.x >> 3) * W + wave, step = (gridDim.x >> 3) * W, all = rt.items * width;
     if (q0 >= all) return;
     const int mine = (all - q0 + step - 1) / step;
-    with_places<KIND, RXMAX, (NH > 1)>(rt.most, [&](auto rx, auto hb) {
+    with_places<KIND, RXMAX, NT, RING>(rt.most, [&](auto rx, auto hb) {
         constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value, TT = RX > 16 ? RX / 16 : 1;
         const int units = (D + Unit<KIND, HB>::kCodes - 1) / Unit<KIND, HB>::kCodes;
         Loader<KIND, HB, NT, RX> loader;
@@ -732,7 +734,7 @@ __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
 
     const int r = lane & 15, g = lane >> 4, H = (int)a.H;
     const int64_t d0 = 16 * NT * (int64_t)tile;
-    with_places<KIND, RXMAX, (NT > 1)>(rt.most, [&](auto rx, auto hb) {
+    with_places<KIND, RXMAX, NT, RING>(rt.most, [&](auto rx, auto hb) {
         constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value, TT = RX > 16 ? RX / 16 : 1;
         const int units = (H + Unit<KIND, HB>::kCodes - 1) / Unit<KIND, HB>::kCodes;
         const int all = rt.items * units, shares = W * a.splits, share = (all + shares - 1) / shares;
@@ -838,13 +840,13 @@ hipError_t mm_kind(const FewMmArgs& a, hipStream_t stream) {
 constexpr int kLds = 160 * 1024;  // of a CU
 
 // Workgroups that share the units of 16 nt columns of the output: enough to
-// give every CU one where a wave without sharing has 32 units and more (half a
-// microsecond each; joining the shares costs five).
+// give every CU one where a wave without sharing has 20 units and more (half a
+// microsecond each; joining the shares costs four).
 int down_splits(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, int nt, int waves) {
     const int64_t chunks = (T + kFewChunk - 1) / kFewChunk, tokens = T < kFewChunk ? T : kFewChunk;
     const int64_t groups = (D + 16 * nt - 1) / (16 * nt) * chunks, slots = tokens * k;
     const int64_t units = (slots < E ? slots : E) * ((H + 127) / 128);  // of a workgroup, about
-    const int64_t wanted = kCus / groups, room = units / (16 * waves);
+    const int64_t wanted = kCus / groups, room = units / (10 * waves);
     const int64_t n = wanted < room ? wanted : room;
     return n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : (int)n;
 }
@@ -860,16 +862,21 @@ hipError_t moe(MoeFewArgs a, hipStream_t stream) {
     const int table = RXMAX == 1 ? 0 : RoutingLayout(a.E, slots, a.items).bytes;
     a.splits = down_splits(a.T, a.D, a.H, a.E, a.k, NT, WD);
     a.part = reinterpret_cast<f32x4*>(a.h + a.T * a.k * a.H);
-    // Whole tiles for every wave that is resident, or the waves of a workgroup share one: two items of 32 tokens and
-    // 512 tiles of 5120 e4m3 rows take 20 us by tiles and 52 shared, 24 items and 64 tiles of 2048 28 and 19.
-    constexpr int kGroups = kCus * (2 * W * RING_T <= kLds ? 2 : 1);
-    const int64_t wide = (a.H + 16 * NH - 1) / (16 * NH);
-    if (a.items * wide >= kGroups * W) {
+    // The waves of a workgroup share a tile (four microseconds of its own a workgroup, half a microsecond a unit and
+    // wave), or each streams whole tiles: one token over 2 experts of 256 tiles and 5120 rows in 4 bits takes 12 us
+    // shared, 64 tokens of a single e4m3 expert of 512 tiles and 5120 rows 52 shared and 37 by tiles, 32 tokens over 16
+    // experts of 64 tiles and 2048 rows 19 and 28.
+    constexpr int64_t kShared = kCus * (2 * W * RING_U <= kLds ? 2 : 1), kTiles = kCus * (2 * W * RING_T <= kLds ? 2 : 1);
+    constexpr int kCodes = Unit<KIND, 128>::kCodes;
+    const int64_t narrow = (a.H + 15) / 16, wide = (a.H + 16 * NH - 1) / (16 * NH), units = (a.D + kCodes - 1) / kCodes;
+    const int64_t shared = (a.items * narrow + kShared - 1) / kShared * (8 + (units + W - 1) / W);
+    const int64_t by_tiles = 8 + (a.items * wide + kTiles * W - 1) / (kTiles * W) * units * NH;
+    if (by_tiles < shared) {
         a.tiles = wide;
-        hipLaunchKernelGGL((moe_few_up_tiles_kernel<KIND, RXMAX, NH, W, RING_T>), dim3(kGroups, (unsigned)chunks), dim3(64 * W),
+        hipLaunchKernelGGL((moe_few_up_tiles_kernel<KIND, RXMAX, NH, W, RING_T>), dim3((unsigned)kTiles, (unsigned)chunks), dim3(64 * W),
                            table, stream, a);
     } else {
-        a.tiles = (a.H + 15) / 16;
+        a.tiles = narrow;
         const int64_t padded = (a.tiles + 7) & ~7;
         hipLaunchKernelGGL((moe_few_up_kernel<KIND, RXMAX, W, RING_U>), dim3((unsigned)(a.items * padded), (unsigned)chunks),
                            dim3(64 * W), table, stream, a);
@@ -892,11 +899,16 @@ hipError_t moe_kind(const MoeFewArgs& a, hipStream_t stream) {
     if (a.T <= 1) return moe<KIND, 1, 19200, 1, 19200, 1, 8, 9728>(a, stream);
     if (a.T <= 4) return moe<KIND, 4, 19200, 1, 19200, 1, 8, 9728>(a, stream);
     if (a.T <= 8) return moe<KIND, 8, 19200, 1, 19200, 1, 8, 9472>(a, stream);
-    // Beside more tokens of an expert a wave takes two tiles at a time, which
-    // halves what it fetches of tokens, in rings of a whole CU.
+    // Beside more tokens of an expert a wave takes two tiles at a time, which halves what it fetches of tokens, in rings
+    // of a whole CU; not in the second kernel where that leaves half the CUs idle.
     const int64_t tokens = a.T < kFewChunk ? a.T : kFewChunk;
-    if (tokens * a.k > 12 * a.E && tokens > 16) return moe<KIND, 32, 31104, 1, 33792, 2, 4, 25600>(a, stream);
-    if (tokens * a.k >= 5 * a.E) return moe<KIND, 16, 19200, 2, 38400, 2, 4, 25600>(a, stream);
+    const bool wide = a.D >= kCus / 2 * 32;
+    if (tokens * a.k > 12 * a.E && tokens > 16) {
+        if (wide) return moe<KIND, 32, 31104, 1, 33792, 2, 4, 25600>(a, stream);
+        return moe<KIND, 32, 31104, 1, 33792, 1, 4, 20992>(a, stream);
+    }
+    if (tokens * a.k >= 5 * a.E && wide) return moe<KIND, 16, 19200, 2, 38400, 2, 4, 25600>(a, stream);
+    if (tokens * a.k >= 5 * a.E) return moe<KIND, 16, 19200, 2, 38400, 1, 8, 12800>(a, stream);
     const int slots = (int)(tokens * a.k), items = (slots < a.E ? slots : a.E) + slots / 16;
     if (RoutingLayout(a.E, slots, items).bytes + 8 * tokens * 64 + 8 * 15552 <= kLds)
         return moe<KIND, 16, 19200, 1, 19200, 1, 8, 15552>(a, stream);
