@@ -63,6 +63,15 @@ struct Stage {
 
 constexpr int ring_stages(int ring, int stage) { return ring / stage < 6 ? ring / stage : 6; }
 
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+// Bytes of a unit: whole cache lines (64 tokens over 64 experts in 4 bits take
+// 119 us in the first kernel, 148 with half ones), but where the tokens would
+// leave the ring without a second stage.
+template <int KIND, int NT, int RX, int RING>
+using UnitBytes = Int<RING >= 2 * Stage<KIND, 128, NT, RX>::kBytes ? 128 : 64>;
+
 // 16 rows of weights.
 struct Tile16 {
     i32x4 q, s;  // their codes and scales
@@ -117,10 +126,12 @@ struct Loader {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if (KIND == kFewE4m3) {
-                if (lane == 0) dma4(tile[n].s, lds + S::kScaleAt + n * S::kScales, 0, at / 128 * ld_s);
+                if (lane == 0)
+                    dma4(tile[n].s, lds + S::kScaleAt + n * S::kScales, 0, (int)((uint32_t)(at / 128) * (uint32_t)ld_s));
             } else {
                 if (lane < U::kBlocks)
-                    dma16(tile[n].s, lds + S::kScaleAt + n * S::kScales, lane * ld_s, u * U::kBlocks * ld_s);
+                    dma16(tile[n].s, lds + S::kScaleAt + n * S::kScales, lane * ld_s,
+                          (int)((uint32_t)u * U::kBlocks * (uint32_t)ld_s));
             }
         }
         const int xat = u * U::kTokenRow;
@@ -554,17 +565,8 @@ __device__ __forceinline__ int item_rows(const Routing& rt, int it, int& first, 
     return (int)(v >> 16);
 }
 
-template <int V>
-using Int = std::integral_constant<int, V>;
-
 // Tokens of an item, at most, in kernels for RXMAX tokens.
 constexpr int item_tokens(int rxmax) { return rxmax > 16 ? rxmax : 16; }
-
-// Bytes of a unit: whole cache lines (64 tokens over 64 experts in 4 bits take
-// 119 us in the first kernel, 148 with half ones), but where the tokens would
-// leave the ring without a second stage.
-template <int KIND, int NT, int RX, int RING>
-using UnitBytes = Int<RING >= 2 * Stage<KIND, 128, NT, RX>::kBytes ? 128 : 64>;
 
 // Calls run with the tokens' places and the unit's bytes for items of `most`
 // tokens, RXMAX at most.
@@ -818,23 +820,26 @@ __global__ __launch_bounds__(256) void moe_few_join_kernel(MoeFewArgs a) {
     store4(v, a.residual ? a.residual + t * a.ld_res + d : nullptr, a.out + t * a.ld_out + d, false, a.vec, 4);
 }
 
-template <int KIND, int HB, int NT, int RX, int W, int RING>
+template <int KIND, int NT, int RX, int W, int RING>
 hipError_t mm(FewMmArgs a, hipStream_t stream) {
     a.tiles = (a.N + 16 * NT - 1) / (16 * NT);
     const dim3 grid((unsigned)((a.tiles + 7) & ~7), (unsigned)((a.T + RX - 1) / RX));
-    hipLaunchKernelGGL((few_mm_kernel<KIND, HB, NT, RX, W, RING>), grid, dim3(64 * W), 0, stream, a);
+    hipLaunchKernelGGL((few_mm_kernel<KIND, UnitBytes<KIND, NT, RX, RING>::value, NT, RX, W, RING>), grid, dim3(64 * W), 0, stream,
+                       a);
     return hipGetLastError();
 }
 
 template <int KIND>
 hipError_t mm_kind(const FewMmArgs& a, hipStream_t stream) {
-    constexpr int kMany = KIND == kFewMx4 ? 64 : 128;
-    if (a.T <= 1) return mm<KIND, 128, 1, 1, 8, 9728>(a, stream);
-    if (a.T <= 4) return mm<KIND, 128, 1, 4, 8, 9728>(a, stream);
-    if (a.T <= 8) return mm<KIND, kMany, 1, 8, 8, 9728>(a, stream);
-    if (a.T <= 16) return mm<KIND, kMany, 1, 16, 4, 19200>(a, stream);
-    if (a.T <= 32) return mm<KIND, 64, 2, 32, 4, 40960>(a, stream);
-    return mm<KIND, 64, 2, 64, 4, 40960>(a, stream);
+    // Up to 16 rows, workgroups of 80 KiB, two on a CU.
+    if (a.T <= 1) return mm<KIND, 1, 1, 8, 9728>(a, stream);
+    if (a.T <= 4) return mm<KIND, 1, 4, 8, 9728>(a, stream);
+    if (a.T <= 8) return mm<KIND, 1, 8, 8, 9728>(a, stream);
+    if (a.T <= 16) return mm<KIND, 1, 16, 4, 19200>(a, stream);
+    // Beside more, two tiles of columns at a time halve what is fetched of x, where that leaves every CU its workgroup.
+    const bool wide = a.N >= kCus * 32;
+    if (a.T <= 32) return wide ? mm<KIND, 2, 32, 4, 40960>(a, stream) : mm<KIND, 1, 32, 4, 40960>(a, stream);
+    return wide ? mm<KIND, 2, 64, 4, 40960>(a, stream) : mm<KIND, 1, 64, 4, 40960>(a, stream);
 }
 
 constexpr int kLds = 160 * 1024;  // of a CU
@@ -903,15 +908,17 @@ hipError_t moe_kind(const MoeFewArgs& a, hipStream_t stream) {
     // of a whole CU; not in the second kernel where that leaves half the CUs idle.
     const int64_t tokens = a.T < kFewChunk ? a.T : kFewChunk;
     const bool wide = a.D >= kCus / 2 * 32;
+    const int slots = (int)(tokens * a.k), items = (slots < a.E ? slots : a.E) + slots / 16;
+    const int table = RoutingLayout(a.E, slots, items).bytes + 512;
     if (tokens * a.k > 12 * a.E && tokens > 16) {
         if (wide) return moe<KIND, 32, 31104, 1, 33792, 2, 4, 25600>(a, stream);
         return moe<KIND, 32, 31104, 1, 33792, 1, 4, 20992>(a, stream);
     }
-    if (tokens * a.k >= 5 * a.E && wide) return moe<KIND, 16, 19200, 2, 38400, 2, 4, 25600>(a, stream);
-    if (tokens * a.k >= 5 * a.E) return moe<KIND, 16, 19200, 2, 38400, 1, 8, 12800>(a, stream);
-    const int slots = (int)(tokens * a.k), items = (slots < a.E ? slots : a.E) + slots / 16;
-    if (RoutingLayout(a.E, slots, items).bytes + 8 * tokens * 64 + 8 * 15552 <= kLds)
-        return moe<KIND, 16, 19200, 1, 19200, 1, 8, 15552>(a, stream);
+    if (tokens * a.k >= 5 * a.E) {
+        if (wide && table + 4 * 38400 <= kLds) return moe<KIND, 16, 19200, 2, 38400, 2, 4, 25600>(a, stream);
+        return moe<KIND, 16, 19200, 2, 36864, 1, 8, 12800>(a, stream);
+    }
+    if (table + 8 * (tokens * 64 + 15552) <= kLds) return moe<KIND, 16, 19200, 1, 19200, 1, 8, 15552>(a, stream);
     return moe<KIND, 16, 19200, 1, 19200, 1, 8, 12800>(a, stream);
 }
 

@@ -66,6 +66,23 @@ def test_within_the_bound(kind, T, D, H, E, k):
     assert torch.equal(_run(kind, x, idx, w, weights, res), out)
 
 
+@pytest.mark.parametrize("kind,T,H,E,k", [("e4m3", 40, 128, 3, 2), ("mxfp8", 64, 96, 12, 2), ("mxfp4", 40, 64, 3, 2),
+                                          ("mxfp4", 64, 160, 12, 2), ("mxfp4", 64, 32, 200, 32), ("mxfp8", 33, 64, 1, 1)])
+def test_wide_outputs_beside_many_tokens(kind, T, H, E, k):
+    """4096 columns and more: the waves take two tiles of them at a time."""
+    need_gpu()
+    D = 4096 + (0 if kind == "e4m3" else 32)
+    print(f"moe_few {kind} T {T} D {D} H {H} E {E} k {k}", flush=True)
+    rng = np.random.default_rng([T, D, H, E, k])
+    weights, v12, vo = _experts(rng, kind, E, D, H)
+    idx, w = _choices(rng, T, E, k)
+    x, res = bf16(rng, (T, D)), bf16(rng, (T, D))
+    out = _run(kind, x, idx, w, weights, res)
+    ref, bound = few.moe(f64(x), idx, w.astype(np.float64), v12, vo, f64(res))
+    assert (np.abs(f64(out) - ref) <= bound).all()
+    assert torch.equal(_run(kind, x, idx, w, weights, res), out)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("T,E,k", [(1, 6, 3), (9, 40, 4), (33, 7, 3), (64, 3, 2), (70, 5, 2)])
 def test_whole_numbers_are_exact(kind, T, E, k):
