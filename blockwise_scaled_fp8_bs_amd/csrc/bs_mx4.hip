@@ -25,7 +25,10 @@ constexpr int kQRows = 32, kQCols = 256;  // a workgroup's tile: 512-byte row se
 __global__ __launch_bounds__(256) void mx4_quant_kernel(Mx4QuantArgs a) {
     __shared__ uint8_t s_byte[kQCols / 32][kQRows];
     const int t = threadIdx.x;
-    const int64_t r0 = (int64_t)(blockIdx.x / a.col_tiles) * kQRows, c0 = (int64_t)(blockIdx.x % a.col_tiles) * kQCols;
+    // Neighbouring tiles share cache lines where rows are no whole number of them, and run on one XCD.
+    const uint32_t tile = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3), cols_of = (uint32_t)a.col_tiles;
+    const int64_t r0 = (int64_t)(tile / cols_of) * kQRows, c0 = (int64_t)(tile % cols_of) * kQCols;
+    if (r0 >= a.R) return;
     const int rows = (int)(a.R - r0 < kQRows ? a.R - r0 : kQRows);
     const int cols = (int)(a.C - c0 < kQCols ? a.C - c0 : kQCols);
     const int c = 8 * (t & 31), r = t >> 5;
@@ -76,7 +79,7 @@ hipError_t launch_mx4_quant(const Mx4QuantArgs& args, hipStream_t stream) {
     Mx4QuantArgs a = args;
     a.col_tiles = (a.C + kQCols - 1) / kQCols;
     const int64_t tiles = (a.R + kQRows - 1) / kQRows * a.col_tiles;
-    hipLaunchKernelGGL(mx4_quant_kernel, dim3((unsigned)tiles), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(mx4_quant_kernel, dim3((unsigned)((tiles + 7) & ~7)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
