@@ -59,32 +59,67 @@ def _rows_of(t, name, dtype, R, C, index):
     return p, ld if R > 1 else C
 
 
-def _weight(q, s, names, kind, N, K, index, experts=None):
-    """C arguments of weights [N, K], or [experts, N, K]: codes, their strides,
-    scales and theirs.  Strides of dimensions with one entry say nothing."""
-    if kind not in _KINDS:
-        raise ValueError(f"kind must be BS_WEIGHT_E4M3_128X128, BS_WEIGHT_MXFP8 or BS_WEIGHT_MXFP4, got {kind!r}")
-    per, block, rows, dtype = _KINDS[kind]
+def _fail_weight(q, s, names, kind, shape, scales, dtype, index):
+    """Says what is wrong with weights that _weight did not take."""
+    _mat(q, names[0], torch.uint8, len(shape))
+    if q.shape != shape:
+        raise ValueError(f"{names[0]} must be {list(shape)}, got {list(q.shape)}")
+    _mat(s, names[1], dtype, len(shape))
+    if s.shape[:-1] != scales[:-1] or s.shape[-1] < scales[-1]:
+        raise ValueError(f"{names[1]} must be {list(scales[:-1])} x >= {scales[-1]} (K-major), got {list(s.shape)}")
+    _other_gpu(*((q, names[0]) if q.get_device() != index else (s, names[1])), index)
+
+
+def _weight(q, s, names, kind, N, K, index):
+    """Codes of weights [N, K], their row stride, scales and theirs.  Strides of
+    dimensions with one entry say nothing."""
+    how = _KINDS.get(kind)
+    if how is None:
+        _fail_kind(kind)
+    per, block, rows, dtype = how
     row, blocks, cols = K // per, K // block, N // rows
-    lead = () if experts is None else (experts,)
-    if q is None or q.dtype is not torch.uint8 or q.shape != lead + (N, row) or q.stride(-1) != 1:
-        _mat(q, names[0], torch.uint8, len(lead) + 2)
-        raise ValueError(f"{names[0]} must be {list(lead + (N, row))}, got {list(q.shape)}")
-    if s is None or s.dtype is not dtype or s.dim() != len(lead) + 2 or s.shape[:-1] != lead + (blocks,) \
-            or s.shape[-1] < cols or (s.stride(-1) != 1 and s.shape[-1] > 1):
-        _mat(s, names[1], dtype, len(lead) + 2)
-        raise ValueError(f"{names[1]} must be {list(lead + (blocks,))} x >= {cols} (K-major), got {list(s.shape)}")
-    for t, name in zip((q, s), names):
-        if t.get_device() != index:
-            _mat(t, name, t.dtype, len(lead) + 2)
-            _other_gpu(t, name, index)
-    ld = q.stride(-2) if N > 1 else (row + 15) // 16 * 16
-    ld_s = s.stride(-2) if blocks > 1 else s.shape[-1] if rows > 1 else (cols + 15) // 16 * 16
-    if experts is None:
-        return q.data_ptr(), ld, s.data_ptr(), ld_s
-    if experts == 1:
-        return q.data_ptr(), 0, ld, s.data_ptr(), 0, ld_s
-    return q.data_ptr(), q.stride(0), ld, s.data_ptr(), s.stride(0), ld_s
+    if q is None or s is None or q.dtype is not torch.uint8 or s.dtype is not dtype or q.shape != (N, row) \
+            or s.dim() != 2 or q.get_device() != index or s.get_device() != index:
+        _fail_weight(q, s, names, kind, (N, row), (blocks, cols), dtype, index)
+    (ld, unit), (ld_s, unit_s), (have, width) = q.stride(), s.stride(), s.shape
+    if unit != 1 or (unit_s != 1 and width > 1) or have != blocks or width < cols:
+        _fail_weight(q, s, names, kind, (N, row), (blocks, cols), dtype, index)
+    if N == 1:
+        ld = (row + 15) // 16 * 16
+    if blocks == 1:
+        ld_s = width if rows == 1 else (cols + 15) // 16 * 16
+    return q.data_ptr(), ld, s.data_ptr(), ld_s
+
+
+def _experts(q, s, names, kind, E, N, K, index):
+    """The same of E experts' weights [E, N, K], strides between experts first."""
+    how = _KINDS.get(kind)
+    if how is None:
+        _fail_kind(kind)
+    per, block, rows, dtype = how
+    row, blocks, cols = K // per, K // block, N // rows
+    if q is None or s is None or q.dtype is not torch.uint8 or s.dtype is not dtype or q.shape != (E, N, row) \
+            or s.dim() != 3 or q.get_device() != index or s.get_device() != index:
+        _fail_weight(q, s, names, kind, (E, N, row), (E, blocks, cols), dtype, index)
+    (each, ld, unit), (each_s, ld_s, unit_s), (experts, have, width) = q.stride(), s.stride(), s.shape
+    if unit != 1 or (unit_s != 1 and width > 1) or have != blocks or width < cols or experts != E:
+        _fail_weight(q, s, names, kind, (E, N, row), (E, blocks, cols), dtype, index)
+    if blocks == 1:
+        ld_s = width if rows == 1 else (cols + 15) // 16 * 16
+    if E == 1:
+        each = each_s = 0
+    return q.data_ptr(), each, ld, s.data_ptr(), each_s, ld_s
+
+
+def _fail_kind(kind):
+    raise ValueError(f"kind must be BS_WEIGHT_E4M3_128X128, BS_WEIGHT_MXFP8 or BS_WEIGHT_MXFP4, got {kind!r}")
+
+
+def _empty(x, stream, shape, dtype):
+    """A tensor for the call from the pool of its stream, on x's GPU."""
+    if stream is None:
+        return x.new_empty(shape) if dtype is torch.bfloat16 else x.new_empty(shape, dtype=dtype)
+    return _new(stream, shape, dtype, x.device)
 
 
 def bs_mx4_quant_1x32(x, q, s, y=None, stream=None):
@@ -123,7 +158,7 @@ def bs_few_mm(x, w, s, kind, residual=None, out=None, out_dtype=torch.bfloat16, 
     if out is None:
         if out_dtype not in _DT:
             raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
-        out = _new(stream, (T, N), out_dtype, x.device)
+        out = _empty(x, stream, (T, N), out_dtype)
         p_out, ld_out = out.data_ptr() or None, N
     else:
         if out.dtype not in _DT:
@@ -164,16 +199,16 @@ def bs_moe_few(x, idx, w, w12, s12, out_proj, s_out, kind, residual=None, out=No
         p_w = _flat(w, "w", torch.float32, (T, k))
         if w.get_device() != index:
             _other_gpu(w, "w", index)
-    up = _weight(w12, s12, ("w12", "s12"), kind, 2 * H, D, index, E)
-    down = _weight(out_proj, s_out, ("out_proj", "s_out"), kind, D, H, index, E)
+    up = _experts(w12, s12, ("w12", "s12"), kind, E, 2 * H, D, index)
+    down = _experts(out_proj, s_out, ("out_proj", "s_out"), kind, E, D, H, index)
     p_res, ld_res = _rows_of(residual, "residual", bf16, T, D, index)
     if out is None:
-        out = _new(stream, (T, D), bf16, x.device)
+        out = _empty(x, stream, (T, D), bf16)
         p_out, ld_out = out.data_ptr() or None, D
     else:
         p_out, ld_out = _rows_of(out, "out", bf16, T, D, index)
     nbytes = _lib.load().bs_moe_few_workspace_bytes(T, D, H, E, k)
-    workspace = _new(stream, nbytes, torch.uint8, x.device)
+    workspace = _empty(x, stream, (nbytes // 2,), bf16)
     _call("bs_moe_few", index, kind, T, D, H, E, k, p_x, ld_x, p_idx, p_w, *up, *down, p_res, ld_res, p_out, ld_out,
           workspace.data_ptr() or None, nbytes, _stream_of(x, stream))
     return out
