@@ -13,9 +13,12 @@ import torch
 from . import binding as _b
 from . import binding_few as _f
 
-#: tokens up to which a module prepared for serving takes the few-token calls:
-#: what one pass over the weights serves
-FEW_TOKENS = 64
+#: tokens up to which a module prepared for serving takes the few-token calls.
+#: In us, these and the quantizers with the GEMMs: a layer of 8192 x 5120 16 and
+#: 61 for 64 tokens, 30 and 64 for 128, 59 and 69 for 256, 115 and 70 for 512; a
+#: gated FFN of 5120 and 8192 54 and 155, 104 and 160, 183 and 168; 16 experts of
+#: 2048 and 1024, top 4, 46 and 90, 65 and 90, 110 and 93.
+FEW_TOKENS = 128
 
 
 class ServedWeights:

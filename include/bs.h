@@ -749,12 +749,14 @@ bs_status bs_few_mm(bs_weight_kind kind, int64_t T, int64_t N, int64_t K, const 
 
 /*
  * bs_moe_few -- the gated experts of few routed tokens and their weighted sum,
- * in two kernels:
+ * in two kernels (three where D is small beside the experts' contractions):
  *   out[t] = residual[t] + sum_j w[t, j] Wo_e (silu(a) b),  e = idx[t, j],
  *   [a | b] = W12_e x[t] (a from W12's rows [0, H), b from [H, 2H))
  * h = w silu(a) b is rounded once to bf16 (from fp32 a and b: what the matrix
  * instructions take), everything else is in fp32 and rounded once at the end.
- * Only experts that some token chose are read, once for every 64 tokens.
+ * Only experts that some token chose are read, for 16 to 32 of an expert's
+ * tokens at a time.  A token's result does not depend on the other tokens, but
+ * for the order of its sums.
  *   x         [T, D] bf16, ld_x >= D
  *   idx       [T, k] int32, contiguous, as bs_moe_route gives them; values
  *             outside [0, E) are not routed, and their w is not used.  NULL

@@ -22,6 +22,8 @@ What it computes (plain numpy, slow on purpose):
   quantize).
 * ``mx``     -- the MXFP8 variant (OCP Microscaling: 32-element blocks, E8M0
   power-of-two scales, E4M3 elements) quantizer and its GEMM.
+* ``few``    -- serving few tokens: the MXFP4 quantizer, products with weights
+  of the three formats and the gated experts of routed tokens, with bounds.
 
 Sources: the three pytorch/ao pull-request pages on blockwise FP8 training
 ("[not for land] float8 blockwise scaling training prototype using

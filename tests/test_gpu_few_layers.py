@@ -39,7 +39,7 @@ def test_linear_layers(cls, weights):
     m = cls(640, 384, device="cuda").eval().prepare_serving(weights)
     w = _values(m.weight, weights)
     with torch.no_grad():
-        for T in (1, 3, 16, 40, 64):
+        for T in (1, 3, 16, 40, 64, 128):
             print(f"{cls.__name__} {weights} {T} tokens", flush=True)
             x = _x(T, 640, T)
             y = m(x.view(1, T, 640))
@@ -47,7 +47,7 @@ def test_linear_layers(cls, weights):
             ref, bound = few.few_mm(f64(x), w)
             assert (np.abs(f64(y[0]) - ref) <= bound).all()
         # more tokens: the training forward's GEMM on the same codes
-        for T in (65, 128, 300):
+        for T in (129, 256, 300):
             print(f"{cls.__name__} {weights} {T} tokens", flush=True)
             x = _x(T, 640, T)
             y = m(x)
@@ -141,7 +141,7 @@ def test_layout_of_exchanged_weights():
             p.copy_(other)
             with pytest.raises(RuntimeError, match="call it again"):
                 m(x)
-            assert torch.equal(m.prepare_serving()(x), got)
+            assert torch.equal(m.prepare_serving(few_tokens=4)(x), got)
             m.load_state_dict({**m.state_dict(), name: old})
             assert m._serving is None and torch.equal(m(x), plain)
             m.prepare_serving().train()
