@@ -65,7 +65,13 @@ struct Stage {
     static constexpr int kLoads = NT * (kTileLoads + 1) + kCopies;
 };
 
-constexpr int ring_stages(int ring, int stage) { return ring / stage < 6 ? ring / stage : 6; }
+// Stages of a ring: at most 6, and at most 63 loads under way (the counter that
+// a wave waits by has six bits).
+template <class S>
+constexpr int ring_stages(int ring) {
+    const int fit = ring / S::kBytes, count = 63 / S::kLoads, most = fit < count ? fit : count;
+    return most < 6 ? most : 6;
+}
 
 template <int V>
 using Int = std::integral_constant<int, V>;
@@ -74,7 +80,7 @@ using Int = std::integral_constant<int, V>;
 // 119 us in the first kernel, 148 with half ones), but where the tokens would
 // leave the ring without a second stage.
 template <int KIND, int NT, int RX, int RING>
-using UnitBytes = Int<RING >= 2 * Stage<KIND, 128, NT, RX>::kBytes ? 128 : 64>;
+using UnitBytes = Int<ring_stages<Stage<KIND, 128, NT, RX>>(RING) >= 2 ? 128 : 64>;
 
 // 16 rows of weights.
 struct Tile16 {
@@ -249,9 +255,8 @@ template <int KIND, int HB, int NT, int RX, int RING, int TT, class Load, class 
 __device__ __forceinline__ void stream_units(const uint8_t* ring, int units, int r, int g, f32x4 (&acc)[NT][TT], Load load,
                                              Before before) {
     using S = Stage<KIND, HB, NT, RX>;
-    constexpr int DEPTH = ring_stages(RING, S::kBytes);
+    constexpr int DEPTH = ring_stages<S>(RING);
     static_assert(DEPTH >= 2, "a ring of two stages at least");
-    static_assert((DEPTH - 1) * S::kLoads < 64, "the counter of loads under way has six bits");
     const uint32_t base = lds_addr(ring);
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) load(d, base + d * S::kBytes);
@@ -850,7 +855,8 @@ hipError_t mm_kind(const FewMmArgs& a, hipStream_t stream) {
     if (a.T <= 4) return mm<KIND, 1, 4, 8, 9728>(a, stream);
     if (a.T <= 8) return mm<KIND, 1, 8, 8, 9728>(a, stream);
     if (a.T <= 16) return mm<KIND, 1, 16, 4, 19200>(a, stream);
-    // Beside more, two tiles of columns at a time halve what is fetched of x, where that leaves every CU its workgroup.
+    // Beside more, two tiles of columns at a time halve what is fetched of x, where that leaves every CU its workgroup: 64
+    // rows of 5120 by 8192 e2m1 columns 14.5 us and 22.1 with one tile, 22 rows of 6400 by 3328 e4m3 columns 12.9 and 9.5.
     const bool wide = a.N >= kCus * 32;
     if (a.T <= 32) return wide ? mm<KIND, 2, 32, 4, 40960>(a, stream) : mm<KIND, 1, 32, 4, 40960>(a, stream);
     return wide ? mm<KIND, 2, 64, 4, 40960>(a, stream) : mm<KIND, 1, 64, 4, 40960>(a, stream);
@@ -919,7 +925,10 @@ hipError_t moe_kind(const MoeFewArgs& a, hipStream_t stream) {
     if (a.T <= 4) return moe<KIND, 4, 19200, 1, 19200, 1, 8, 9728>(a, stream);
     if (a.T <= 8) return moe<KIND, 8, 19200, 1, 19200, 1, 8, 9472>(a, stream);
     // Beside more tokens of an expert a wave takes two tiles at a time, which halves what it fetches of tokens, in rings
-    // of a whole CU; not in the second kernel where that leaves half the CUs idle.
+    // of a whole CU (64 tokens over 64 e2m1 experts of 2048, width 4096: 119 + 63 us, 153 + 95 with one); not in the
+    // second kernel where that leaves half the CUs idle (32 tokens over 16 e4m3 experts of 1024, width 2048: 15 us, 18
+    // with two and shares).  Where experts have more than 12 tokens, many have more than 16: items of 32 read their
+    // weights once (64 tokens of one e4m3 expert of 8192, width 5120: 37 + 30 us, 62 + 49 by items of 16).
     const int64_t tokens = a.T < kFewChunk ? a.T : kFewChunk;
     const bool wide = a.D >= kCus / 2 * 32;
     const int slots = (int)(tokens * a.k), items = (slots < a.E ? slots : a.E) + slots / 16;
