@@ -27,14 +27,21 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // the two stages apart); the kernel waits for them explicitly (vmcnt(0))
 // before the barrier that publishes the stage.
 // Byte address = buffer base + voffset (per lane) + soffset (uniform).
+//
+// The compiler keeps the wait states that gfx9 asks of software for its own
+// instructions, not for those in inline asm: one between a write of m0 and a
+// load into LDS, five between a vector instruction's write of a scalar register
+// (v_readfirstlane, and v_readlane where scalar registers were spilled) and a
+// vector memory instruction that reads it.  The operands are there before the
+// asm begins, so s_mov_b32 and the four states of s_nop 3 are both.
 __device__ __forceinline__ void dma16(i32x4 rs, uint32_t lds_base, int voffset, int soffset) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :: "s"(__builtin_amdgcn_readfirstlane(lds_base)), "v"(voffset), "s"(rs),
                     "s"(__builtin_amdgcn_readfirstlane(soffset)) : "memory");
 }
 
 __device__ __forceinline__ void dma4(i32x4 rs, uint32_t lds_base, int voffset, int soffset) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds"
                  :: "s"(__builtin_amdgcn_readfirstlane(lds_base)), "v"(voffset), "s"(rs),
                     "s"(__builtin_amdgcn_readfirstlane(soffset)) : "memory");
 }
