@@ -124,7 +124,8 @@ struct Loader {
         }
     }
 
-    // S::kLoads loads, whatever is there of the unit
+    // S::kLoads loads, whatever is there of the unit: what lies past the contraction is fetched from kOut, also the scales
+    // (a byte 255 behind the last row of them would make NaN of the zeros in their place)
     __device__ __forceinline__ void load(const Tile16 (&tile)[NT], const i32x4 x, int u, uint32_t lds) const {
         const int at = u * HB;
         const bool in = at + piece < row_bytes;
@@ -137,10 +138,11 @@ struct Loader {
         for (int n = 0; n < NT; ++n) {
             if (KIND == kFewE4m3) {
                 if (lane == 0)
-                    dma4(tile[n].s, lds + S::kScaleAt + n * S::kScales, 0, (int)((uint32_t)(at / 128) * (uint32_t)ld_s));
+                    dma4(tile[n].s, lds + S::kScaleAt + n * S::kScales, at < K ? 0 : kOut,
+                         (int)((uint32_t)(at / 128) * (uint32_t)ld_s));
             } else {
                 if (lane < U::kBlocks)
-                    dma16(tile[n].s, lds + S::kScaleAt + n * S::kScales, lane * ld_s,
+                    dma16(tile[n].s, lds + S::kScaleAt + n * S::kScales, 32 * (u * U::kBlocks + lane) < K ? lane * ld_s : kOut,
                           (int)((uint32_t)u * U::kBlocks * (uint32_t)ld_s));
             }
         }
