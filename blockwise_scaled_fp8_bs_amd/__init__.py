@@ -56,6 +56,8 @@ from .binding_few import (  # noqa: F401,E402
     BS_WEIGHT_E4M3_128X128,
     BS_WEIGHT_MXFP4,
     BS_WEIGHT_MXFP8,
+    bs_diag_few_mm_plan,
+    bs_diag_moe_few_plan,
     bs_few_mm,
     bs_moe_few,
     bs_mx4_quant_1x32,

@@ -67,6 +67,8 @@ SIGNATURES = {
     "bs_diag_e4m3_census": (_E, [_P, _P, _P, _P]),
     "bs_diag_division": (_E, [_P, _P]),
     "bs_diag_stream": (_E, [_P, _I64, _P, _I64, _P]),
+    "bs_diag_few_mm_plan": (_E, [_E, _I64, _I64, _I64, _P]),
+    "bs_diag_moe_few_plan": (_E, [_E, _I64, _I64, _I64, _I64, _I64, _P]),
 }
 
 _lib = None

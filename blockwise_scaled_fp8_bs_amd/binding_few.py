@@ -14,6 +14,8 @@ Weights [N, K] by kind, codes as uint8 with contiguous rows:
 * BS_WEIGHT_MXFP4: [N, K/2] (two codes a byte) and uint8 scales [K/32, >= N].
 """
 
+import ctypes
+
 import torch
 
 from . import _lib
@@ -212,3 +214,23 @@ def bs_moe_few(x, idx, w, w12, s12, out_proj, s_out, kind, residual=None, out=No
     _call("bs_moe_few", index, kind, T, D, H, E, k, p_x, ld_x, p_idx, p_w, *up, *down, p_res, ld_res, p_out, ld_out,
           workspace.data_ptr() or None, nbytes, _stream_of(x, stream))
     return out
+
+
+def _plan(fn, names, *sizes):
+    values = (ctypes.c_int64 * len(names))()
+    _check(getattr(_lib.load(), fn)(*sizes, ctypes.addressof(values)), fn)
+    return dict(zip(names, values))
+
+
+def bs_diag_few_mm_plan(kind, T, N, K):
+    """What bs_few_mm runs for these sizes (host only): rows of x and tiles of 16
+    columns of a workgroup, workgroups along the columns, threads of one."""
+    return _plan("bs_diag_few_mm_plan", ("rows", "tiles", "workgroups", "threads"), kind, T, N, K)
+
+
+def bs_diag_moe_few_plan(kind, T, D, H, E, k):
+    """What bs_moe_few runs for these sizes (host only): tokens of an item and
+    items of 64 tokens, at most; tiles of h that a wave streams at a time (0: a
+    workgroup's waves share one) and the waves that they are spread over; tiles
+    of the output of a workgroup and workgroups that share them."""
+    return _plan("bs_diag_moe_few_plan", ("tokens", "items", "up_tiles", "up_waves", "out_tiles", "splits"), kind, T, D, H, E, k)

@@ -72,8 +72,21 @@ struct MoeFewArgs {
 };
 
 hipError_t launch_mx4_quant(const Mx4QuantArgs& a, hipStream_t stream);
-hipError_t launch_few_mm(const FewMmArgs& a, FewKind kind, hipStream_t stream);
-hipError_t launch_moe_few(const MoeFewArgs& a, FewKind kind, hipStream_t stream);
+// What a call runs (bs_diag_few_mm_plan and bs_diag_moe_few_plan).
+struct FewMmPlan {
+    int64_t rows, tiles;          // rows of x and tiles of 16 columns of a workgroup
+    int64_t workgroups, threads;  // along the columns; of a workgroup
+};
+struct MoeFewPlan {
+    int64_t tokens, items;  // tokens of an item, items of a chunk, at most
+    int64_t up_tiles;       // tiles of h that a wave streams at a time, 0: the waves of a workgroup share one
+    int64_t up_waves;       // waves that whole tiles are spread over
+    int64_t out_tiles, splits;  // tiles of the output at a time, workgroups that share them
+};
+
+// With `plan`: nothing is launched, it says what would be.
+hipError_t launch_few_mm(const FewMmArgs& a, FewKind kind, hipStream_t stream, FewMmPlan* plan = nullptr);
+hipError_t launch_moe_few(const MoeFewArgs& a, FewKind kind, hipStream_t stream, MoeFewPlan* plan = nullptr);
 
 // Workspace of the workgroups that share columns of the output (0: none can).
 int64_t moe_few_shares_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k);

@@ -841,9 +841,14 @@ __global__ __launch_bounds__(256) void moe_few_join_kernel(MoeFewArgs a) {
     store4(v, a.residual ? a.residual + t * a.ld_res + d : nullptr, a.out + t * a.ld_out + d, false, a.vec, 4);
 }
 
+// The launchers below only say in `plan` what they would run where there is one.
 template <int KIND, int NT, int RX, int W, int RING>
-hipError_t mm(FewMmArgs a, hipStream_t stream) {
+hipError_t mm(FewMmArgs a, hipStream_t stream, FewMmPlan* plan) {
     a.tiles = (a.N + 16 * NT - 1) / (16 * NT);
+    if (plan) {
+        *plan = {RX, NT, (a.tiles + 7) & ~(int64_t)7, 64 * W};
+        return hipSuccess;
+    }
     const dim3 grid((unsigned)((a.tiles + 7) & ~7), (unsigned)((a.T + RX - 1) / RX));
     hipLaunchKernelGGL((few_mm_kernel<KIND, UnitBytes<KIND, NT, RX, RING>::value, NT, RX, W, RING>), grid, dim3(64 * W), 0, stream,
                        a);
@@ -851,17 +856,17 @@ hipError_t mm(FewMmArgs a, hipStream_t stream) {
 }
 
 template <int KIND>
-hipError_t mm_kind(const FewMmArgs& a, hipStream_t stream) {
+hipError_t mm_kind(const FewMmArgs& a, hipStream_t stream, FewMmPlan* plan) {
     // Up to 16 rows, workgroups of 80 KiB, two on a CU.
-    if (a.T <= 1) return mm<KIND, 1, 1, 8, 9728>(a, stream);
-    if (a.T <= 4) return mm<KIND, 1, 4, 8, 9728>(a, stream);
-    if (a.T <= 8) return mm<KIND, 1, 8, 8, 9728>(a, stream);
-    if (a.T <= 16) return mm<KIND, 1, 16, 4, 19200>(a, stream);
+    if (a.T <= 1) return mm<KIND, 1, 1, 8, 9728>(a, stream, plan);
+    if (a.T <= 4) return mm<KIND, 1, 4, 8, 9728>(a, stream, plan);
+    if (a.T <= 8) return mm<KIND, 1, 8, 8, 9728>(a, stream, plan);
+    if (a.T <= 16) return mm<KIND, 1, 16, 4, 19200>(a, stream, plan);
     // Beside more, two tiles of columns at a time halve what is fetched of x, where that leaves every CU its workgroup: 64
     // rows of 5120 by 8192 e2m1 columns 14.5 us and 22.1 with one tile, 22 rows of 6400 by 3328 e4m3 columns 12.9 and 9.5.
     const bool wide = a.N >= kCus * 32;
-    if (a.T <= 32) return wide ? mm<KIND, 2, 32, 4, 40960>(a, stream) : mm<KIND, 1, 32, 4, 40960>(a, stream);
-    return wide ? mm<KIND, 2, 64, 4, 40960>(a, stream) : mm<KIND, 1, 64, 4, 40960>(a, stream);
+    if (a.T <= 32) return wide ? mm<KIND, 2, 32, 4, 40960>(a, stream, plan) : mm<KIND, 1, 32, 4, 40960>(a, stream, plan);
+    return wide ? mm<KIND, 2, 64, 4, 40960>(a, stream, plan) : mm<KIND, 1, 64, 4, 40960>(a, stream, plan);
 }
 
 constexpr int kLds = 160 * 1024;  // of a CU
@@ -881,7 +886,7 @@ int down_splits(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, int nt, i
 // NH, NT: tiles of h and of the output a wave takes at a time; W, RING of the
 // three kernels.
 template <int KIND, int RXMAX, int RING_U, int NH, int RING_T, int NT, int WD, int RING_D>
-hipError_t moe(MoeFewArgs a, hipStream_t stream) {
+hipError_t moe(MoeFewArgs a, hipStream_t stream, MoeFewPlan* plan) {
     constexpr int PER = item_tokens(RXMAX), W = 4;
     const int64_t chunks = (a.T + kFewChunk - 1) / kFewChunk, tokens = a.T < kFewChunk ? a.T : kFewChunk;
     const int slots = (int)(tokens * a.k);
@@ -898,6 +903,10 @@ hipError_t moe(MoeFewArgs a, hipStream_t stream) {
     const int64_t narrow = (a.H + 15) / 16, wide = (a.H + 16 * NH - 1) / (16 * NH), units = (a.D + kCodes - 1) / kCodes;
     const int64_t shared = (a.items * narrow + kShared - 1) / kShared * (8 + (units + W - 1) / W);
     const int64_t by_tiles = 8 + (a.items * wide + kTiles * W - 1) / (kTiles * W) * units * NH;
+    if (plan) {
+        *plan = {PER, a.items, by_tiles < shared ? NH : 0, kTiles * W, NT, a.splits};
+        return hipSuccess;
+    }
     if (by_tiles < shared) {
         a.tiles = wide;
         hipLaunchKernelGGL((moe_few_up_tiles_kernel<KIND, RXMAX, NH, W, RING_T>), dim3((unsigned)kTiles, (unsigned)chunks), dim3(64 * W),
@@ -921,11 +930,11 @@ hipError_t moe(MoeFewArgs a, hipStream_t stream) {
 }
 
 template <int KIND>
-hipError_t moe_kind(const MoeFewArgs& a, hipStream_t stream) {
+hipError_t moe_kind(const MoeFewArgs& a, hipStream_t stream, MoeFewPlan* plan) {
     // Up to 8 tokens, workgroups of 80 KiB, two on a CU.
-    if (a.T <= 1) return moe<KIND, 1, 19200, 1, 19200, 1, 8, 9728>(a, stream);
-    if (a.T <= 4) return moe<KIND, 4, 19200, 1, 19200, 1, 8, 9728>(a, stream);
-    if (a.T <= 8) return moe<KIND, 8, 19200, 1, 19200, 1, 8, 9472>(a, stream);
+    if (a.T <= 1) return moe<KIND, 1, 19200, 1, 19200, 1, 8, 9728>(a, stream, plan);
+    if (a.T <= 4) return moe<KIND, 4, 19200, 1, 19200, 1, 8, 9728>(a, stream, plan);
+    if (a.T <= 8) return moe<KIND, 8, 19200, 1, 19200, 1, 8, 9472>(a, stream, plan);
     // Beside more tokens of an expert a wave takes two tiles at a time, which halves what it fetches of tokens, in rings
     // of a whole CU (64 tokens over 64 e2m1 experts of 2048, width 4096: 119 + 63 us, 153 + 95 with one); not in the
     // second kernel where that leaves half the CUs idle (32 tokens over 16 e4m3 experts of 1024, width 2048: 15 us, 18
@@ -936,22 +945,22 @@ hipError_t moe_kind(const MoeFewArgs& a, hipStream_t stream) {
     const int slots = (int)(tokens * a.k), items = (slots < a.E ? slots : a.E) + slots / 16;
     const int table = RoutingLayout(a.E, slots, items).bytes + 512;
     if (tokens * a.k > 12 * a.E && tokens > 16) {
-        if (wide) return moe<KIND, 32, 31104, 1, 33792, 2, 4, 25600>(a, stream);
-        return moe<KIND, 32, 31104, 1, 33792, 1, 4, 20992>(a, stream);
+        if (wide) return moe<KIND, 32, 31104, 1, 33792, 2, 4, 25600>(a, stream, plan);
+        return moe<KIND, 32, 31104, 1, 33792, 1, 4, 20992>(a, stream, plan);
     }
     if (tokens * a.k >= 5 * a.E) {
-        if (wide && table + 4 * 38400 <= kLds) return moe<KIND, 16, 19200, 2, 38400, 2, 4, 25600>(a, stream);
-        return moe<KIND, 16, 19200, 2, 36864, 1, 8, 12800>(a, stream);
+        if (wide && table + 4 * 38400 <= kLds) return moe<KIND, 16, 19200, 2, 38400, 2, 4, 25600>(a, stream, plan);
+        return moe<KIND, 16, 19200, 2, 36864, 1, 8, 12800>(a, stream, plan);
     }
-    if (table + 8 * (tokens * 64 + 15552) <= kLds) return moe<KIND, 16, 19200, 1, 19200, 1, 8, 15552>(a, stream);
-    return moe<KIND, 16, 19200, 1, 19200, 1, 8, 12800>(a, stream);
+    if (table + 8 * (tokens * 64 + 15552) <= kLds) return moe<KIND, 16, 19200, 1, 19200, 1, 8, 15552>(a, stream, plan);
+    return moe<KIND, 16, 19200, 1, 19200, 1, 8, 12800>(a, stream, plan);
 }
 
 }  // namespace
 
-hipError_t launch_few_mm(const FewMmArgs& a, FewKind kind, hipStream_t stream) {
-    return kind == kFewE4m3 ? mm_kind<kFewE4m3>(a, stream)
-           : kind == kFewMx8 ? mm_kind<kFewMx8>(a, stream) : mm_kind<kFewMx4>(a, stream);
+hipError_t launch_few_mm(const FewMmArgs& a, FewKind kind, hipStream_t stream, FewMmPlan* plan) {
+    return kind == kFewE4m3 ? mm_kind<kFewE4m3>(a, stream, plan)
+           : kind == kFewMx8 ? mm_kind<kFewMx8>(a, stream, plan) : mm_kind<kFewMx4>(a, stream, plan);
 }
 
 int64_t moe_few_shares_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k) {
@@ -963,9 +972,9 @@ int64_t moe_few_shares_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t
     return most > 1 ? most * T * D * 4 : 0;
 }
 
-hipError_t launch_moe_few(const MoeFewArgs& a, FewKind kind, hipStream_t stream) {
-    return kind == kFewE4m3 ? moe_kind<kFewE4m3>(a, stream)
-           : kind == kFewMx8 ? moe_kind<kFewMx8>(a, stream) : moe_kind<kFewMx4>(a, stream);
+hipError_t launch_moe_few(const MoeFewArgs& a, FewKind kind, hipStream_t stream, MoeFewPlan* plan) {
+    return kind == kFewE4m3 ? moe_kind<kFewE4m3>(a, stream, plan)
+           : kind == kFewMx8 ? moe_kind<kFewMx8>(a, stream, plan) : moe_kind<kFewMx4>(a, stream, plan);
 }
 
 }  // namespace bs

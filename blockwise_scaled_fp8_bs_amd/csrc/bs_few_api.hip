@@ -178,4 +178,33 @@ bs_status bs_moe_few(bs_weight_kind kind, int64_t T, int64_t D, int64_t H, int64
     return hip_status(bs::launch_moe_few(a, few_kind(kind), stream), fn);
 }
 
+bs_status bs_diag_few_mm_plan(bs_weight_kind kind, int64_t T, int64_t N, int64_t K, int64_t* plan) {
+    static const char* fn = "bs_diag_few_mm_plan";
+    CHECK(check_kind(fn, kind));
+    REQUIRE(plan, BS_ERR_NULL, "plan is NULL");
+    REQUIRE(T >= 1 && T <= kMaxTokens && N >= 1 && N <= kMaxI32 && K >= 1, BS_ERR_SHAPE,
+            "T=%lld must be in [1, 2^21], N=%lld in [1, 2^31), K=%lld >= 1", (ll)T, (ll)N, (ll)K);
+    bs::FewMmArgs a{};
+    a.T = T; a.N = N; a.K = K;
+    bs::FewMmPlan p;
+    const bs_status st = hip_status(bs::launch_few_mm(a, few_kind(kind), nullptr, &p), fn);
+    if (st == BS_OK) plan[0] = p.rows, plan[1] = p.tiles, plan[2] = p.workgroups, plan[3] = p.threads;
+    return st;
+}
+
+bs_status bs_diag_moe_few_plan(bs_weight_kind kind, int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, int64_t* plan) {
+    static const char* fn = "bs_diag_moe_few_plan";
+    CHECK(check_kind(fn, kind));
+    REQUIRE(plan, BS_ERR_NULL, "plan is NULL");
+    REQUIRE(T >= 1 && D >= 1 && H >= 1 && bs_moe_few_workspace_bytes(T, D, H, E, k) > 0 && k <= E, BS_ERR_SHAPE,
+            "T=%lld, D=%lld, H=%lld, E=%lld or k=%lld is out of range", (ll)T, (ll)D, (ll)H, (ll)E, (ll)k);
+    bs::MoeFewArgs a{};
+    a.T = T; a.D = D; a.H = H; a.E = (int32_t)E; a.k = (int32_t)k;
+    bs::MoeFewPlan p;
+    const bs_status st = hip_status(bs::launch_moe_few(a, few_kind(kind), nullptr, &p), fn);
+    if (st == BS_OK)
+        plan[0] = p.tokens, plan[1] = p.items, plan[2] = p.up_tiles, plan[3] = p.up_waves, plan[4] = p.out_tiles, plan[5] = p.splits;
+    return st;
+}
+
 }  // extern "C"

@@ -837,6 +837,21 @@ bs_status bs_diag_division(unsigned long long* result, hipStream_t stream);
  */
 bs_status bs_diag_stream(const void* src, int64_t n_read, void* dst, int64_t n_write, hipStream_t stream);
 
+/*
+ * What bs_few_mm and bs_moe_few run for a size, for tests and profiles: host
+ * only, nothing is enqueued.
+ *   bs_diag_few_mm_plan   plan[4]: rows of x and tiles of 16 columns of a
+ *                         workgroup, workgroups along the columns, threads of
+ *                         one
+ *   bs_diag_moe_few_plan  plan[6]: tokens of an item and items of 64 tokens, at
+ *                         most; tiles of 16 columns of h that a wave streams at a
+ *                         time (0: a workgroup's waves share one), waves that
+ *                         they are spread over; tiles of the output of a
+ *                         workgroup, workgroups that share them
+ */
+bs_status bs_diag_few_mm_plan(bs_weight_kind kind, int64_t T, int64_t N, int64_t K, int64_t* plan);
+bs_status bs_diag_moe_few_plan(bs_weight_kind kind, int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, int64_t* plan);
+
 #ifdef __cplusplus
 }
 #endif

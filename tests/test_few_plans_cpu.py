@@ -1,0 +1,42 @@
+"""What the few-token calls would launch, and the workspace for it: no GPU."""
+
+import random
+
+import pytest
+
+import blockwise_scaled_fp8_bs_amd as bs
+from blockwise_scaled_fp8_bs_amd import _lib
+
+KINDS = (bs.BS_WEIGHT_E4M3_128X128, bs.BS_WEIGHT_MXFP8, bs.BS_WEIGHT_MXFP4)
+
+
+def _sizes(rng, kind):
+    step = 128 if kind == bs.BS_WEIGHT_E4M3_128X128 else 32
+    E = min(1024, int(2 ** rng.uniform(0, 10.3)))
+    size = lambda top: step * max(1, int(2 ** rng.uniform(0, top)) // step)  # noqa: E731
+    return int(2 ** rng.uniform(0, 9)), rng.choice([size(15), size(15), 4096]), size(15), E, rng.randint(1, min(E, 32))
+
+
+def test_the_workspace_holds_what_a_launch_leaves_in_it():
+    rng = random.Random(1)
+    shared = set()
+    for _ in range(4000):
+        kind = rng.choice(KINDS)
+        T, D, H, E, k = _sizes(rng, kind)
+        plan = bs.bs_diag_moe_few_plan(kind, T, D, H, E, k)
+        # h of every slot, and the sums of workgroups that share columns
+        need = T * k * H * 2 + (plan["splits"] * T * D * 4 if plan["splits"] > 1 else 0)
+        assert _lib.load().bs_moe_few_workspace_bytes(T, D, H, E, k) >= need
+        shared.add((plan["tokens"], plan["out_tiles"], plan["splits"] > 1))
+        # the items' first rows and experts are kept in 16 bits each
+        assert plan["items"] <= 2 ** 15 and min(T, 64) * k < 2 ** 16
+    assert {s for s in shared if s[2]} == {(16, 1, True), (16, 2, True), (32, 1, True), (32, 2, True)}
+
+
+@pytest.mark.parametrize("fn,sizes", [(bs.bs_diag_few_mm_plan, (3, 1, 64, 64)), (bs.bs_diag_few_mm_plan, (1, 0, 64, 64)),
+                                      (bs.bs_diag_few_mm_plan, (1, 1, 0, 64)), (bs.bs_diag_few_mm_plan, (1, 1, 64, 0)),
+                                      (bs.bs_diag_moe_few_plan, (-1, 1, 64, 64, 4, 2)), (bs.bs_diag_moe_few_plan, (1, 0, 64, 64, 4, 2)),
+                                      (bs.bs_diag_moe_few_plan, (1, 1, 64, 64, 4, 5)), (bs.bs_diag_moe_few_plan, (1, 1, 64, 0, 4, 2))])
+def test_sizes_without_a_plan(fn, sizes):
+    with pytest.raises(bs.BsError):
+        fn(*sizes)
