@@ -15,6 +15,7 @@ typedef long long ll;
 
 constexpr int64_t kMaxI32 = 0x7fffffff;
 constexpr int64_t kMaxTokens = (int64_t)1 << 21;   // 32768 chunks: the launch grid's second axis
+constexpr int64_t kMaxThreads = 0xffffffffll;      // of a launch along one axis
 constexpr int64_t kMaxScales = (int64_t)1 << 30;   // bytes of a matrix's scales: 32-bit offsets, past its end too
 
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -96,7 +97,8 @@ bs_status bs_mx4_quant_1x32(const uint16_t* x, int64_t R, int64_t C, int64_t ld_
         REQUIRE(ld_y >= C && ld_y < kMaxLd, BS_ERR_LAYOUT, "ld_y=%lld must be >= C=%lld and < 2^22", (ll)ld_y, (ll)C);
         REQUIRE(aligned16(y) && ld_y % 8 == 0, BS_ERR_ALIGN, "y must be 16-byte aligned with ld_y %% 8 == 0");
     }
-    REQUIRE((R + 31) / 32 * ((C + 255) / 256) <= kMaxI32, BS_ERR_SHAPE, "%lld x %lld is more than one launch takes", (ll)R, (ll)C);
+    const int64_t tiles = (R + 31) / 32 * ((C + 255) / 256);  // of 256 threads; launched in eights
+    REQUIRE((tiles + 7) / 8 * 8 * 256 <= kMaxThreads, BS_ERR_SHAPE, "%lld x %lld is more than one launch takes", (ll)R, (ll)C);
     return hip_status(bs::launch_mx4_quant({x, R, C, ld_x, q, ld_q, s, ld_s, y, ld_y, 0}, stream), fn);
 }
 
@@ -126,6 +128,10 @@ bs_status bs_few_mm(bs_weight_kind kind, int64_t T, int64_t N, int64_t K, const 
     a.residual = residual; a.ld_res = ld_res; a.out = out; a.ld_out = ld_out; a.f32 = f32;
     a.vec = N % 4 == 0 && ld_out % 4 == 0 && aligned_to(out, f32 ? 16 : 8) &&
             (!residual || (ld_res % 4 == 0 && aligned_to(residual, 8)));
+    bs::FewMmPlan plan;
+    CHECK(hip_status(bs::launch_few_mm(a, few_kind(kind), stream, &plan), fn));
+    REQUIRE(plan.workgroups * plan.threads <= kMaxThreads, BS_ERR_SHAPE, "N=%lld with T=%lld is more than one launch takes", (ll)N,
+            (ll)T);
     return hip_status(bs::launch_few_mm(a, few_kind(kind), stream), fn);
 }
 

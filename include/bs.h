@@ -713,7 +713,8 @@ typedef enum bs_weight_kind {
  * values of a row, one E8M0 byte each, byte = floor(log2(amax)) - 2 + 127
  * clamped to [0, 254] (a zero block gets byte 0), elements
  * e2m1(clamp(x / 2^(byte - 127), -6, 6)), nearest even, sign of zero kept.
- *   x  [R, C] bf16, finite, ld_x >= C; C % 32 == 0, any R
+ *   x  [R, C] bf16, finite, ld_x >= C; C % 32 == 0; R up to 2^29 - 256 for C up
+ *      to 256, less by that for more (a launch's 2^32 threads)
  *   q  [R, C / 2] bytes, ld_q >= C / 2, a multiple of 16: column 2j in the low
  *      four bits of byte j, column 2j + 1 in the high ones
  *   s  [C / 32][ld_s >= R] bytes, K-major: s[(c / 32) * ld_s + r], ld_s a
@@ -732,7 +733,9 @@ bs_status bs_mx4_quant_1x32(const uint16_t* x, int64_t R, int64_t C, int64_t ld_
  * change with T.
  *   x         [T, K] bf16, ld_x >= K, 0 <= T <= 2^21 (above 64 the weights are
  *             read once for every 64 rows), K >= 1
- *   w         [N, K] codes of the given kind, ld_w in bytes, a multiple of 16
+ *   w         [N, K] codes of the given kind, ld_w in bytes, a multiple of 16;
+ *             N up to 2^27 - 128 (a launch's 2^32 threads), more beside more than 8
+ *             rows
  *   s         its scales, K-major with row stride ld_s in elements: float
  *             scales aligned to their type; scale bytes 16-byte aligned, ld_s a
  *             multiple of 16, and read (never used) up to the next multiple of

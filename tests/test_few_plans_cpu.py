@@ -40,3 +40,18 @@ def test_the_workspace_holds_what_a_launch_leaves_in_it():
 def test_sizes_without_a_plan(fn, sizes):
     with pytest.raises(bs.BsError):
         fn(*sizes)
+
+
+def test_sizes_past_a_launch_s_threads():
+    """2^32 along an axis: the next size is refused, not left to the launch to fail."""
+    lib, P, SHAPE = _lib.load(), 0x10000, 2
+    quant = lambda R, C: lib.bs_mx4_quant_1x32(P, R, C, C, P, max(C // 2, 16), P, R + 15 & ~15, None, 0, None)  # noqa: E731
+    for R, C in ((2 ** 29 - 255, 32), (2 ** 29 - 255, 256), (2 ** 28 - 127, 288)):
+        assert quant(R, C) == SHAPE and "one launch" in lib.bs_last_error().decode()
+    for T, N in ((1, 2 ** 27 - 127), (8, 2 ** 27 - 127), (9, 2 ** 28 - 127), (16, 2 ** 28 - 127)):
+        N = (N + 127) // 128 * 128
+        for n, refused in ((N - 128, False), (N, True)):
+            plan = bs.bs_diag_few_mm_plan(bs.BS_WEIGHT_E4M3_128X128, T, n, 128)
+            assert (plan["workgroups"] * plan["threads"] >= 2 ** 32) == refused
+        call = lib.bs_few_mm(bs.BS_WEIGHT_E4M3_128X128, T, N, 128, P, 128, P, 128, P, N // 128, None, 0, P, N, 0, None)
+        assert call == SHAPE and "one launch" in lib.bs_last_error().decode()
