@@ -182,7 +182,7 @@ class Float8BlockwiseGatedFFN(_s.ServedWeights, torch.nn.Module):
         return self._lay_out(layout)
 
     def forward(self, x):
-        layout = None if torch.is_grad_enabled() else self._layout()
+        layout = self._layout_for(x)
         if layout is None:
             return float8_blockwise_gated_ffn(x, self.w1, self.w2, self.out_proj)
         *gemm, q12, s12, qo, so, kind, few_tokens = layout

@@ -453,7 +453,7 @@ class Float8BlockwiseMoE(_s.ServedWeights, torch.nn.Module):
             raise ValueError(f"x has {x2.shape[1]} features, the experts expect {self.dim}")
         logits = torch.nn.functional.linear(x2, self.router)
         idx, w = moe_route(logits, self.top_k, bias=self.balance, **self.how)
-        layout = None if torch.is_grad_enabled() or x2.shape[0] == 0 else self._layout()
+        layout = None if x2.shape[0] == 0 else self._layout_for(x, residual)
         if layout is not None:
             r2 = None if residual is None else _rows(residual, "residual")
             if x2.shape[0] <= layout[-1]:

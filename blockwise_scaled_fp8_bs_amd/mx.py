@@ -153,7 +153,7 @@ class Float8MXLinear(_s.ServedWeights, torch.nn.Module):
         return self._lay_out(layout)
 
     def forward(self, x):
-        layout = None if torch.is_grad_enabled() else self._layout()
+        layout = self._layout_for(x)
         if layout is None:
             return float8_mx_linear(x, self.weight)
         q, s, few_q, few_s, kind, few_tokens = layout

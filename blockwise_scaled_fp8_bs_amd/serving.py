@@ -9,6 +9,7 @@ layer's than the GEMMs' is.  More tokens take the GEMMs, on the same weights.
 """
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as _b
 from . import binding_few as _f
@@ -55,6 +56,14 @@ class ServedWeights:
         if any(p._version != version or not p.is_set_to(memory) for p, memory, version in self._served):
             raise RuntimeError("the weights changed after prepare_serving(): call it again")
         return self._serving
+
+    def _layout_for(self, *inputs):
+        """The layout to answer these inputs with: None also where gradients are on.
+        Forward-mode tangents raise, as in training: the kernels would drop them."""
+        layout = None if torch.is_grad_enabled() else self._layout()
+        if layout is not None and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in inputs):
+            raise RuntimeError("forward-mode AD is not supported: the input has a tangent, which would be lost")
+        return layout
 
     def _drop_layout(self):
         self._serving = self._served = None
