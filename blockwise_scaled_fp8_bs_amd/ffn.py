@@ -169,14 +169,14 @@ class Float8BlockwiseGatedFFN(_s.ServedWeights, torch.nn.Module):
 
         def layout(w1, w2, out_proj):
             w12 = torch.cat([w1, w2])
-            if weights == "fp8":
-                gemm = few = _s.rows_128(w12) + _s.rows_128(out_proj)
-                kind = _f.BS_WEIGHT_E4M3_128X128
-            else:
+            few = ()
+            if weights == "mxfp4":
                 q12, s12, w12 = _s.rows_mx4(w12, values=True)
                 qo, so, out_proj = _s.rows_mx4(out_proj, values=True)
-                gemm, few = _s.rows_128(w12) + _s.rows_128(out_proj), (q12, s12, qo, so)
-                kind = _f.BS_WEIGHT_MXFP4
+                few = (q12, s12, qo, so) if few_tokens else ()
+            gemm = _s.rows_128(w12) + _s.rows_128(out_proj)
+            kind = _f.BS_WEIGHT_MXFP4 if few else _f.BS_WEIGHT_E4M3_128X128
+            few = few or gemm
             return gemm + tuple(t[None] for t in few) + (kind, few_tokens)
 
         return self._lay_out(layout)

@@ -141,16 +141,19 @@ class Float8BlockwiseLinear(_s.ServedWeights, torch.nn.Module):
 
         weights: "fp8" (the 128x128 blocks of the training forward) or "mxfp4"
         (4 bits, for half the traffic of few tokens; more tokens take the 4-bit
-        values in FP8).  Up to few_tokens tokens meet it in bf16 (bs_few_mm);
-        more are quantized, as in training.
+        values in FP8, which are kept too: half as much memory again).  Up to
+        few_tokens tokens meet it in bf16 (bs_few_mm); more are quantized, as in
+        training.  With 0 the 4-bit codes, which no pass would read, are not kept.
         """
         _s.check_formats(weights, few_tokens, ("fp8", "mxfp4"))
 
         def layout(w):
-            if weights == "fp8":
-                return _s.rows_128(w) * 2 + (_f.BS_WEIGHT_E4M3_128X128, few_tokens)
-            q, s, y = _s.rows_mx4(w, values=True)
-            return _s.rows_128(y) + (q, s, _f.BS_WEIGHT_MXFP4, few_tokens)
+            few = ()
+            if weights == "mxfp4":
+                q, s, w = _s.rows_mx4(w, values=True)
+                few = (q, s, _f.BS_WEIGHT_MXFP4) if few_tokens else ()
+            gemm = _s.rows_128(w)
+            return gemm + (few or gemm + (_f.BS_WEIGHT_E4M3_128X128,)) + (few_tokens,)
 
         return self._lay_out(layout)
 

@@ -408,24 +408,30 @@ class Float8BlockwiseMoE(_s.ServedWeights, torch.nn.Module):
                 p.uniform_(-p.shape[-1] ** -0.5, p.shape[-1] ** -0.5)
         self.last_counts = None
 
-    def prepare_serving(self, weights="fp8", few_tokens=0):
+    def prepare_serving(self, weights="fp8", few_tokens=None):
         """Quantizes the expert weights for the forward; call again after they
         change.  Not for inference tensors, whose changes nothing counts.
 
         weights: "fp8" (the 128x128 blocks of the training forward) or "mxfp4"
         (4 bits, for half the traffic of few tokens; passes of more tokens take
-        the 4-bit values in FP8).  few_tokens: tokens up to which a pass takes
-        bs_moe_few; 0: none.
+        the 4-bit values in FP8, which are kept too: half as much memory again).
+        few_tokens: tokens up to which a pass takes bs_moe_few; by default none
+        with "fp8", whose passes then give the training forward's bits, and
+        FEW_TOKENS with "mxfp4".  With 0 the 4-bit codes, which no pass would
+        read, are not kept.
         """
+        if few_tokens is None:
+            few_tokens = _s.FEW_TOKENS if weights == "mxfp4" else 0
         _s.check_formats(weights, few_tokens, ("fp8", "mxfp4"))
 
         def layout(w12, out_proj):
-            if weights == "fp8":
-                gemm = _expert_weights(w12)[:2] + _expert_weights(out_proj)[:2]
-                return gemm + gemm + (_f.BS_WEIGHT_E4M3_128X128, few_tokens)
-            q12, s12, w12 = _s.experts_mx4(w12)
-            qo, so, out_proj = _s.experts_mx4(out_proj)
-            return _expert_weights(w12)[:2] + _expert_weights(out_proj)[:2] + (q12, s12, qo, so, _f.BS_WEIGHT_MXFP4, few_tokens)
+            few = ()
+            if weights == "mxfp4":
+                q12, s12, w12 = _s.experts_mx4(w12)
+                qo, so, out_proj = _s.experts_mx4(out_proj)
+                few = (q12, s12, qo, so, _f.BS_WEIGHT_MXFP4) if few_tokens else ()
+            gemm = _expert_weights(w12)[:2] + _expert_weights(out_proj)[:2]
+            return gemm + (few or gemm + (_f.BS_WEIGHT_E4M3_128X128,)) + (few_tokens,)
 
         return self._lay_out(layout)
 

@@ -138,17 +138,20 @@ class Float8MXLinear(_s.ServedWeights, torch.nn.Module):
 
         weights: "mxfp8" (as in training) or "mxfp4" (4 bits, for half the
         traffic of few tokens; more tokens take the 4-bit values in MXFP8,
-        which holds them exactly but for the smallest of all scales).  Up to
-        few_tokens tokens meet it in bf16 (bs_few_mm); more are quantized, as
-        in training.
+        which holds them exactly but for the smallest of all scales, and which
+        is kept too: half as much memory again).  Up to few_tokens tokens meet
+        it in bf16 (bs_few_mm); more are quantized, as in training.  With 0 the
+        4-bit codes, which no pass would read, are not kept.
         """
         _s.check_formats(weights, few_tokens, ("mxfp8", "mxfp4"))
 
         def layout(w):
-            if weights == "mxfp8":
-                return _s.rows_mx8(w) * 2 + (_f.BS_WEIGHT_MXFP8, few_tokens)
-            q, s, y = _s.rows_mx4(w, values=True)
-            return _s.rows_mx8(y) + (q, s, _f.BS_WEIGHT_MXFP4, few_tokens)
+            few = ()
+            if weights == "mxfp4":
+                q, s, w = _s.rows_mx4(w, values=True)
+                few = (q, s, _f.BS_WEIGHT_MXFP4) if few_tokens else ()
+            gemm = _s.rows_mx8(w)
+            return gemm + (few or gemm + (_f.BS_WEIGHT_MXFP8,)) + (few_tokens,)
 
         return self._lay_out(layout)
 
