@@ -128,8 +128,9 @@ class Float8BlockwiseGatedFFN(_s.ServedWeights, torch.nn.Module):
     [out, in] weight).
 
     For serving, ``prepare_serving()`` lays the weights out once; while that
-    layout is there (see ``ServedWeights``) and gradients are off, forward
-    takes any number of tokens.
+    layout is there and gradients are off, forward takes any number of tokens.
+    ``ServedWeights`` says when it is dropped, and until when a pass captured
+    into a graph may be replayed.
     """
 
     _served_names = ("w1", "w2", "out_proj")

@@ -112,8 +112,9 @@ class Float8BlockwiseLinear(_s.ServedWeights, torch.nn.Module):
     blockwise-scaled FP8 (activations and gradients 1x128, weights 128x128).
 
     For serving, ``prepare_serving()`` lays the weight out once; while that
-    layout is there (see ``ServedWeights``) and gradients are off, forward
-    takes any number of tokens.
+    layout is there and gradients are off, forward takes any number of tokens.
+    ``ServedWeights`` says when it is dropped, and until when a pass captured
+    into a graph may be replayed.
     """
 
     _served_names = ("weight",)

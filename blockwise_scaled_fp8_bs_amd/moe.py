@@ -381,9 +381,8 @@ class Float8BlockwiseMoE(_s.ServedWeights, torch.nn.Module):
     only.  With ``prepare_serving(few_tokens=...)`` passes of up to that many
     tokens take the experts in two kernels instead, tokens in bf16, and
     ``last_counts`` is None after them.  Other weights than those laid out are
-    quantized by the forward that they are there for.  A pass captured into a
-    graph reads the memory of the layout that was there: capture it again after
-    prepare_serving(), and do not replay it once the layout was dropped.
+    quantized by the forward that they are there for.  ``ServedWeights`` says
+    until when a pass captured into a graph may be replayed.
     """
 
     _served_names = ("w12", "out_proj")

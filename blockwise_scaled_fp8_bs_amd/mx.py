@@ -111,8 +111,9 @@ class Float8MXLinear(_s.ServedWeights, torch.nn.Module):
     """Bias-free linear layer whose three GEMMs run in MXFP8.
 
     For serving, ``prepare_serving()`` lays the weight out once; while that
-    layout is there (see ``ServedWeights``) and gradients are off, forward
-    takes any number of tokens.
+    layout is there and gradients are off, forward takes any number of tokens.
+    ``ServedWeights`` says when it is dropped, and until when a pass captured
+    into a graph may be replayed.
     """
 
     _served_names = ("weight",)

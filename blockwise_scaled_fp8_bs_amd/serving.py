@@ -32,6 +32,11 @@ class ServedWeights:
     what writes past that (through ``.data``, in a collective, in a kernel of
     one's own) is not seen, and needs prepare_serving() again.  train(), moving
     the module and loading a state drop the layout, and a copy has none.
+
+    A pass captured into a graph reads the memory of the layout that was there,
+    whose checks a replay does not repeat: capture it again after
+    prepare_serving(), and do not replay it once the layout was dropped, when
+    that memory may hold something else.
     """
 
     _serving = _served = None
