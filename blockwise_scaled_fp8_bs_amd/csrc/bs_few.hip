@@ -862,9 +862,12 @@ hipError_t mm_kind(const FewMmArgs& a, hipStream_t stream, FewMmPlan* plan) {
     if (a.T <= 4) return mm<KIND, 1, 4, 8, 9728>(a, stream, plan);
     if (a.T <= 8) return mm<KIND, 1, 8, 8, 9728>(a, stream, plan);
     if (a.T <= 16) return mm<KIND, 1, 16, 4, 19200>(a, stream, plan);
-    // Beside more, two tiles of columns at a time halve what is fetched of x, where that leaves every CU its workgroup: 64
-    // rows of 5120 by 8192 e2m1 columns 14.5 us and 22.1 with one tile, 22 rows of 6400 by 3328 e4m3 columns 12.9 and 9.5.
-    const bool wide = a.N >= kCus * 32;
+    // Beside more, a workgroup fills its CU, and two tiles of columns at a time halve what is fetched of x: taken where one
+    // would need a second round of the CUs.  64 rows of 5120 by e4m3 weights, one tile and two: 4096 columns 15.7 and 19.3
+    // us, 4352 27.3 and 19.5, 6144 28.1 and 20.3, 8192 29.0 and 21.0, 16384 55 and 40; 128 rows of 2048: 2048 columns 7.4 and
+    // 9.0, 2304 12.6 and 9.0.  (17 to 256 rows of 1024 to 5120, the other formats: the same side is the faster one.)
+    const int64_t rows = a.T <= 32 ? 32 : 64, groups = (a.N + 15) / 16 * ((a.T + rows - 1) / rows);
+    const bool wide = groups > kCus;
     if (a.T <= 32) return wide ? mm<KIND, 2, 32, 4, 40960>(a, stream, plan) : mm<KIND, 1, 32, 4, 40960>(a, stream, plan);
     return wide ? mm<KIND, 2, 64, 4, 40960>(a, stream, plan) : mm<KIND, 1, 64, 4, 40960>(a, stream, plan);
 }

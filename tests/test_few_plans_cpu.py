@@ -55,3 +55,15 @@ def test_sizes_past_a_launch_s_threads():
             assert (plan["workgroups"] * plan["threads"] >= 2 ** 32) == refused
         call = lib.bs_few_mm(bs.BS_WEIGHT_E4M3_128X128, T, N, 128, P, 128, P, 128, P, N // 128, None, 0, P, N, 0, None)
         assert call == SHAPE and "one launch" in lib.bs_last_error().decode()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_products_take_one_round_of_the_cus_where_they_can(kind):
+    """Beside 17 rows and more, a workgroup fills a CU: two tiles of columns where one takes a second round of the 256."""
+    for T, one, two in ((17, 4096, 4224), (32, 4096, 5120), (64, 4096, 6144), (64, 1024, 8064), (65, 2048, 2176), (128, 2048, 4096),
+                        (256, 1024, 1152)):
+        plan = bs.bs_diag_few_mm_plan(kind, T, one, 1024)
+        chunks = -(-T // plan["rows"])
+        assert plan["tiles"] == 1 and plan["workgroups"] * chunks <= 256
+        plan = bs.bs_diag_few_mm_plan(kind, T, two, 1024)
+        assert plan["tiles"] == 2 and (plan["workgroups"] * chunks <= 256 or two > 8192 // chunks)

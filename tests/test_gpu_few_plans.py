@@ -19,7 +19,7 @@ UNIT = {"e4m3": 128, "mxfp8": 128, "mxfp4": 256}     # weights of a row in a uni
 # --- products: two tiles of columns a workgroup
 
 def _columns(kind):
-    return (8192, 8320) if kind == "e4m3" else (8192, 8200, 8209, 8225)
+    return (8192, 4224, 8320) if kind == "e4m3" else (8192, 4097, 8200, 6161, 8209, 8225)
 
 
 WIDE = [(kind, T, N, K) for kind in KINDS
