@@ -739,9 +739,12 @@ bs_status bs_mx4_quant_1x32(const uint16_t* x, int64_t R, int64_t C, int64_t ld_
  *   s         its scales, K-major with row stride ld_s in elements: float
  *             scales aligned to their type; scale bytes 16-byte aligned, ld_s a
  *             multiple of 16, and read (never used) up to the next multiple of
- *             16 past the last row of w; below 2^30 bytes of them.  MX weights below 2^-126 in magnitude
- *             may count as 0, and values above the largest bf16 (scale bytes
- *             that no quantizer makes) are infinite.
+ *             16 past the last row of w; below 2^30 bytes of them.  MX weights
+ *             below 2^-126 in magnitude are rounded to bf16 (multiples of
+ *             2^-133; MXFP4's are that), and values above the largest bf16
+ *             (scale bytes that no quantizer makes) are infinite.  A float
+ *             scale multiplies the sum of its 128 codes times x, which has to
+ *             stay in fp32's range itself
  *   residual  [T, N] bf16 or NULL (zeros); may be out itself where that is bf16
  *   out       [T, N] bf16 or fp32, ld_out >= N; rows need no alignment (columns
  *             by fours, 8- or 16-byte aligned, are stored faster)

@@ -56,3 +56,33 @@ def test_rows_behind_the_last_of_experts(kind, K):
         out = bs.bs_moe_few(x, torch.from_numpy(idx).cuda(), torch.from_numpy(w).cuda(), *args, KINDS[kind])
         ref, bound = few.moe(f64(x), idx, w.astype(np.float64), *values)
         assert (np.abs(f64(out) - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("kind", ["mxfp8", "mxfp4"])
+def test_every_scale_byte_with_every_code(kind):
+    """All codes under all scales, alone in their rows: exact where the weight is a normal number of bf16's range; below
+    that it is rounded to bf16's subnormal ones, multiples of 2^-133, and off by 2^-134 at most, half a step; above, it
+    is infinite (and would make NaN of a zero of x)."""
+    need_gpu()
+    codes = 256 if kind == "mxfp8" else 16
+    for byte in range(255):
+        print(f"few_mm {kind}: every code under scale byte {byte}", flush=True)
+        at = byte % 32
+        q = np.zeros((codes, 32), np.uint8)
+        q[:, at] = np.arange(codes)
+        if kind == "mxfp8":
+            q[[0x7F, 0xFF]] = 0                               # NaN
+        else:
+            q = few.pack(q)
+        s = np.full((codes, 1), byte, np.uint8)
+        weight = few.weights(q, s, kind)[:, at]
+        up = 2.0 ** min(max(127 - byte, -100), 100)           # the products are around 1, or normal at least
+        x = torch.zeros((1, 32), dtype=torch.bfloat16, device="cuda")
+        x[0, at] = up
+        w, sw = device_weight(q, s, kind)
+        out, want = f64(bs.bs_few_mm(x, w, sw, KINDS[kind], out_dtype=torch.float32))[0], weight * up
+        small, infinite = np.abs(weight) < 2.0 ** -126, np.abs(weight) >= 2.0 ** 128
+        normal = ~small & ~infinite
+        assert np.array_equal(out[normal], want[normal])
+        assert (np.abs(out[small] - want[small]) <= 2.0 ** -134 * up).all()
+        assert np.isinf(out[infinite]).all() and (np.sign(out[infinite]) == np.sign(weight[infinite])).all()
