@@ -46,6 +46,32 @@ __device__ __forceinline__ void dma4(i32x4 rs, uint32_t lds_base, int voffset, i
                     "s"(__builtin_amdgcn_readfirstlane(soffset)) : "memory");
 }
 
+// N of them from one buffer and uniform offset, 1 KiB after the other in LDS:
+// the five states once, then one after each step of m0.
+template <int N>
+__device__ __forceinline__ void dma16_run(i32x4 rs, uint32_t lds_base, const int* voffset, int soffset) {
+    static_assert(N == 1 || N == 2 || N % 4 == 0, "in fours");
+#define BS_DMA_NEXT "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 "
+    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_base);
+    const int so = __builtin_amdgcn_readfirstlane(soffset);
+    if constexpr (N == 1) {
+        dma16(rs, lds_base, voffset[0], soffset);
+    } else if constexpr (N == 2) {
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %3, %4 offen lds\n\t"
+                     BS_DMA_NEXT "%2, %3, %4 offen lds"
+                     :: "s"(m0), "v"(voffset[0]), "v"(voffset[1]), "s"(rs), "s"(so) : "memory", "scc");
+    } else {
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %5, %6 offen lds\n\t"
+                     BS_DMA_NEXT "%2, %5, %6 offen lds\n\t"
+                     BS_DMA_NEXT "%3, %5, %6 offen lds\n\t"
+                     BS_DMA_NEXT "%4, %5, %6 offen lds"
+                     :: "s"(m0), "v"(voffset[0]), "v"(voffset[1]), "v"(voffset[2]), "v"(voffset[3]), "s"(rs), "s"(so)
+                     : "memory", "scc");
+        if constexpr (N > 4) dma16_run<N - 4>(rs, lds_base + 4096, voffset + 4, soffset);
+    }
+#undef BS_DMA_NEXT
+}
+
 __device__ __forceinline__ void wait_dma() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 }  // namespace bs

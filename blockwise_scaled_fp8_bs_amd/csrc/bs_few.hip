@@ -136,11 +136,11 @@ struct Loader {
     __device__ __forceinline__ void load(const Tile16 (&tile)[NT], const i32x4 x, int u, uint32_t lds) const {
         const int at = u * HB;
         const bool in = at + piece < row_bytes;
+        int off[S::kCopies > S::kTileLoads ? S::kCopies : S::kTileLoads];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < S::kTileLoads; ++i) off[i] = in ? row[i] : kOut;
 #pragma unroll
-            for (int i = 0; i < S::kTileLoads; ++i)
-                dma16(tile[n].q, lds + n * S::kTile + i * 1024, in ? row[i] : kOut, at);
+        for (int n = 0; n < NT; ++n) dma16_run<S::kTileLoads>(tile[n].q, lds + n * S::kTile, off, at);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if (KIND == kFewE4m3) {
@@ -155,10 +155,8 @@ struct Loader {
         }
         const int xat = u * U::kTokenRow;
 #pragma unroll
-        for (int i = 0; i < S::kCopies; ++i) {
-            const int off = xat + token_piece(i, lane) < 2 * K ? token[i] : kOut;
-            if (RX * S::kSlots >= 64 || lane < RX * S::kSlots) dma16(x, lds + S::kTokenAt + i * 1024, off, xat);
-        }
+        for (int i = 0; i < S::kCopies; ++i) off[i] = xat + token_piece(i, lane) < 2 * K ? token[i] : kOut;
+        if (RX * S::kSlots >= 64 || lane < RX * S::kSlots) dma16_run<S::kCopies>(x, lds + S::kTokenAt, off, xat);
     }
 };
 
