@@ -944,12 +944,16 @@ hipError_t moe_kind(const MoeFewArgs& a, hipStream_t stream, MoeFewPlan* plan) {
     if (a.T <= 4) return moe<KIND, 4, 19200, 1, 19200, 1, 8, 9728>(a, stream, plan);
     if (a.T <= 8) return moe<KIND, 8, 19200, 1, 19200, 1, 8, 9472>(a, stream, plan);
     // Beside more tokens of an expert a wave takes two tiles at a time, which halves what it fetches of tokens, in rings
-    // of a whole CU (64 tokens over 64 e2m1 experts of 2048, width 4096: 119 + 63 us, 153 + 95 with one); not in the
-    // second kernel where that leaves half the CUs idle (32 tokens over 16 e4m3 experts of 1024, width 2048: 15 us, 18
-    // with two and shares).  Where experts have more than 12 tokens, many have more than 16: items of 32 read their
-    // weights once (64 tokens of one e4m3 expert of 8192, width 5120: 37 + 30 us, 62 + 49 by items of 16).
+    // of a whole CU (64 tokens over 64 e2m1 experts of 2048, width 4096: 119 + 63 us, 153 + 95 with one).  In the second
+    // kernel where one tile would need a second round of the CUs, or where workgroups that share the tiles fill them:
+    // both kernels in us with one and two, a gated FFN of 8192 in e4m3 of 64 tokens, width 4096 54.9 and 58.8, 5120 85 and
+    // 69, of 128 tokens, width 2048 54 and 58, 2560 78 and 66, 4096 95 and 81; 64 tokens over 16 experts of 1024, width 2560
+    // 48 and 45 (three shares), 4096 64 and 63 (two).  Chunks count by their tokens (65 of them, width 2560, 16 experts: 59
+    // and 65).  Where experts have more than 12 tokens, many have more than 16: items of 32 read their weights once (64
+    // tokens of one e4m3 expert of 8192, width 5120: 37 + 30 us, 62 + 49 by items of 16).
     const int64_t tokens = a.T < kFewChunk ? a.T : kFewChunk;
-    const bool wide = a.D >= kCus / 2 * 32;
+    const int64_t work = a.D * (a.T > kFewChunk ? a.T : kFewChunk), round = kCus * 16 * kFewChunk;
+    const bool wide = work > round || (2 * work > round && down_splits(a.T, a.D, a.H, a.E, a.k, 2, 4) > 1);
     const int slots = (int)(tokens * a.k), items = (slots < a.E ? slots : a.E) + slots / 16;
     const int table = RoutingLayout(a.E, slots, items).bytes + 512;
     if (tokens * a.k > 12 * a.E && tokens > 16) {

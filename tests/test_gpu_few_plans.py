@@ -136,6 +136,22 @@ def test_workgroups_that_share_columns(kind, sizes, tokens, tiles):
     _check(rng, kind, T, D, H, E, k, *_choices(rng, T, E, k))
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("sizes,tokens,tiles", [((128, 2560, 256, 4, 2), 32, 2), ((100, 2816, 128, 16, 3), 16, 2),
+                                                ((64, 4096, 256, 4, 2), 32, 1), ((20, 4224, 128, 8, 3), 16, 2)])
+def test_tiles_of_the_output(kind, sizes, tokens, tiles):
+    """Two at a time where one would need a second round of the CUs, also by the tokens of a second chunk."""
+    need_gpu()
+    T, D, H, E, k = sizes
+    if kind != "e4m3":
+        H += 32
+    plan = bs.bs_diag_moe_few_plan(KINDS[kind], T, D, H, E, k)
+    assert plan["out_tiles"] == tiles and plan["tokens"] == tokens and plan["splits"] == 1
+    print(f"moe_few {kind} T {T} D {D} H {H} E {E} k {k}, {tiles} tiles of the output", flush=True)
+    rng = np.random.default_rng([T, D, H, E, k, 9])
+    _check(rng, kind, T, D, H, E, k, *_choices(rng, T, E, k))
+
+
 # (T, D, H, E, k), tokens of an item, tiles of h that a wave streams at a time
 STREAMED = [((1, 384, 6144, 8, 8), 16, 1), ((2, 384, 4096, 16, 8), 16, 1), ((4, 512, 2048, 24, 8), 16, 1),
             ((5, 384, 4096, 12, 4), 16, 1), ((8, 384, 2048, 24, 4), 16, 1), ((12, 384, 2048, 24, 6), 16, 1),
