@@ -164,8 +164,9 @@ class Float8BlockwiseGatedFFN(_s.ServedWeights, torch.nn.Module):
 
     def prepare_serving(self, weights="fp8", few_tokens=_s.FEW_TOKENS):
         """Quantizes the weights for the forward, w1 and w2 stacked; call again
-        after they change.  weights and few_tokens as for Float8BlockwiseLinear;
-        few tokens take both products in two kernels (bs_moe_few)."""
+        after they change.  weights and few_tokens as for Float8BlockwiseLinear
+        (128 by default); few tokens take both products in two kernels
+        (bs_moe_few)."""
         _s.check_formats(weights, few_tokens, ("fp8", "mxfp4"))
 
         def layout(w1, w2, out_proj):

@@ -134,16 +134,19 @@ class Float8MXLinear(_s.ServedWeights, torch.nn.Module):
             m.weight.copy_(lin.weight.to(torch.bfloat16))
         return m
 
-    def prepare_serving(self, weights="mxfp8", few_tokens=_s.FEW_TOKENS):
+    def prepare_serving(self, weights="mxfp8", few_tokens=None):
         """Quantizes the weight for the forward; call again after it changes.
 
         weights: "mxfp8" (as in training) or "mxfp4" (4 bits, for half the
         traffic of few tokens; more tokens take the 4-bit values in MXFP8,
         which holds them exactly but for the smallest of all scales, and which
         is kept too: half as much memory again).  Up to few_tokens tokens meet
-        it in bf16 (bs_few_mm); more are quantized, as in training.  With 0 the
-        4-bit codes, which no pass would read, are not kept.
+        it in bf16 (bs_few_mm); more are quantized, as in training.  By default
+        128 up to 16384 outputs, 64 up to 32768, less beyond (few_tokens_of).
+        With 0 the 4-bit codes, which no pass would read, are not kept.
         """
+        if few_tokens is None:
+            few_tokens = _s.few_tokens_of(self.out_features)
         _s.check_formats(weights, few_tokens, ("mxfp8", "mxfp4"))
 
         def layout(w):

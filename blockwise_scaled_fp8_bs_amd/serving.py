@@ -14,12 +14,23 @@ from torch.autograd import forward_ad
 from . import binding as _b
 from . import binding_few as _f
 
-#: tokens up to which a module prepared for serving takes the few-token calls.
-#: In us, these and the quantizers with the GEMMs: a layer of 8192 x 5120 16 and
-#: 61 for 64 tokens, 30 and 64 for 128, 59 and 69 for 256, 115 and 70 for 512; a
-#: gated FFN of 5120 and 8192 54 and 155, 104 and 160, 183 and 168; 16 experts of
-#: 2048 and 1024, top 4, 46 and 90, 65 and 90, 110 and 93.
+#: tokens up to which a module prepared for serving takes the few-token calls, narrow dense layers, gated FFNs and
+#: experts in 4 bits.  In us, these and the quantizers with the GEMMs: a layer of 8192 x 5120 17 and 63 for 64 tokens, 32
+#: and 65 for 128, 62 and 70 for 256, 120 and 71 for 512; a gated FFN of 5120 and 8192 58 and 161, 110 and 165, 184 and
+#: 171; 16 experts of 2048 and 1024, top 4, 47 and 92, 67 and 92, 112 and 95.
 FEW_TOKENS = 128
+
+
+def few_tokens_of(columns):
+    """The same of a dense layer with that many outputs.
+
+    The few-token kernel takes a round of the CUs for 8192 of them (and 64 tokens), the GEMM for 65536, about four times
+    as long; from 32768 on both are bound by the bytes of the weights.  In us, weights from memory: 16384 x 5120 40 and
+    82 for 64 tokens, 68 and 87 for 128; 24576 x 5120 58 and 83, 104 and 89; 32768 x 5120 76 and 85, 136 and 91; 65536 x
+    5120 91 and 93 for 17 tokens, 105 and 93 for 32, 147 and 95 for 64.
+    """
+    rounds = -(-columns // 8192) / max(1, -(-columns // 65536))
+    return FEW_TOKENS if rounds <= 2 else 64 if rounds <= 4 else 32 if rounds <= 6 else 16
 
 
 class ServedWeights:
@@ -156,5 +167,5 @@ def token_rows(x, features):
     return x.view(-1, features)
 
 
-__all__ = ["FEW_TOKENS", "ServedWeights", "check_formats", "experts_mx4", "quantized_rows", "rows_128", "rows_mx4",
+__all__ = ["FEW_TOKENS", "ServedWeights", "check_formats", "experts_mx4", "few_tokens_of", "quantized_rows", "rows_128", "rows_mx4",
            "rows_mx8", "token_rows"]

@@ -49,3 +49,13 @@ def test_formats_of_training(name, quantizers):
     assert _fours(layout) == 0 and layout[-2] == EIGHT[name]
     assert layout[-1] == (0 if name == "moe" else serving.FEW_TOKENS)
     assert LAYERS[name]().prepare_serving(few_tokens=7)._serving[-1] == 7
+
+
+def test_few_tokens_of_wide_layers(quantizers):
+    """Less of them by default where the GEMM, in one round, is faster than several of the few-token kernel."""
+    for columns, tokens in ((128, 128), (16384, 128), (16512, 64), (32768, 64), (32896, 32), (49152, 32), (65536, 16), (131072, 16)):
+        assert serving.few_tokens_of(columns) == tokens
+        for cls in (bs.Float8BlockwiseLinear, bs.Float8MXLinear):
+            m = cls(128, columns)
+            assert m.prepare_serving()._serving[-1] == tokens and m.prepare_serving("mxfp4")._serving[-1] == tokens
+            assert m.prepare_serving(few_tokens=100)._serving[-1] == 100
