@@ -18,11 +18,11 @@
 //
 // Tokens stay in bf16: quantizing them would save nothing where the weights
 // are the traffic.  Sums are in fp32; h alone is rounded on the way, to bf16,
-// which is what the matrix instructions take.  That is half of the result's
-// error: 0.0021 to 0.0024 of its norm against float64 in the measured cases,
+// which is what the matrix instructions take.  With it the result's error is
+// 0.0017 to 0.0023 of its norm against float64 in the measured cases, 0.0016 to
 // 0.0017 from the rounding of the result alone (the layers' FP8 GEMMs round h to
-// 3 bits of mantissa).  A second bf16 part of h would remove it, but double h in
-// the workspace and on its way through LDS, which bounds beside many tokens.
+// 3 bits of mantissa).  A second bf16 part of h would remove that, but double h
+// in the workspace and on its way through LDS, which bounds beside many tokens.
 //
 // Measured on MI355X: a call of few bytes takes 3.6 us (product) and 5 + 5.5
 // (experts), and the weights come on top at up to 6.1 TB/s (24 tokens over 64
@@ -367,9 +367,9 @@ __device__ __forceinline__ int xcd_tile(int b, int padded) { return (b & 7) * (p
 
 // Workgroup: 16 NT columns of up to RX rows; its waves take turns along the
 // contraction, so that 4096 columns are enough for every CU.  One row: 4096 x
-// 4096 e4m3 6.0 us, 8192 x 5120 e2m1 7.2; 16 rows: 8192 x 5120 e4m3 10.1 (4.2
+// 4096 e4m3 6.1 us, 8192 x 5120 e2m1 7.3; 16 rows: 8192 x 5120 e4m3 10.6 (4.0
 // TB/s).  Beside many rows the rows bound it, 64 of them 655 kB a workgroup
-// through its CU's 64 bytes a clock: 8192 x 5120 e2m1 13.7 us, 5.5 of them that.
+// through its CU's 64 bytes a clock: 8192 x 5120 e2m1 14.2 us, 5.5 of them that.
 template <int KIND, int HB, int NT, int RX, int W, int RING>
 __global__ __launch_bounds__(64 * W) void few_mm_kernel(FewMmArgs a) {
     constexpr int TT = RX > 16 ? RX / 16 : 1;
@@ -613,8 +613,8 @@ __device__ __forceinline__ void store_h(const MoeFewArgs& a, int64_t row, int64_
 }
 
 // Workgroup: 16 columns of h of a work item; its waves take turns along the
-// contraction.  One token: 4 experts of 64 tiles, 2048 e4m3 rows 7.9 us (17 MB);
-// 2 of 256 tiles, 5120 e2m1 rows 11.9 (45 MB): five microseconds and the bytes.
+// contraction.  One token: 4 experts of 64 tiles, 2048 e4m3 rows 8.1 us (17 MB);
+// 2 of 256 tiles, 5120 e2m1 rows 12.2 (45 MB): five microseconds and the bytes.
 template <int KIND, int RXMAX, int W, int RING>
 __global__ __launch_bounds__(64 * W) void moe_few_up_kernel(MoeFewArgs a) {
     constexpr int PER = item_tokens(RXMAX);
@@ -662,7 +662,7 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_kernel(MoeFewArgs a) {
 // The same where there are many tiles: every wave streams whole tiles (16 NH
 // columns), one after the other, without a barrier; an XCD's waves walk
 // neighbouring tiles.  24 tokens over 64 experts of 128 tiles, 4096 e4m3 rows:
-// 176 us, 5.9 TB/s; 64 tokens, e2m1: 119 us, 4.8 TB/s (2 tiles a wave; 153 with
+// 175 us, 5.9 TB/s; 64 tokens, e2m1: 120 us, 4.8 TB/s (2 tiles a wave; 153 with
 // one, which fetches the tokens twice as often).
 template <int KIND, int RXMAX, int NH, int W, int RING>
 __global__ __launch_bounds__(64 * W) void moe_few_up_tiles_kernel(MoeFewArgs a) {
@@ -740,8 +740,8 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_tiles_kernel(MoeFewArgs a) 
 // the order of the waves.  Where few columns leave CUs idle, several
 // workgroups share the units, and each leaves its sums in the workspace (the
 // last one adding them up behind a fence took 10 to 30 us more than a kernel).
-// 24 tokens over 64 experts of 2048, 4096 e4m3 columns: 80 us, 6.4 TB/s; 64
-// tokens, e2m1, 2 tiles a wave and 2 shares: 63 + 4.7 us, 4.2 TB/s (95 with one
+// 24 tokens over 64 experts of 2048, 4096 e4m3 columns: 79 us, 6.5 TB/s; 64
+// tokens, e2m1, 2 tiles a wave and 2 shares: 62 + 4.7 us, 4.3 TB/s (95 with one
 // tile and none).
 template <int KIND, int RXMAX, int NT, int W, int RING>
 __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
