@@ -6,6 +6,9 @@ inserts them for instructions of its own, but does not look into inline asm:
 * one between a scalar write of m0 and the load;
 * five between a vector instruction's write of a scalar register and a vector
   memory instruction that reads it.
+
+gfx950 leaves two more between such a write and a vector instruction that reads
+the register as a mask, as the carry of an addition that inline asm writes.
 """
 
 import os
@@ -18,7 +21,7 @@ import pytest
 from blockwise_scaled_fp8_bs_amd import _lib
 
 OBJDUMP = os.environ.get("LLVM_OBJDUMP", "/opt/rocm/llvm/bin/llvm-objdump")
-SGPR_TO_VMEM, M0_TO_LDS = 5, 1
+SGPR_TO_VMEM, M0_TO_LDS, SGPR_TO_MASK = 5, 1, 2
 
 _RANGE, _ONE = re.compile(r"\bs\[(\d+):(\d+)\]"), re.compile(r"\bs(\d+)\b")
 
@@ -39,7 +42,8 @@ def vector_writes(op, operands):
 
 
 def hazards(lines):
-    """Copies into LDS in a listing, and those among them that come too early (in the listing's order)."""
+    """Copies into LDS in a listing, and those among them, and additions with a carry, that come too early (in the
+    listing's order)."""
     loads, early = 0, []
     recent = []  # of the last instructions: states since, scalar registers written by a vector one, m0 written
     for line in lines:
@@ -53,6 +57,8 @@ def hazards(lines):
             used = scalars(rest)
             if any((age < SGPR_TO_VMEM and used & written) or (age < M0_TO_LDS and m0) for age, written, m0 in recent):
                 early.append(line)
+        if op == "v_addc_co_u32_e64" and any(age < SGPR_TO_MASK and scalars(operands[4]) & written for age, written, _ in recent):
+            early.append(line)
         states = int(rest, 0) + 1 if op == "s_nop" else 1
         recent = [(age + states, written, m0) for age, written, m0 in recent if age + states < SGPR_TO_VMEM]
         recent.append((0, vector_writes(op, operands), op.startswith("s_") and operands[0] == "m0"))
@@ -68,6 +74,9 @@ def test_what_is_looked_for():
                   "v_add_co_u32_e64 v3, s[6:7], v1, v2"):
         assert hazards([write, "s_mov_b32 m0, s2", "s_nop 2", load]) == (1, [load])
         assert hazards([write, "s_mov_b32 m0, s2", nop, load]) == (1, [])
+    add = "v_addc_co_u32_e64 v1, s[0:1], v1, v1, s[2:3]"
+    assert hazards(["v_cmp_lt_i32_e64 s[2:3], v0, v1", "s_nop 0", add]) == (0, [add])
+    assert hazards(["v_cmp_lt_i32_e64 s[2:3], v0, v1", "s_nop 1", add]) == (0, [])
     assert hazards(["v_readfirstlane_b32 s2, v0", "s_mov_b32 m0, s2", "s_nop 0", load, "v_mov_b32_e32 v1, s9"]) == (1, [])
 
 
