@@ -625,19 +625,15 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& p) {
                 dma4(o.sb, lds_addr(&sm.sb[s].f[0]), voff_s, (int)((int64_t)kb * p.ld_sb * 4));
         }
     };
-    // Copy c = 0..7 of this wave's share: A for even c, B for odd c, rows
-    // [(8i + w) * 8, +8) of round i = c / 2.
-    auto issue_copy = [&](const Operands& o, int32_t kb, int s, int c) {
+    // Round i = 0..3 of this wave's copies: rows [(8i + w) * 8, +8) of A and B.
+    auto issue_copy = [&](const Operands& o, int32_t kb, int s, int i) {
         const int k_off = kb * BK;
-        const int i = c >> 1;
-        if ((c & 1) == 0)
-            dma16(o.a, lds_addr(&sm.a[s][(8 * i + w) * 1024]), voff_a, k_off + (int)(64 * i * p.lda));
-        else
-            dma16(o.b, lds_addr(&sm.b[s][(8 * i + w) * 1024]), voff_b, k_off + (int)(64 * i * p.ldb));
+        dma16_pair(o.a, lds_addr(&sm.a[s][(8 * i + w) * 1024]), voff_a, (int)(64 * i * p.lda),
+                   o.b, lds_addr(&sm.b[s][(8 * i + w) * 1024]), voff_b, (int)(64 * i * p.ldb), k_off);
     };
     auto issue_loads = [&](const Operands& o, int32_t kb, int s) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) issue_copy(o, kb, s, c);
+        for (int i = 0; i < 4; ++i) issue_copy(o, kb, s, i);
         issue_scales(o, kb, s, 0);
     };
     // The same copies issued by the four waves of group g alone (rows
@@ -658,8 +654,8 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& p) {
         const int k_off = kb * BK;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            dma16(o.a, lds_addr(&sm.a[s][(4 * i + wq) * 1024]), voff_a4, k_off + (int)(32 * i * p.lda));
-            dma16(o.b, lds_addr(&sm.b[s][(4 * i + wq) * 1024]), voff_b4, k_off + (int)(32 * i * p.ldb));
+            dma16_pair(o.a, lds_addr(&sm.a[s][(4 * i + wq) * 1024]), voff_a4, (int)(32 * i * p.lda),
+                       o.b, lds_addr(&sm.b[s][(4 * i + wq) * 1024]), voff_b4, (int)(32 * i * p.ldb), k_off);
         }
         issue_scales(o, kb, s, 4 * g);
     };
@@ -670,16 +666,18 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& p) {
         const int k_off = kb * BK;
 #pragma unroll
         for (int i = 4 * h; i < 4 * h + 4; ++i) {
-            dma16(o.a, lds_addr(&sm.a[s][(4 * i + wq) * 1024]), voff_a4, k_off + (int)(32 * i * p.lda));
-            dma16(o.b, lds_addr(&sm.b[s][(4 * i + wq) * 1024]), voff_b4, k_off + (int)(32 * i * p.ldb));
+            dma16_pair(o.a, lds_addr(&sm.a[s][(4 * i + wq) * 1024]), voff_a4, (int)(32 * i * p.lda),
+                       o.b, lds_addr(&sm.b[s][(4 * i + wq) * 1024]), voff_b4, (int)(32 * i * p.ldb), k_off);
         }
         if (h == 0) issue_scales(o, kb, s, 4 * g);
     };
     // GROUP_M (MoE forward and dgrad, 128x128 B scales) has all eight waves
     // share the next K block's copies instead: wave w issues its issue_copy
-    // pieces, one after each of its third to tenth MFMAs (waves 0 and 1 the
-    // scales with the first piece), so every copy is still issued in the
-    // first third of the block.  Both waves of a SIMD then carry the same
+    // rounds, a pair of copies after each of its third, fifth, seventh and ninth
+    // MFMAs (waves 0 and 1 the scales with the first), so every copy is still
+    // issued in the first third of the block (single copies after the third to
+    // tenth wait for their operands twice as often: MoE forward and dgrad about
+    // 1 % slower).  Both waves of a SIMD then carry the same
     // load and reach the block-end barrier together: with one group issuing,
     // the other group spent 16-24 % of its time waiting there.  The shared
     // spread is 3-5 % faster than one group spreading its copies over its
@@ -831,9 +829,9 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& p) {
                         const int q = i * TN + j;
                         pbuf[q & 1] =
                             __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af, zero, 0, 0, 0, 0, 0, 0);
-                        if (kSpread && q >= kSpreadAt && q < kSpreadAt + 8 && spread) {
+                        if (kSpread && q >= kSpreadAt && q < kSpreadAt + 8 && (q - kSpreadAt) % 2 == 0 && spread) {
                             if (q == kSpreadAt) issue_scales(ops, cur.kb0 + it + 1, s ^ 1, 0);
-                            issue_copy(ops, cur.kb0 + it + 1, s ^ 1, q - kSpreadAt);
+                            issue_copy(ops, cur.kb0 + it + 1, s ^ 1, (q - kSpreadAt) / 2);
                         }
                         if (q > 0) fold(pbuf[(q - 1) & 1], pi, pj);
                         if (kLateIssue && (q == 2 || q == 4) && it + 1 < nkb)
