@@ -62,6 +62,7 @@ SIGNATURES = {
     "bs_moe_few": (_E, [_E, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64,
                         _P, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
     "bs_moe_few_workspace_bytes": (_I64, [_I64, _I64, _I64, _I64, _I64]),
+    "bs_moe_few_full_workspace_bytes": (_I64, [_I64, _I64, _I64, _I64, _I64]),
     "bs_status_string": (ctypes.c_char_p, [_E]),
     "bs_last_error": (ctypes.c_char_p, []),
     "bs_diag_e4m3_census": (_E, [_P, _P, _P, _P]),

@@ -209,7 +209,7 @@ def bs_moe_few(x, idx, w, w12, s12, out_proj, s_out, kind, residual=None, out=No
         p_out, ld_out = out.data_ptr() or None, D
     else:
         p_out, ld_out = _rows_of(out, "out", bf16, T, D, index)
-    nbytes = _lib.load().bs_moe_few_workspace_bytes(T, D, H, E, k)
+    nbytes = _lib.load().bs_moe_few_full_workspace_bytes(T, D, H, E, k)
     workspace = _empty(x, stream, (nbytes // 2,), bf16)
     _call("bs_moe_few", index, kind, T, D, H, E, k, p_x, ld_x, p_idx, p_w, *up, *down, p_res, ld_res, p_out, ld_out,
           workspace.data_ptr() or None, nbytes, _stream_of(x, stream))

@@ -10,6 +10,7 @@ namespace bs {
 
 constexpr int64_t kFewChunk = 64;               // tokens that a workgroup takes at a time
 constexpr int kCus = 256;
+constexpr int64_t kTwoParts = 8;                // tokens up to which bs_moe_few can keep h in two parts
 constexpr int kMaxSplits = 16;                  // workgroups that share columns of bs_moe_few's output
 constexpr int64_t kMaxFewDim = (int64_t)1 << 18;  // widths of bs_moe_few: a chunk's slots times them in 32-bit offsets
 
@@ -63,7 +64,8 @@ struct MoeFewArgs {
     uint16_t* out;
     int64_t ld_out;
     bool vec;
-    uint16_t* h;    // workspace [T * k, H] bf16
+    uint16_t* h;    // workspace [T * k, parts, H] bf16
+    int32_t parts;  // that h is kept in
     // set by the launcher
     int64_t tiles;
     int32_t items;      // work items of a chunk at most

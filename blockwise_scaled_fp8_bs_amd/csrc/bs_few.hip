@@ -588,11 +588,12 @@ __device__ __forceinline__ int item_rows(const Routing& rt, int it, int& first, 
 constexpr int item_tokens(int rxmax) { return rxmax > 16 ? rxmax : 16; }
 
 // Calls run with the tokens' places and the unit's bytes for items of `most`
-// tokens, RXMAX at most.
+// places, RXMAX at most.
 template <int KIND, int RXMAX, int NT, int RING, class Run>
 __device__ __forceinline__ void with_places(int most, Run run) {
     if (RXMAX == 1 || most <= 1) return run(Int<1>{}, UnitBytes<KIND, NT, 1, RING>{});
-    if constexpr (RXMAX > 1) {
+    if constexpr (RXMAX == 2) return run(Int<2>{}, UnitBytes<KIND, NT, 2, RING>{});
+    if constexpr (RXMAX > 2) {
         if (RXMAX == 4 || most <= 4) return run(Int<4>{}, UnitBytes<KIND, NT, 4, RING>{});
     }
     if constexpr (RXMAX > 4) {
@@ -604,12 +605,19 @@ __device__ __forceinline__ void with_places(int most, Run run) {
     if constexpr (RXMAX > 16) run(Int<32>{}, UnitBytes<KIND, NT, 32, RING>{});
 }
 
-// h of one lane's four columns: weight silu(a) b, rounded once.
+// h of one lane's four columns, weight silu(a) b: rounded to bf16, and with two
+// parts what that left out (nothing of an infinity or a NaN) in a row of its own.
 __device__ __forceinline__ void store_h(const MoeFewArgs& a, int64_t row, int64_t col, float weight, f32x4 ga, f32x4 up) {
-    uint32_t o[4];
+    uint32_t o[4], rest[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = bf16_bits(weight * (ga[j] / (1.f + __expf(-ga[j])) * up[j]));
-    *reinterpret_cast<uint2*>(a.h + row * a.H + col) = make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
+    for (int j = 0; j < 4; ++j) {
+        const float v = weight * (ga[j] / (1.f + __expf(-ga[j])) * up[j]);
+        o[j] = bf16_bits(v);
+        rest[j] = (o[j] & 0x7f80u) == 0x7f80u ? 0u : bf16_bits(v - bf16_lo(o[j]));
+    }
+    uint16_t* const h = a.h + row * a.parts * a.H + col;
+    *reinterpret_cast<uint2*>(h) = make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
+    if (a.parts > 1) *reinterpret_cast<uint2*>(h + a.H) = make_uint2(rest[0] | rest[1] << 16, rest[2] | rest[3] << 16);
 }
 
 // Workgroup: 16 columns of h of a work item; its waves take turns along the
@@ -745,7 +753,8 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_tiles_kernel(MoeFewArgs a) 
 // tile and none).
 template <int KIND, int RXMAX, int NT, int W, int RING>
 __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
-    constexpr int PER = item_tokens(RXMAX), Q = 4 * NT;  // f32x4 of a token
+    constexpr int PER = item_tokens(RXMAX), Q = 4 * NT;     // f32x4 of a token
+    constexpr int PLACES = RXMAX <= 8 ? 2 * RXMAX : RXMAX;  // for both parts of h, if there are two
     extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];
     __shared__ __attribute__((aligned(16))) uint8_t s_ring[W * RING];
     __shared__ OneToken s_one[RXMAX == 1 ? W : 1];
@@ -762,7 +771,8 @@ __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
 
     const int r = lane & 15, g = lane >> 4, H = (int)a.H;
     const int64_t d0 = 16 * NT * (int64_t)tile;
-    with_places<KIND, RXMAX, NT, RING>(rt.most, [&](auto rx, auto hb) {
+    const bool two = RXMAX <= 8 && a.parts > 1;
+    with_places<KIND, PLACES, NT, RING>(rt.most << two, [&](auto rx, auto hb) {
         constexpr int RX = decltype(rx)::value, HB = decltype(hb)::value, TT = RX > 16 ? RX / 16 : 1;
         const int units = (H + Unit<KIND, HB>::kCodes - 1) / Unit<KIND, HB>::kCodes;
         const int all = rt.items * units, shares = W * a.splits, share = (all + shares - 1) / shares;
@@ -781,7 +791,7 @@ __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
             const int e = item_rows<PER>(rt, there ? l_item : 0, first, n);
 #pragma unroll
             for (int i = 0; i < NT; ++i) rows[i] = tile_rows<KIND>(a.wo, e, d0 + 16 * i, a.D, H, there);
-            h = make_rsrc(a.h + (t0 * a.k + first) * a.H, there ? (int64_t)n * H * 2 : 0);
+            h = make_rsrc(a.h + ((t0 * a.k + first) << two) * a.H, there ? ((int64_t)n << two) * H * 2 : 0);
         };
         select();
         f32x4 acc[NT][TT];
@@ -790,15 +800,25 @@ __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
             int first, n;
             item_rows<PER>(rt, m_item, first, n);
 #pragma unroll
-            for (int t = 0; t < TT; ++t)
-                if (16 * t + r < n) {
-                    f32x4* const s = own + rt.token[first + 16 * t + r] * Q + g;
+            for (int t = 0; t < TT; ++t) {
+                if (two) {  // a token's parts are neighbours
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            acc[i][t][j] += __uint_as_float(
+                                __builtin_amdgcn_mov_dpp((int)__float_as_uint(acc[i][t][j]), 0xB1, 0xF, 0xF, false));  // quad_perm 1,0,3,2
+                }
+                const int c = (16 * t + r) >> two;
+                if (c < n && !(two && (r & 1))) {
+                    f32x4* const s = own + rt.token[first + c] * Q + g;
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
                         const f32x4 v = s[4 * i], p = acc[i][t];
                         s[4 * i] = f32x4{v[0] + p[0], v[1] + p[1], v[2] + p[2], v[3] + p[3]};
                     }
                 }
+            }
             zero(acc);
         };
         stream_units<KIND, HB, NT, RX, RING>(
@@ -901,7 +921,7 @@ hipError_t moe(MoeFewArgs a, hipStream_t stream, MoeFewPlan* plan) {
     a.items = (slots < a.E ? slots : a.E) + (tokens > PER ? slots / PER : 0);
     const int table = RXMAX == 1 ? 0 : RoutingLayout(a.E, slots, a.items).bytes;
     a.splits = down_splits(a.T, a.D, a.H, a.E, a.k, NT, WD);
-    a.part = reinterpret_cast<f32x4*>(a.h + a.T * a.k * a.H);
+    a.part = reinterpret_cast<f32x4*>(a.h + a.parts * a.T * a.k * a.H);
     // The waves of a workgroup share a tile (four microseconds of its own a workgroup, half a microsecond a unit and
     // wave), or each streams whole tiles: one token over 2 experts of 256 tiles and 5120 rows in 4 bits takes 12 us
     // shared, 64 tokens of a single e4m3 expert of 512 tiles and 5120 rows 52 shared and 37 by tiles, 32 tokens over 16
@@ -942,7 +962,7 @@ hipError_t moe_kind(const MoeFewArgs& a, hipStream_t stream, MoeFewPlan* plan) {
     // Up to 8 tokens, workgroups of 80 KiB, two on a CU.
     if (a.T <= 1) return moe<KIND, 1, 19200, 1, 19200, 1, 8, 9728>(a, stream, plan);
     if (a.T <= 4) return moe<KIND, 4, 19200, 1, 19200, 1, 8, 9728>(a, stream, plan);
-    if (a.T <= 8) return moe<KIND, 8, 19200, 1, 19200, 1, 8, 9472>(a, stream, plan);
+    if (a.T <= 8) return moe<KIND, 8, 19200, 1, 19200, 1, 4, 19200>(a, stream, plan);
     // Beside more tokens of an expert a wave takes two tiles at a time, which halves what it fetches of tokens, in rings
     // of a whole CU (64 tokens over 64 e2m1 experts of 2048, width 4096: 119 + 63 us, 153 + 95 with one).  In the second
     // kernel where one tile would need a second round of the CUs, or where workgroups that share the tiles fill them:

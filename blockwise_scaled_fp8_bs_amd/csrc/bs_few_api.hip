@@ -142,6 +142,11 @@ int64_t bs_moe_few_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, i
     return T == 0 || D == 0 ? 0 : T * k * H * 2 + bs::moe_few_shares_bytes(T, D, H, E, k);
 }
 
+int64_t bs_moe_few_full_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k) {
+    const int64_t n = bs_moe_few_workspace_bytes(T, D, H, E, k);
+    return n > 0 && T <= bs::kTwoParts ? n + T * k * H * 2 : n;
+}
+
 bs_status bs_moe_few(bs_weight_kind kind, int64_t T, int64_t D, int64_t H, int64_t E, int64_t k, const uint16_t* x,
                      int64_t ld_x, const int32_t* idx, const float* w, const uint8_t* w12, int64_t stride_w12,
                      int64_t ld_w12, const void* s12, int64_t stride_s12, int64_t ld_s12, const uint8_t* out_proj,
@@ -181,6 +186,7 @@ bs_status bs_moe_few(bs_weight_kind kind, int64_t T, int64_t D, int64_t H, int64
     a.residual = residual; a.ld_res = ld_res; a.out = out; a.ld_out = ld_out;
     a.vec = ld_out % 4 == 0 && aligned_to(out, 8) && (!residual || (ld_res % 4 == 0 && aligned_to(residual, 8)));
     a.h = static_cast<uint16_t*>(workspace);
+    a.parts = T <= bs::kTwoParts && workspace_bytes >= bs_moe_few_full_workspace_bytes(T, D, H, E, k) ? 2 : 1;
     return hip_status(bs::launch_moe_few(a, few_kind(kind), stream), fn);
 }
 

@@ -94,13 +94,16 @@ def few_mm(x, w, residual=None, bf16=True):
     return ref, (bound + HALF_BF16 * (np.abs(ref) + bound) if bf16 else bound)
 
 
-def moe(x, idx, w, w12, wo, residual=None):
+def moe(x, idx, w, w12, wo, residual=None, parts=1):
     """(out, bound) of residual + sum_j w_j wo_e (silu(a) b), [a | b] = w12_e x:
     x [T, D], idx and w [T, k], w12 [E][2H, D], wo [E][D, H], all float64.
 
     With da, db the bounds of a and b: |silu'| <= 1.1, so silu(a) b is off by at
     most |silu(a)| db + 1.1 da (|b| + db), times the weight, and 2^-20 of itself
-    for the arithmetic of the formula; h is rounded once to bf16.
+    for the arithmetic of the formula; h is rounded once to bf16, or kept in two
+    parts: what the first rounding left out, at most 2^-8 of h, is rounded to bf16
+    in turn (off by at most 2^-8 of that, or half a step of bf16's smallest
+    numbers, 2^-134), and the sums have twice the terms.
     """
     T, D = x.shape
     out = np.zeros((T, D)) if residual is None else np.array(residual, np.float64)
@@ -117,10 +120,10 @@ def moe(x, idx, w, w12, wo, residual=None):
                 g = a / (1 + np.exp(-a))
             h = weight * g * b
             dh = abs(weight) * (np.abs(g) * db + 1.1 * da * (np.abs(b) + db)) + 2.0 ** -20 * np.abs(h)
-            dh = dh + HALF_BF16 * (np.abs(h) + dh)
+            dh = dh + HALF_BF16 ** parts * (np.abs(h) + dh) + (2.0 ** -134 if parts > 1 else 0.0)
             out[t] += wo[e] @ h
             mag[t] += np.abs(wo[e]) @ (np.abs(h) + dh)
             err[t] += np.abs(wo[e]) @ dh
-            terms += H
+            terms += parts * H
     err = err + (terms + 64) * STEP_F32 * mag
     return out, err + HALF_BF16 * (np.abs(out) + err)
