@@ -179,7 +179,8 @@ def bs_moe_few(x, idx, w, w12, s12, out_proj, s_out, kind, residual=None, out=No
     idx [T, k] int32 (outside [0, E): not routed) and w [T, k] float32 (None:
     ones), as bs_moe_route gives them; with idx None every token takes the only
     expert.  w12 [E, 2H, D] and out_proj [E, D, H] with scales s12 and s_out of
-    the given kind; residual [T, D] bf16; out bf16.
+    the given kind; residual [T, D] bf16; out bf16.  Up to 8 tokens the
+    activations between the two products are kept in two bf16 parts.
     """
     bf16 = torch.bfloat16
     T, D = _first(x, "x", bf16)

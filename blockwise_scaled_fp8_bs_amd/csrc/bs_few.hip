@@ -18,11 +18,15 @@
 //
 // Tokens stay in bf16: quantizing them would save nothing where the weights
 // are the traffic.  Sums are in fp32; h alone is rounded on the way, to bf16,
-// which is what the matrix instructions take.  With it the result's error is
-// 0.0017 to 0.0023 of its norm against float64 in the measured cases, 0.0016 to
-// 0.0017 from the rounding of the result alone (the layers' FP8 GEMMs round h to
-// 3 bits of mantissa).  A second bf16 part of h would remove that, but double h
-// in the workspace and on its way through LDS, which bounds beside many tokens.
+// which is what the matrix instructions take.  Up to 8 tokens it is kept in two
+// bf16 parts, h and what its rounding left out, side by side in the instructions'
+// 16 columns: the result's error against float64 is then that of its own
+// rounding, 0.0016 to 0.0017 of the norm, up to 0.0024 with one part (1 to 4
+// tokens take the same time, 5 to 8 0 to 7 % more: a gated FFN of 5120 and 8192
+// in MXFP8 44 us, 41 with one).  Beside more tokens the parts would take columns
+// of their own, and twice the way through LDS that bounds there: one part (16
+// tokens through an FFN of 2048 and 4096 in e4m3 17 us, 20 with two; 24 over 16
+// experts of 1024 37 and 44; 64 over 64 e2m1 experts of 2048 181 and 219).
 //
 // Measured on MI355X: a call of few bytes takes 3.6 us (product) and 5 + 5.5
 // (experts), and the weights come on top at up to 6.1 TB/s (24 tokens over 64
@@ -413,8 +417,8 @@ __global__ __launch_bounds__(64 * W) void few_mm_kernel(FewMmArgs a) {
 // gated experts: h of the routed slots, then their weighted sum
 // ---------------------------------------------------------------------------
 //
-// h has a row for every token of every expert that it chose (one that it names
-// twice counts once), in the order of the experts and, within one, of the
+// h has a row (or one for each part) for every token of every expert that it
+// chose (one that it names twice counts once), in the order of the experts and, within one, of the
 // tokens.  A work item is 16 of an expert's tokens at most, 32 where most
 // experts have more than that.
 
@@ -621,8 +625,8 @@ __device__ __forceinline__ void store_h(const MoeFewArgs& a, int64_t row, int64_
 }
 
 // Workgroup: 16 columns of h of a work item; its waves take turns along the
-// contraction.  One token: 4 experts of 64 tiles, 2048 e4m3 rows 8.1 us (17 MB);
-// 2 of 256 tiles, 5120 e2m1 rows 12.2 (45 MB): five microseconds and the bytes.
+// contraction.  One token: 4 experts of 64 tiles, 2048 e4m3 rows 8.3 us (17 MB);
+// 2 of 256 tiles, 5120 e2m1 rows 12.6 (45 MB): five microseconds and the bytes.
 template <int KIND, int RXMAX, int W, int RING>
 __global__ __launch_bounds__(64 * W) void moe_few_up_kernel(MoeFewArgs a) {
     constexpr int PER = item_tokens(RXMAX);
@@ -754,7 +758,7 @@ __global__ __launch_bounds__(64 * W) void moe_few_up_tiles_kernel(MoeFewArgs a) 
 template <int KIND, int RXMAX, int NT, int W, int RING>
 __global__ __launch_bounds__(64 * W) void moe_few_down_kernel(MoeFewArgs a) {
     constexpr int PER = item_tokens(RXMAX), Q = 4 * NT;     // f32x4 of a token
-    constexpr int PLACES = RXMAX <= 8 ? 2 * RXMAX : RXMAX;  // for both parts of h, if there are two
+    constexpr int PLACES = RXMAX <= 8 ? 2 * RXMAX : RXMAX;  // both parts of h, where there are two
     extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];
     __shared__ __attribute__((aligned(16))) uint8_t s_ring[W * RING];
     __shared__ OneToken s_one[RXMAX == 1 ? W : 1];
@@ -959,7 +963,8 @@ hipError_t moe(MoeFewArgs a, hipStream_t stream, MoeFewPlan* plan) {
 
 template <int KIND>
 hipError_t moe_kind(const MoeFewArgs& a, hipStream_t stream, MoeFewPlan* plan) {
-    // Up to 8 tokens, workgroups of 80 KiB, two on a CU.
+    // Up to 8 tokens, workgroups of 80 KiB, two on a CU (from 5 on with longer rings for fewer waves in the second kernel:
+    // 5 tokens through an FFN of 5120 and 8192 in e4m3 39 us, 43 with eight waves).
     if (a.T <= 1) return moe<KIND, 1, 19200, 1, 19200, 1, 8, 9728>(a, stream, plan);
     if (a.T <= 4) return moe<KIND, 4, 19200, 1, 19200, 1, 8, 9728>(a, stream, plan);
     if (a.T <= 8) return moe<KIND, 8, 19200, 1, 19200, 1, 4, 19200>(a, stream, plan);

@@ -758,8 +758,10 @@ bs_status bs_few_mm(bs_weight_kind kind, int64_t T, int64_t N, int64_t K, const 
  * in two kernels (three where D is small beside the experts' contractions):
  *   out[t] = residual[t] + sum_j w[t, j] Wo_e (silu(a) b),  e = idx[t, j],
  *   [a | b] = W12_e x[t] (a from W12's rows [0, H), b from [H, 2H))
- * h = w silu(a) b is rounded once to bf16 (from fp32 a and b: what the matrix
- * instructions take), everything else is in fp32 and rounded once at the end.
+ * h = w silu(a) b is rounded to bf16 (from fp32 a and b: what the matrix
+ * instructions take), or up to 8 tokens, in a workspace with room for it, kept
+ * in two bf16 parts (16 bits of mantissa); everything else is in fp32 and
+ * rounded once at the end.
  * Only experts that some token chose are read, for 16 to 32 of an expert's
  * tokens at a time.  A token's result does not depend on the other tokens, but
  * for the order of its sums.
@@ -775,9 +777,10 @@ bs_status bs_few_mm(bs_weight_kind kind, int64_t T, int64_t N, int64_t K, const 
  *   out_proj  [E][D, H], stride_wo, ld_wo; s_out, stride_so, ld_so
  *   residual  [T, D] bf16 or NULL (zeros); may be out itself
  *   out       [T, D] bf16, ld_out >= D
- *   workspace bs_moe_few_workspace_bytes(T, D, H, E, k) bytes of DEVICE memory,
- *             16-byte aligned, without initial contents; calls that share one must not
- *             overlap in time
+ *   workspace bs_moe_few_workspace_bytes(T, D, H, E, k) bytes of DEVICE memory
+ *             at least, 16-byte aligned, without initial contents; with
+ *             bs_moe_few_full_workspace_bytes of them or more, h has two parts
+ *             wherever it can. Calls that share one must not overlap in time
  *   D and H multiples of 128 (E4M3_128X128) or 32 (MX), at most 262144;
  *   1 <= E <= 1024, 1 <= k <= min(E, 32), 0 <= T <= 2^21.
  */
@@ -792,6 +795,9 @@ bs_status bs_moe_few(bs_weight_kind kind, int64_t T, int64_t D, int64_t H, int64
  * the experts' H, sums of workgroups that share columns (joined by a third
  * kernel).  Invalid arguments give 0. */
 int64_t bs_moe_few_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k);
+
+/* The same with room for both parts of h: T k H 2 bytes more up to 8 tokens. */
+int64_t bs_moe_few_full_workspace_bytes(int64_t T, int64_t D, int64_t H, int64_t E, int64_t k);
 
 /* Human-readable name of a status code (static storage). */
 const char* bs_status_string(bs_status status);

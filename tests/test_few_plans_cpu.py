@@ -67,3 +67,12 @@ def test_products_take_one_round_of_the_cus_where_they_can(kind):
         assert plan["tiles"] == 1 and plan["workgroups"] * chunks <= 256
         plan = bs.bs_diag_few_mm_plan(kind, T, two, 1024)
         assert plan["tiles"] == 2 and (plan["workgroups"] * chunks <= 256 or two > 8192 // chunks)
+
+
+def test_workspace_of_both_parts():
+    """Room for a second part of the activations up to 8 tokens; the least is what it was."""
+    lib = _lib.load()
+    for T, D, H, E, k in ((1, 96, 64, 4, 2), (3, 96, 64, 4, 2), (8, 128, 8192, 16, 8)):
+        assert lib.bs_moe_few_full_workspace_bytes(T, D, H, E, k) == lib.bs_moe_few_workspace_bytes(T, D, H, E, k) + T * k * H * 2
+    for T, D, H, E, k in ((9, 96, 64, 4, 2), (64, 128, 8192, 16, 8), (0, 96, 64, 4, 2), (3, 96, 64, 4, 33), (-1, 96, 64, 4, 2)):
+        assert lib.bs_moe_few_full_workspace_bytes(T, D, H, E, k) == lib.bs_moe_few_workspace_bytes(T, D, H, E, k)
